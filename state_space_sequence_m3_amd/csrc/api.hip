@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "m3_check.h"
 #include "m3_device.h"
 #include "m3_launch.h"
 #include "m3scan.h"
@@ -15,6 +16,14 @@ namespace {
 
 thread_local char g_err[512] = "";
 
+// 0 = not checked yet, 1 = gfx950, 2 = something else
+std::atomic<int> g_dev_ok[256];
+std::atomic<int> g_cus[256];
+
+}  // namespace
+
+namespace m3 {
+
 m3_status fail(m3_status s, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -22,9 +31,6 @@ m3_status fail(m3_status s, const char* fmt, ...) {
     va_end(ap);
     return s;
 }
-
-// 0 = not checked yet, 1 = gfx950, 2 = something else
-std::atomic<int> g_dev_ok[256];
 
 m3_status check_device() {
     int dev = -1;
@@ -44,16 +50,33 @@ m3_status check_device() {
     return M3_OK;
 }
 
-size_t io_size(const m3_dims* d) { return d->io == M3_BF16 ? 2 : 4; }
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-// [p, p + n) and [q, q + m) overlap (both non-empty)
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-    if (!p || !q || n == 0 || m == 0) return false;
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    return a < b + m && b < a + n;
+int device_cus() {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 256) return 256;
+    int n = g_cus[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+    g_cus[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
+
+m3_status launched(hipError_t e, const char* what) {
+    if (e != hipSuccess) return fail(M3_E_LAUNCH, "%s: launch failed: %s", what, hipGetErrorString(e));
+    return M3_OK;
+}
+
+}  // namespace m3
+
+namespace {
+
+using m3::aligned;
+using m3::check_device;
+using m3::device_cus;
+using m3::fail;
+using m3::launched;
+using m3::overlap;
+
+size_t io_size(const m3_dims* d) { return d->io == M3_BF16 ? 2 : 4; }
 
 struct Buf {
     const void* p;
@@ -116,11 +139,6 @@ m3_status check_align(const Buf* bufs, int n, size_t a) {
     return M3_OK;
 }
 
-m3_status launched(hipError_t e, const char* what) {
-    if (e != hipSuccess) return fail(M3_E_LAUNCH, "%s: launch failed: %s", what, hipGetErrorString(e));
-    return M3_OK;
-}
-
 // dst[i] = src ? src[i] : 0 over n 16-bit words (the sizes used here are all even in bytes)
 __global__ void copy_or_zero_kernel(uint16_t* dst, const uint16_t* src, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
@@ -138,18 +156,6 @@ hipError_t copy_or_zero(void* dst, const void* src, size_t bytes, hipStream_t s)
     const unsigned blocks = (unsigned)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096);
     hipLaunchKernelGGL(copy_or_zero_kernel, dim3(blocks), dim3(256), 0, s, (uint16_t*)dst, (const uint16_t*)src, n);
     return hipGetLastError();
-}
-
-// Compute units of the current device (256 when there is none to ask), cached per device.
-std::atomic<int> g_cus[256];
-int device_cus() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 256) return 256;
-    int n = g_cus[dev].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-    g_cus[dev].store(n, std::memory_order_relaxed);
-    return n;
 }
 
 // Sequence split of a prefill call (m3_prefill, m3_layer_prefill): when the (b, h) pairs are too

@@ -1,0 +1,119 @@
+// block_launch.h -- argument blocks and launchers of the operators of m3block.h, shared between
+// their C-ABI file (block_api.hip) and the kernels.  Shapes, pointers and workspaces are validated
+// by the C-ABI file before any launcher runs.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace m3 {
+
+// ---------------------------------------------------------------------------- gated scan
+// A tile is kScanTile tokens x kScanCols channels, one workgroup.  Dense batches of sequences
+// longer than a tile are cut sequence by sequence (`per_seq`); shorter sequences and packed batches
+// are cut along the flat token axis, so a tile can hold many sequences.
+constexpr int kScanTile = 128;
+constexpr int kScanCols = 128;
+
+struct GatedScanArgs {
+    const int32_t* cu;      // packed offsets, or nullptr: dense
+    const void* gate;
+    const void* x;
+    const float* bias;
+    const float* h_in;
+    void* y;
+    float* h_out;
+    float* states;          // [nchunks, D] state each tile starts from (forward: out, nullable)
+    // backward
+    const void* dy;
+    const float* dh_out;
+    void* dgate;
+    void* dx;
+    float* dbias;
+    float* dh_in;
+    float* part;            // [nchunks, D] each tile's share of dbias (nchunks > 1)
+    int64_t b, L, T;        // sequences; tokens of each (dense); tokens of all
+    int64_t D;
+    int64_t gate_p, x_p, y_p, dgate_p, dx_p;   // pitches in bytes
+    uint64_t* words;        // [nchunks, ncols * kScanCols] chain words (nchunks > 1)
+    unsigned* ticket;
+    int64_t nchunks;
+    int64_t seq_chunks;     // tiles per sequence (per_seq)
+    int ncols;              // column blocks
+    int per_seq;
+};
+
+hipError_t launch_gated_scan(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s);
+hipError_t launch_gated_scan_backward(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s);
+
+struct GatedStepArgs {
+    const void* gate;
+    const void* x;
+    const float* bias;
+    const float* h;
+    void* y;
+    float* h_out;
+    int64_t b, D;
+    int64_t gate_p, x_p, y_p;   // pitches in bytes
+};
+hipError_t launch_gated_step(const GatedStepArgs& a, bool bf16_io, bool vec, hipStream_t s);
+
+// ------------------------------------------------------------------------------ RMS norm
+constexpr int64_t kNormMaxWidth = 16384;
+
+struct RmsNormArgs {
+    const void* x;
+    const void* residual;
+    const float* weight;
+    void* r_out;
+    void* y;
+    uint8_t* q;
+    float* scale;
+    // backward
+    const void* r;
+    const void* dy;
+    const void* dr_out;
+    void* dx;
+    float* dweight;
+    float* part;               // [blocks, D]
+    int64_t rows;
+    int D;
+    int64_t x_p, res_p, r_p, y_p, dx_p;   // pitches in bytes
+    int group;                 // 0: the row
+    int ngroups;
+    float eps;
+};
+hipError_t launch_rmsnorm(const RmsNormArgs& a, bool bf16_io, hipStream_t s);
+hipError_t launch_rmsnorm_backward(const RmsNormArgs& a, bool bf16_io, hipStream_t s);
+int64_t rmsnorm_backward_parts(int64_t rows, int64_t D);   // rows of dweight partial sums
+
+// ----------------------------------------------------------------- column sums, gradient norm
+// out[d] = sum over i < n of part[i * D + d], in a fixed order
+hipError_t launch_column_sum(const float* part, int64_t n, int64_t D, float* out, hipStream_t s);
+
+constexpr int kGradBatch = 96;           // tensors per launch (their table is a kernel argument)
+constexpr int64_t kGradChunk = 16384;    // elements per unit of work
+constexpr int kGradBlocks = 1024;        // workgroups, and partial sums, per launch at most
+
+struct GradBatch {
+    const void* src[kGradBatch];
+    void* dst[kGradBatch];
+    int64_t numel[kGradBatch];
+    uint32_t first[kGradBatch + 1];      // first unit of work of each tensor, and their number
+    uint32_t is_bf16[(kGradBatch + 31) / 32];
+    int n;
+};
+inline int grad_blocks(const GradBatch& b) {
+    const uint32_t units = b.first[b.n];
+    return units < (uint32_t)kGradBlocks ? (int)units : kGradBlocks;
+}
+// part[0 .. grad_blocks): sums of squares
+hipError_t launch_grad_sumsq(const GradBatch& b, double* part, hipStream_t s);
+// stats = {norm, coef} of n partial sums; with sum, also their sum there
+hipError_t launch_grad_stats(const double* part, int64_t n, float max_norm, float* stats, double* sum, hipStream_t s);
+// dst = coef src, coef from n partial sums; with stats, also {norm, coef} there
+hipError_t launch_grad_scale(const GradBatch& b, const double* part, int n, float max_norm, float* stats,
+                             hipStream_t s);
+
+}  // namespace m3

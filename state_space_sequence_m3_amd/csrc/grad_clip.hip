@@ -1,0 +1,174 @@
+// grad_clip.hip -- the 2-norm over many tensors and the scaling that clips it.
+//
+// The tensors' table travels as a kernel argument, so a call needs no copy to the device and no
+// launch per tensor.  Work is cut into units of kGradChunk elements of one tensor; a workgroup
+// takes every gridDim-th unit, so which sums meet in which order is fixed.
+#include "block_launch.h"
+#include "m3_device.h"
+
+namespace m3 {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct __attribute__((packed, aligned(2))) Bytes16 { uint32_t v[4]; };
+
+// The tensor that holds unit u: the last one whose first unit is at or before it (tensors have at
+// least one unit each).
+__device__ __forceinline__ int tensor_of(const GradBatch& b, uint32_t u) {
+    int lo = 0, hi = b.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (b.first[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+__device__ __forceinline__ bool is_bf16(const GradBatch& b, int i) { return (b.is_bf16[i >> 5] >> (i & 31)) & 1; }
+
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double s[kThreads / 64];
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double t = 0.0;
+    for (int k = 0; k < kThreads / 64; ++k) t += s[k];
+    __syncthreads();
+    return t;
+}
+
+__global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const GradBatch b, double* part) {
+    double acc[2] = {0.0, 0.0};
+    const uint32_t units = b.first[b.n];
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int i = tensor_of(b, u);
+        const int64_t at = (int64_t)(u - b.first[i]) * kGradChunk;
+        const int64_t left = b.numel[i] - at;
+        const int n = (int)(left < kGradChunk ? left : kGradChunk);
+        if (is_bf16(b, i)) {
+            const uint16_t* p = (const uint16_t*)b.src[i] + at;
+            int e = threadIdx.x * 8;
+#pragma unroll 4
+            for (; e + 8 <= n; e += kThreads * 8) {
+                const Bytes16 v = *(const Bytes16*)(p + e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const double lo = __uint_as_float(v.v[k] << 16), hi = __uint_as_float(v.v[k] & 0xffff0000u);
+                    acc[0] = fma(lo, lo, acc[0]);
+                    acc[1] = fma(hi, hi, acc[1]);
+                }
+            }
+            for (; e < n; ++e) {
+                const double g = __uint_as_float((uint32_t)p[e] << 16);
+                acc[0] = fma(g, g, acc[0]);
+            }
+        } else {
+            const float* p = (const float*)b.src[i] + at;
+            int e = threadIdx.x * 4;
+#pragma unroll 4
+            for (; e + 4 <= n; e += kThreads * 4) {
+                const Bytes16 v = *(const Bytes16*)(p + e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const double g = __uint_as_float(v.v[k]);
+                    acc[k & 1] = fma(g, g, acc[k & 1]);
+                }
+            }
+            for (; e < n; ++e) {
+                const double g = p[e];
+                acc[0] = fma(g, g, acc[0]);
+            }
+        }
+    }
+    const double t = block_sum(acc[0] + acc[1]);
+    if (threadIdx.x == 0) part[blockIdx.x] = t;
+}
+
+// the sum of n partial sums, the same in every workgroup
+__device__ __forceinline__ double all_parts(const double* part, int64_t n) {
+    double v = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) v += part[i];
+    return block_sum(v);
+}
+__device__ __forceinline__ float2 norm_and_coef(double sum, float max_norm) {
+    const double norm = sqrt(sum);
+    const double c = (double)max_norm / (norm + 1e-6);
+    return make_float2((float)norm, c > 1.0 ? 1.f : (float)c);   // a NaN stays one
+}
+
+__global__ __launch_bounds__(kThreads) void grad_stats_kernel(const double* part, int64_t n, float max_norm,
+                                                              float* stats, double* sum) {
+    const double t = all_parts(part, n);
+    if (threadIdx.x == 0) {
+        const float2 nc = norm_and_coef(t, max_norm);
+        if (stats) {
+            stats[0] = nc.x;
+            stats[1] = nc.y;
+        }
+        if (sum) *sum = t;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradBatch b, const double* part, int n_part,
+                                                              float max_norm, float* stats) {
+    const float2 nc = norm_and_coef(all_parts(part, n_part), max_norm);
+    if (stats && blockIdx.x == 0 && threadIdx.x == 0) {
+        stats[0] = nc.x;
+        stats[1] = nc.y;
+    }
+    const float coef = nc.y;
+    const uint32_t units = b.first[b.n];
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int i = tensor_of(b, u);
+        if (coef == 1.f && b.src[i] == b.dst[i]) continue;
+        const int64_t at = (int64_t)(u - b.first[i]) * kGradChunk;
+        const int64_t left = b.numel[i] - at;
+        const int n = (int)(left < kGradChunk ? left : kGradChunk);
+        if (is_bf16(b, i)) {
+            const uint16_t* p = (const uint16_t*)b.src[i] + at;
+            uint16_t* o = (uint16_t*)b.dst[i] + at;
+            int e = threadIdx.x * 8;
+#pragma unroll 4
+            for (; e + 8 <= n; e += kThreads * 8) {
+                const Bytes16 v = *(const Bytes16*)(p + e);
+                Bytes16 w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w.v[k] = pack_bf16x2(coef * __uint_as_float(v.v[k] << 16), coef * __uint_as_float(v.v[k] & 0xffff0000u));
+                *(Bytes16*)(o + e) = w;
+            }
+            for (; e < n; ++e) o[e] = bf16_bits_rne(coef * __uint_as_float((uint32_t)p[e] << 16));
+        } else {
+            const float* p = (const float*)b.src[i] + at;
+            float* o = (float*)b.dst[i] + at;
+            int e = threadIdx.x * 4;
+#pragma unroll 4
+            for (; e + 4 <= n; e += kThreads * 4) {
+                const Bytes16 v = *(const Bytes16*)(p + e);
+                Bytes16 w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w.v[k] = __float_as_uint(coef * __uint_as_float(v.v[k]));
+                *(Bytes16*)(o + e) = w;
+            }
+            for (; e < n; ++e) o[e] = coef * p[e];
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_grad_sumsq(const GradBatch& b, double* part, hipStream_t s) {
+    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(grad_blocks(b)), dim3(kThreads), 0, s, b, part);
+    return hipGetLastError();
+}
+hipError_t launch_grad_stats(const double* part, int64_t n, float max_norm, float* stats, double* sum, hipStream_t s) {
+    hipLaunchKernelGGL(grad_stats_kernel, dim3(1), dim3(kThreads), 0, s, part, n, max_norm, stats, sum);
+    return hipGetLastError();
+}
+hipError_t launch_grad_scale(const GradBatch& b, const double* part, int n, float max_norm, float* stats,
+                             hipStream_t s) {
+    hipLaunchKernelGGL(grad_scale_kernel, dim3(grad_blocks(b)), dim3(kThreads), 0, s, b, part, n, max_norm, stats);
+    return hipGetLastError();
+}
+
+}  // namespace m3
