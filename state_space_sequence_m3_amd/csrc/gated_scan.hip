@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kWaves = 8;                        // waves per tile
 constexpr int kSteps = kScanTile / kWaves;       // consecutive tokens of one wave
+constexpr int kFwdWavesPerSimd = 4, kBwdWavesPerSimd = 2;
 
 // z = sigmoid(u) and 1 - z, each to a few units in its last place: the smaller one is e^-|u| / (1 + e^-|u|),
 // not a difference from 1.  fp32 io carries the rounding of u log2(e) along; with bf16 io the
@@ -112,33 +113,87 @@ __device__ __forceinline__ int64_t seq_of(const GatedScanArgs& a, int64_t t) {
     return lo;
 }
 
-// A tile's place: tokens [t0, t0 + nv), the chain's neighbour tiles, and its row of `states`.
+// A tile's place: tokens [t0, t0 + nv), its neighbours in the chain, and its row of `states`.
 struct Tile {
     int64_t t0, prev, next, row;
+    uint32_t links_before, links_after;   // tiles of the same chain
     int nv;
 };
-__device__ __forceinline__ Tile tile_of(const GatedScanArgs& a, int64_t c) {
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ uint32_t uniform32(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ Tile tile_of(const GatedScanArgs& a, uint32_t c) {
     Tile t;
     if (a.per_seq) {
         // tiles in the order (place in the sequence, sequence): the tiles that run at the same time
         // belong to as many sequences as there are, and a chain link waits less
-        const int64_t j = c / a.b, s = c % a.b;
-        t.t0 = s * a.L + j * kScanTile;
-        const int64_t left = a.L - j * kScanTile;
+        const uint32_t b = (uint32_t)a.b, j = uniform32(c / b), s = c - j * b, n = (uint32_t)a.seq_chunks;
+        t.t0 = (int64_t)s * a.L + (int64_t)j * kScanTile;
+        const int64_t left = a.L - (int64_t)j * kScanTile;
         t.nv = (int)(left < kScanTile ? left : kScanTile);
-        t.prev = j > 0 ? c - a.b : -1;
-        t.next = j + 1 < a.seq_chunks ? c + a.b : -1;
-        t.row = s * a.seq_chunks + j;
+        t.prev = j > 0 ? (int64_t)c - b : -1;
+        t.next = j + 1 < n ? (int64_t)c + b : -1;
+        t.links_before = j;
+        t.links_after = n - 1 - j;
+        t.row = (int64_t)s * n + j;
     } else {
         const int64_t total = a.cu ? seq_start(a, a.b) : a.T;
-        t.t0 = c * kScanTile;
+        t.t0 = (int64_t)c * kScanTile;
         const int64_t left = total - t.t0;
         t.nv = (int)(left < 0 ? 0 : (left < kScanTile ? left : kScanTile));
-        t.prev = c - 1;
-        t.next = c + 1 < a.nchunks ? c + 1 : -1;
+        t.prev = (int64_t)c - 1;
+        t.next = (int64_t)c + 1 < a.nchunks ? (int64_t)c + 1 : -1;
+        t.links_before = c;
+        t.links_after = (uint32_t)a.nchunks - 1 - c;
         t.row = c;
     }
     return t;
+}
+
+// Which tokens of a tile start or end a sequence.  A tile of one long sequence (per_seq) knows by its
+// place; else one thread per token looks its sequence up, and all threads must come here.
+struct Marks {
+    int seq[kScanTile];                          // the sequence of each token
+    uint64_t starts[kScanTile / 64], ends[kScanTile / 64];
+};
+__device__ __forceinline__ void find_marks(const GatedScanArgs& a, const Tile& tile, Marks& m) {
+    if (a.per_seq) return;
+    const int i = threadIdx.x;
+    if (i < kScanTile) {
+        bool start = false, end = false;
+        if (i < tile.nv) {
+            const int64_t t = tile.t0 + i, s = seq_of(a, t);
+            m.seq[i] = (int)s;
+            start = seq_start(a, s) == t;
+            end = seq_start(a, s + 1) == t + 1;
+        }
+        const uint64_t ms = __ballot(start), me = __ballot(end);
+        if ((i & 63) == 0) {
+            m.starts[i >> 6] = ms;
+            m.ends[i >> 6] = me;
+        }
+    }
+    __syncthreads();
+}
+// the kSteps tokens of wave w, as bits
+__device__ __forceinline__ uint32_t wave_starts(const GatedScanArgs& a, const Tile& tile, const Marks& m, int w) {
+    if (a.per_seq) return w == 0 && tile.prev < 0 ? 1u : 0u;
+    return uniform32((uint32_t)(m.starts[w * kSteps / 64] >> (w * kSteps % 64))) & ((1u << kSteps) - 1);
+}
+__device__ __forceinline__ uint32_t wave_ends(const GatedScanArgs& a, const Tile& tile, const Marks& m, int w) {
+    if (a.per_seq) {
+        const int last = tile.nv - 1 - w * kSteps;
+        return tile.next < 0 && last >= 0 && last < kSteps ? 1u << last : 0u;
+    }
+    return uniform32((uint32_t)(m.ends[w * kSteps / 64] >> (w * kSteps % 64))) & ((1u << kSteps) - 1);
+}
+// the sequence of token i of wave w (a start or an end)
+__device__ __forceinline__ int64_t mark_seq(const GatedScanArgs& a, const Tile& tile, const Marks& m, int w, int i) {
+    return a.per_seq ? tile.row / a.seq_chunks : (int64_t)uniform32((uint32_t)m.seq[w * kSteps + i]);
 }
 
 // ------------------------------------------------------------------------------ chain words
@@ -160,7 +215,7 @@ __device__ __forceinline__ uint64_t get_word(const uint64_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-constexpr int kWindow = 8;            // words looked at together
+constexpr int kWindow = 4;            // words looked at together
 constexpr int kMaxPolls = 1 << 22;    // some seconds: a wait that long means a workspace in use twice
 
 // The state that enters a tile whose neighbour in the chain is `first`, the one after that
@@ -171,12 +226,12 @@ constexpr int kMaxPolls = 1 << 22;    // some seconds: a wait that long means a 
 // itself waits for earlier ones only; the first tile of a chain waits for none.  A wait that
 // outlasts kMaxPolls gives NaN.
 __device__ __forceinline__ void chain_wait(const uint64_t* words, int64_t stride, int64_t first, int64_t step,
-                                           int64_t links, const int64_t (&d)[2], float (&carry)[2]) {
+                                           uint32_t links, const int64_t (&d)[2], float (&carry)[2]) {
     for (int poll = 0; poll < kMaxPolls; ++poll) {
         uint64_t w[kWindow][2];
 #pragma unroll
         for (int k = 0; k < kWindow; ++k) {
-            if (k < links) {
+            if ((uint32_t)k < links) {
                 const uint64_t* row = words + (first + k * step) * stride;
                 w[k][0] = get_word(row + d[0]);
                 w[k][1] = get_word(row + d[1]);
@@ -213,86 +268,96 @@ __global__ __launch_bounds__(256) void chain_reset_kernel(uint4* words, int64_t 
 }
 
 // ---------------------------------------------------------------------------------- forward
+// The tile a workgroup works on, and its columns: the workgroup's place in the grid, or, where tiles
+// wait for each other, a number from a counter, so that tiles start in chain order.
+__device__ __forceinline__ bool take_item(const GatedScanArgs& a, unsigned& s_ticket, uint32_t& c, int& col) {
+    uint32_t item = blockIdx.x;
+    if (a.nchunks > 1) {
+        if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u);
+        __syncthreads();
+        item = uniform32(s_ticket);
+        if (item >= (uint32_t)a.nchunks * (uint32_t)a.ncols) return false;
+    }
+    c = uniform32(item / (uint32_t)a.ncols);
+    col = (int)(item - c * (uint32_t)a.ncols);
+    return true;
+}
+
 template <typename T, bool VEC>
-__global__ __launch_bounds__(kWaves * 64) void gated_scan_kernel(const GatedScanArgs a) {
+__global__ __launch_bounds__(kWaves * 64, kFwdWavesPerSimd) void gated_scan_kernel(const GatedScanArgs a) {
     __shared__ float2 sA[kWaves][64], sB[kWaves][64], sCarry[64];
     __shared__ int sHard[kWaves];   // bit 0: the wave's tokens hold a sequence start; bit 1: its first token is one
+    __shared__ Marks sMarks;
     __shared__ unsigned sTicket;
     const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t item = blockIdx.x;
-    if (a.nchunks > 1) {
-        if (threadIdx.x == 0) sTicket = atomicAdd(a.ticket, 1u);
-        __syncthreads();
-        item = __builtin_amdgcn_readfirstlane(sTicket);
-        if (item >= a.nchunks * a.ncols) return;
-    }
-    const int64_t c = item / a.ncols;
-    const int col = (int)(item % a.ncols);
+    const int w = uniform32(threadIdx.x >> 6);
+    uint32_t c;
+    int col;
+    if (!take_item(a, sTicket, c, col)) return;
     const Tile tile = tile_of(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
-
     const int64_t tw = tile.t0 + w * kSteps;
     const int left = tile.nv - w * kSteps;
     const int nv = left < 0 ? 0 : (left < kSteps ? left : kSteps);
 
-    float keep[kSteps][2], add[kSteps][2];
-    uint32_t starts = 0;
-    int64_t seq = 0;
+    // rows past the last one are read as the last one again, and do nothing
+    Pair<T, VEC> rg[kSteps], rx[kSteps];
     if (nv > 0) {
-        Pair<T, VEC> rg[kSteps], rx[kSteps];
         const char* gp = (const char*)a.gate + tw * a.gate_p;
         const char* xp = (const char*)a.x + tw * a.x_p;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int64_t r = i < nv ? i : nv - 1;
-            rg[i].load(gp + r * a.gate_p, cols.off[0], cols.off[1]);
-            rx[i].load(xp + r * a.x_p, cols.off[0], cols.off[1]);
+            rg[i].load(gp, cols.off[0], cols.off[1]);
+            rx[i].load(xp, cols.off[0], cols.off[1]);
+            gp += i + 1 < nv ? a.gate_p : 0;
+            xp += i + 1 < nv ? a.x_p : 0;
         }
-        float bias[2] = {0.f, 0.f};
-        if (a.bias) {
-            bias[0] = a.bias[cols.off[0] / sizeof(T)];
-            bias[1] = a.bias[cols.off[1] / sizeof(T)];
-        }
-        seq = seq_of(a, tw);
-        int64_t s = seq, end = seq_start(a, s + 1);
-        const bool starts_here = seq_start(a, s) == tw;
+    }
+    float bias[2] = {0.f, 0.f};
+    if (a.bias) {
+        bias[0] = a.bias[cols.off[0] / sizeof(T)];
+        bias[1] = a.bias[cols.off[1] / sizeof(T)];
+    }
+    find_marks(a, tile, sMarks);
+    const uint32_t starts = wave_starts(a, tile, sMarks, w);
+    float keep[kSteps][2], add[kSteps][2];
+    float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};   // the wave's map
+    if (nv > 0) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
+        for (int i = 0; i < kSteps; ++i)
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 float z;
                 gate_of<T>(rg[i].get(v) + bias[v], z, keep[i][v]);
                 add[i][v] = z * rx[i].get(v);
-                if (i >= nv) {
-                    keep[i][v] = 1.f;
-                    add[i][v] = 0.f;
-                }
-            }
-            if (i < nv && (i == 0 ? starts_here : tw + i == end)) {
-                while (i > 0 && s + 1 < a.b && seq_start(a, s + 1) <= tw + i) ++s;
-                end = seq_start(a, s + 1);
-                starts |= 1u << i;
-                if (a.h_in) {
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-                        if (cols.ok[v]) add[i][v] = fmaf(keep[i][v], a.h_in[s * a.D + cols.d[v]], add[i][v]);
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-            for (int v = 0; v < 2; ++v) {
-                keep[i][v] = 1.f;
-                add[i][v] = 0.f;
             }
     }
-    {   // the wave's map
-        float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};
+    if (nv < kSteps) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            if (i >= nv) {
+                keep[i][0] = keep[i][1] = 1.f;
+                add[i][0] = add[i][1] = 0.f;
+            }
+    }
+    if (starts == 0) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                A[v] *= keep[i][v];
+                B[v] = fmaf(keep[i][v], B[v], add[i][v]);
+            }
+    } else {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             if ((starts >> i) & 1) {
+                if (a.h_in) {
+                    const float* h = a.h_in + mark_seq(a, tile, sMarks, w, i) * a.D;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+                        if (cols.ok[v]) add[i][v] = fmaf(keep[i][v], h[cols.d[v]], add[i][v]);
+                }
                 A[0] = A[1] = 0.f;
                 B[0] = add[i][0];
                 B[1] = add[i][1];
@@ -304,17 +369,17 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_kernel(const GatedScan
                 }
             }
         }
-        sA[w][lane] = make_float2(A[0], A[1]);
-        sB[w][lane] = make_float2(B[0], B[1]);
-        if (lane == 0) sHard[w] = (starts != 0 ? 1 : 0) | (starts & 1 ? 2 : 0);
     }
+    sA[w][lane] = make_float2(A[0], A[1]);
+    sB[w][lane] = make_float2(B[0], B[1]);
+    if (lane == 0) sHard[w] = (starts != 0 ? 1 : 0) | (starts & 1 ? 2 : 0);
     __syncthreads();
     // the map of the waves before this one
     float Ap[2] = {1.f, 1.f}, Bp[2] = {0.f, 0.f};
     bool hard = false;
     auto compose = [&](int k) {
         const float2 A = sA[k][lane], B = sB[k][lane];
-        if (__builtin_amdgcn_readfirstlane(sHard[k]) & 1) {
+        if (uniform32(sHard[k]) & 1) {
             hard = true;
             Ap[0] = Ap[1] = 0.f;
             Bp[0] = B.x;
@@ -332,17 +397,14 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_kernel(const GatedScan
         const float A0[2] = {Ap[0], Ap[1]}, B0[2] = {Bp[0], Bp[1]};
         const bool hard0 = hard;
         compose(w);
-        const int64_t stride = (int64_t)a.ncols * kScanCols;
-        uint64_t* mine = a.words + c * stride;
         if (a.nchunks > 1) {
+            const int64_t stride = (int64_t)a.ncols * kScanCols;
+            uint64_t* mine = a.words + c * stride;
 #pragma unroll
             for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], hard ? final_word(Bp[v]) : map_word(Ap[v], Bp[v]));
-            const bool starts_here = (__builtin_amdgcn_readfirstlane(sHard[0]) & 2) != 0;
-            if (tile.prev >= 0 && tile.nv > 0 && !starts_here) {
-                const int64_t step = a.per_seq ? -a.b : -1;
-                const int64_t links = a.per_seq ? c / a.b : c;
-                chain_wait(a.words, stride, tile.prev, step, links, cols.d, carry);
-            }
+            const bool starts_here = (uniform32(sHard[0]) & 2) != 0;
+            if (tile.prev >= 0 && tile.nv > 0 && !starts_here)
+                chain_wait(a.words, stride, tile.prev, a.per_seq ? -a.b : -1, tile.links_before, cols.d, carry);
             if (!hard) {
 #pragma unroll
                 for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], final_word(fmaf(Ap[v], carry[v], Bp[v])));
@@ -359,34 +421,36 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_kernel(const GatedScan
         hard = hard0;
     }
     __syncthreads();
+    float h[2];
     {
         const float2 cy = sCarry[lane];
-        carry[0] = cy.x;
-        carry[1] = cy.y;
+        h[0] = hard ? Bp[0] : fmaf(Ap[0], cy.x, Bp[0]);
+        h[1] = hard ? Bp[1] : fmaf(Ap[1], cy.y, Bp[1]);
     }
-    float h[2];
+    const uint32_t ends = wave_ends(a, tile, sMarks, w);
+    char* yp = (char*)a.y + tw * a.y_p;
+    if (nv == kSteps && (starts | ends) == 0) {
 #pragma unroll
-    for (int v = 0; v < 2; ++v) h[v] = hard ? Bp[v] : fmaf(Ap[v], carry[v], Bp[v]);
-    if (nv > 0) {
-        char* yp = (char*)a.y + tw * a.y_p;
-        int64_t s = seq, end = seq_start(a, s + 1);
+        for (int i = 0; i < kSteps; ++i) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) h[v] = fmaf(keep[i][v], h[v], add[i][v]);
+            store_pair<T, VEC>(yp, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], h[0], h[1]);
+            yp += a.y_p;
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             if (i < nv) {
-                if ((starts >> i) & 1) {
-                    while (i > 0 && s + 1 < a.b && seq_start(a, s + 1) <= tw + i) ++s;
-                    end = seq_start(a, s + 1);
-                    h[0] = add[i][0];
-                    h[1] = add[i][1];
-                } else {
+                if ((starts >> i) & 1) h[0] = h[1] = 0.f;   // and the carried state is in add
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) h[v] = fmaf(keep[i][v], h[v], add[i][v]);
-                }
-                store_pair<T, VEC>(yp + i * a.y_p, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], h[0], h[1]);
-                if (tw + i + 1 == end) {
+                for (int v = 0; v < 2; ++v) h[v] = fmaf(keep[i][v], h[v], add[i][v]);
+                store_pair<T, VEC>(yp, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], h[0], h[1]);
+                yp += a.y_p;
+                if ((ends >> i) & 1) {
+                    float* o = a.h_out + mark_seq(a, tile, sMarks, w, i) * a.D;
 #pragma unroll
                     for (int v = 0; v < 2; ++v)
-                        if (cols.ok[v]) a.h_out[s * a.D + cols.d[v]] = h[v];
+                        if (cols.ok[v]) o[cols.d[v]] = h[v];
                 }
             }
         }
@@ -407,120 +471,128 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_kernel(const GatedScan
 // G_t = keep_t G_{t+1} + keep_t dy_t, an affine map again, and the same chain in the other
 // direction.  A sequence's last token takes dh_out for G_{t+1}.
 template <typename T, bool VEC>
-__global__ __launch_bounds__(kWaves * 64) void gated_scan_backward_kernel(const GatedScanArgs a) {
+__global__ __launch_bounds__(kWaves * 64, kBwdWavesPerSimd) void gated_scan_backward_kernel(const GatedScanArgs a) {
     __shared__ float2 sA[kWaves][64], sB[kWaves][64], sRA[kWaves][64], sRB[kWaves][64], sCarry[64];
     __shared__ int sHard[kWaves];   // bit 0: holds a sequence start; 1: holds an end; 2: its last token is an end
+    __shared__ Marks sMarks;
     __shared__ unsigned sTicket;
     const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t item = blockIdx.x;
-    if (a.nchunks > 1) {
-        if (threadIdx.x == 0) sTicket = atomicAdd(a.ticket, 1u);
-        __syncthreads();
-        item = __builtin_amdgcn_readfirstlane(sTicket);
-        if (item >= a.nchunks * a.ncols) return;
-    }
-    const int64_t c = a.nchunks - 1 - item / a.ncols;   // from the last tile to the first
-    const int col = (int)(item % a.ncols);
+    const int w = uniform32(threadIdx.x >> 6);
+    uint32_t c;
+    int col;
+    if (!take_item(a, sTicket, c, col)) return;
+    c = (uint32_t)a.nchunks - 1 - c;   // from the last tile to the first
     const Tile tile = tile_of(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
-
     const int64_t tw = tile.t0 + w * kSteps;
     const int left = tile.nv - w * kSteps;
     const int nv = left < 0 ? 0 : (left < kSteps ? left : kSteps);
 
-    float z[kSteps][2], keep[kSteps][2], xs[kSteps][2], lam[kSteps][2];   // lam: dy, then l_t
-    uint32_t starts = 0, ends = 0;
-    int64_t seq = 0;
+    Pair<T, VEC> rg[kSteps], rx[kSteps], rd[kSteps];
     if (nv > 0) {
-        Pair<T, VEC> rg[kSteps], rx[kSteps], rd[kSteps];
         const char* gp = (const char*)a.gate + tw * a.gate_p;
         const char* xp = (const char*)a.x + tw * a.x_p;
         const char* dp = (const char*)a.dy + tw * a.y_p;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int64_t r = i < nv ? i : nv - 1;
-            rg[i].load(gp + r * a.gate_p, cols.off[0], cols.off[1]);
-            rd[i].load(dp + r * a.y_p, cols.off[0], cols.off[1]);
-            rx[i].load(xp + r * a.x_p, cols.off[0], cols.off[1]);
+            rg[i].load(gp, cols.off[0], cols.off[1]);
+            rx[i].load(xp, cols.off[0], cols.off[1]);
+            rd[i].load(dp, cols.off[0], cols.off[1]);
+            gp += i + 1 < nv ? a.gate_p : 0;
+            xp += i + 1 < nv ? a.x_p : 0;
+            dp += i + 1 < nv ? a.y_p : 0;
         }
-        float bias[2] = {0.f, 0.f};
-        if (a.bias) {
-            bias[0] = a.bias[cols.off[0] / sizeof(T)];
-            bias[1] = a.bias[cols.off[1] / sizeof(T)];
-        }
-        seq = seq_of(a, tw);
-        int64_t s = seq, end = seq_start(a, s + 1);
-        if (seq_start(a, s) == tw) starts |= 1u;
+    }
+    float h[2], bias[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
+    for (int v = 0; v < 2; ++v) h[v] = cols.ok[v] ? a.states[tile.row * a.D + cols.d[v]] : 0.f;
+    if (a.bias) {
+        bias[0] = a.bias[cols.off[0] / sizeof(T)];
+        bias[1] = a.bias[cols.off[1] / sizeof(T)];
+    }
+    find_marks(a, tile, sMarks);
+    const uint32_t starts = wave_starts(a, tile, sMarks, w), ends = wave_ends(a, tile, sMarks, w);
+
+    float z[kSteps][2], keep[kSteps][2], xs[kSteps][2], lam[kSteps][2];   // lam: dy
+    if (nv > 0) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 gate_of<T>(rg[i].get(v) + bias[v], z[i][v], keep[i][v]);
                 xs[i][v] = rx[i].get(v);
                 lam[i][v] = rd[i].get(v);
-                if (i >= nv) {
+            }
+    }
+    if (nv < kSteps) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            if (i >= nv) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
                     z[i][v] = 0.f;
                     keep[i][v] = 1.f;
                     xs[i][v] = 0.f;
                     lam[i][v] = 0.f;
                 }
             }
-            if (i < nv) {
-                if (i > 0 && tw + i == end) {
-                    while (s + 1 < a.b && seq_start(a, s + 1) <= tw + i) ++s;
-                    end = seq_start(a, s + 1);
-                    starts |= 1u << i;
-                }
-                if (tw + i + 1 == end) {
-                    ends |= 1u << i;
-                    if (a.dh_out) {
-#pragma unroll
-                        for (int v = 0; v < 2; ++v)
-                            if (cols.ok[v]) lam[i][v] += a.dh_out[s * a.D + cols.d[v]];
-                    }
-                }
-            }
-        }
-    } else {
+    }
+    const bool marked = (starts | ends) != 0;
+    if (ends != 0 && a.dh_out) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
-            for (int v = 0; v < 2; ++v) {
-                z[i][v] = 0.f;
-                keep[i][v] = 1.f;
-                xs[i][v] = 0.f;
-                lam[i][v] = 0.f;
+            if ((ends >> i) & 1) {
+                const float* d = a.dh_out + mark_seq(a, tile, sMarks, w, i) * a.D;
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+                    if (cols.ok[v]) lam[i][v] += d[cols.d[v]];
             }
     }
     {   // the wave's maps, forwards and backwards
-        float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};
-        int64_t s = seq;
+        float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f}, RA[2] = {1.f, 1.f}, RB[2] = {0.f, 0.f};
+        if (!marked) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            if ((starts >> i) & 1) {
-                while (i > 0 && s + 1 < a.b && seq_start(a, s + 1) <= tw + i) ++s;
-                A[0] = A[1] = 0.f;
+            for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-                for (int v = 0; v < 2; ++v) B[v] = a.h_in && cols.ok[v] ? a.h_in[s * a.D + cols.d[v]] : 0.f;
+                for (int v = 0; v < 2; ++v) {
+                    A[v] *= keep[i][v];
+                    B[v] = fmaf(keep[i][v], B[v], z[i][v] * xs[i][v]);
+                }
+            RA[0] = A[0];
+            RA[1] = A[1];
+#pragma unroll
+            for (int i = kSteps - 1; i >= 0; --i)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) RB[v] = keep[i][v] * (RB[v] + lam[i][v]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                if ((starts >> i) & 1) {
+                    A[0] = A[1] = B[0] = B[1] = 0.f;
+                    if (a.h_in) {
+                        const float* hi = a.h_in + mark_seq(a, tile, sMarks, w, i) * a.D;
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) B[v] = cols.ok[v] ? hi[cols.d[v]] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    A[v] *= keep[i][v];
+                    B[v] = fmaf(keep[i][v], B[v], z[i][v] * xs[i][v]);
+                }
             }
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                A[v] *= keep[i][v];
-                B[v] = fmaf(keep[i][v], B[v], z[i][v] * xs[i][v]);
+            for (int i = kSteps - 1; i >= 0; --i) {
+                if ((ends >> i) & 1) RA[0] = RA[1] = RB[0] = RB[1] = 0.f;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    RA[v] *= keep[i][v];
+                    RB[v] = keep[i][v] * (RB[v] + lam[i][v]);
+                }
             }
         }
         sA[w][lane] = make_float2(A[0], A[1]);
         sB[w][lane] = make_float2(B[0], B[1]);
-        float RA[2] = {1.f, 1.f}, RB[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = kSteps - 1; i >= 0; --i) {
-            if ((ends >> i) & 1) RA[0] = RA[1] = RB[0] = RB[1] = 0.f;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                RA[v] *= keep[i][v];
-                RB[v] = keep[i][v] * (RB[v] + lam[i][v]);
-            }
-        }
         sRA[w][lane] = make_float2(RA[0], RA[1]);
         sRB[w][lane] = make_float2(RB[0], RB[1]);
         if (lane == 0)
@@ -528,12 +600,9 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_backward_kernel(const 
     }
     __syncthreads();
     // state that enters this wave
-    float h[2];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) h[v] = cols.ok[v] ? a.states[tile.row * a.D + cols.d[v]] : 0.f;
     for (int k = 0; k < w; ++k) {
         const float2 A = sA[k][lane], B = sB[k][lane];
-        const bool cut = __builtin_amdgcn_readfirstlane(sHard[k]) & 1;
+        const bool cut = uniform32(sHard[k]) & 1;
         h[0] = cut ? B.x : fmaf(A.x, h[0], B.x);
         h[1] = cut ? B.y : fmaf(A.y, h[1], B.y);
     }
@@ -542,7 +611,7 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_backward_kernel(const 
     bool hard = false;
     auto compose = [&](int k) {
         const float2 A = sRA[k][lane], B = sRB[k][lane];
-        if (__builtin_amdgcn_readfirstlane(sHard[k]) & 2) {
+        if (uniform32(sHard[k]) & 2) {
             hard = true;
             Ap[0] = Ap[1] = 0.f;
             Bp[0] = B.x;
@@ -568,12 +637,9 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_backward_kernel(const 
             // nothing enters from behind when the tile's last token ends a sequence, or tokens end here
             int last = 0;
             for (int k = 0; k < kWaves; ++k) last = tile.nv > k * kSteps ? sHard[k] : last;
-            const bool ends_here = tile.nv == 0 || (__builtin_amdgcn_readfirstlane(last) & 4) != 0;
-            if (tile.next >= 0 && !ends_here) {
-                const int64_t step = a.per_seq ? a.b : 1;
-                const int64_t links = a.per_seq ? a.seq_chunks - 1 - c / a.b : a.nchunks - 1 - c;
-                chain_wait(a.words, stride, tile.next, step, links, cols.d, carry);
-            }
+            const bool ends_here = tile.nv == 0 || (uniform32(last) & 4) != 0;
+            if (tile.next >= 0 && !ends_here)
+                chain_wait(a.words, stride, tile.next, a.per_seq ? a.b : 1, tile.links_after, cols.d, carry);
             if (!hard) {
 #pragma unroll
                 for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], final_word(fmaf(Ap[v], carry[v], Bp[v])));
@@ -584,6 +650,32 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_backward_kernel(const 
         Bp[0] = B0[0]; Bp[1] = B0[1];
         hard = hard0;
     }
+    // forwards: what dgate is of l_t, in the place of x
+    if (starts == 0) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float x = xs[i][v];
+                xs[i][v] = z[i][v] * keep[i][v] * (x - h[v]);
+                h[v] = fmaf(keep[i][v], h[v], z[i][v] * x);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            if ((starts >> i) & 1) {
+                const float* hi = a.h_in ? a.h_in + mark_seq(a, tile, sMarks, w, i) * a.D : nullptr;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) h[v] = hi && cols.ok[v] ? hi[cols.d[v]] : 0.f;
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float x = xs[i][v];
+                xs[i][v] = z[i][v] * keep[i][v] * (x - h[v]);
+                h[v] = fmaf(keep[i][v], h[v], z[i][v] * x);
+            }
+        }
+    }
     __syncthreads();
     float G[2];
     {
@@ -591,56 +683,44 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_backward_kernel(const 
         G[0] = hard ? Bp[0] : fmaf(Ap[0], cy.x, Bp[0]);
         G[1] = hard ? Bp[1] : fmaf(Ap[1], cy.y, Bp[1]);
     }
-    // forwards: what dgate is of l_t, in the place of x
-    int64_t s = seq;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        if ((starts >> i) & 1) {
-            while (i > 0 && s + 1 < a.b && seq_start(a, s + 1) <= tw + i) ++s;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) h[v] = a.h_in && cols.ok[v] ? a.h_in[s * a.D + cols.d[v]] : 0.f;
-        }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const float x = xs[i][v];
-            xs[i][v] = z[i][v] * keep[i][v] * (x - h[v]);
-            h[v] = fmaf(keep[i][v], h[v], z[i][v] * x);
-        }
-    }
     // backwards
     float sum[2] = {0.f, 0.f};
-    if (nv > 0) {
-        char* gp = (char*)a.dgate + tw * a.dgate_p;
-        char* xp = (char*)a.dx + tw * a.dx_p;
+    char* gp = (char*)a.dgate + (tw + nv - 1) * a.dgate_p;
+    char* xp = (char*)a.dx + (tw + nv - 1) * a.dx_p;
+    auto token = [&](int i) {
+        float dg[2], dx[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const float l = lam[i][v] + G[v];
+            dx[v] = z[i][v] * l;
+            dg[v] = xs[i][v] * l;
+            sum[v] += dg[v];
+            G[v] = keep[i][v] * l;
+        }
+        store_pair<T, VEC>(gp, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], dg[0], dg[1]);
+        store_pair<T, VEC>(xp, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], dx[0], dx[1]);
+        gp -= a.dgate_p;
+        xp -= a.dx_p;
+    };
+    if (nv == kSteps && !marked) {
+#pragma unroll
+        for (int i = kSteps - 1; i >= 0; --i) token(i);
+    } else {
 #pragma unroll
         for (int i = kSteps - 1; i >= 0; --i) {
             if (i < nv) {
                 if ((ends >> i) & 1) G[0] = G[1] = 0.f;
-                float dg[2], dx[2];
+                token(i);
+                if (((starts >> i) & 1) && a.dh_in) {
+                    float* o = a.dh_in + mark_seq(a, tile, sMarks, w, i) * a.D;
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const float l = lam[i][v] + G[v];
-                    dx[v] = z[i][v] * l;
-                    dg[v] = xs[i][v] * l;
-                    sum[v] += dg[v];
-                    G[v] = keep[i][v] * l;
-                }
-                store_pair<T, VEC>(gp + i * a.dgate_p, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], dg[0], dg[1]);
-                store_pair<T, VEC>(xp + i * a.dx_p, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], dx[0], dx[1]);
-                if ((starts >> i) & 1) {
-                    if (a.dh_in && s >= 0) {
-#pragma unroll
-                        for (int v = 0; v < 2; ++v)
-                            if (cols.ok[v]) a.dh_in[s * a.D + cols.d[v]] = G[v];
-                    }
-                    --s;
-                    while (i > 0 && s > 0 && seq_start(a, s) >= tw + i) --s;
+                    for (int v = 0; v < 2; ++v)
+                        if (cols.ok[v]) o[cols.d[v]] = G[v];
                 }
             }
         }
     }
     if (a.dbias) {   // the tile's share: waves summed in order
-        __syncthreads();
         sA[w][lane] = make_float2(sum[0], sum[1]);
         __syncthreads();
         if (w == 0) {
@@ -650,7 +730,7 @@ __global__ __launch_bounds__(kWaves * 64) void gated_scan_backward_kernel(const 
                 t.x += sA[k][lane].x;
                 t.y += sA[k][lane].y;
             }
-            float* out = a.nchunks > 1 ? a.part + c * a.D : a.dbias;
+            float* out = a.nchunks > 1 ? a.part + (int64_t)c * a.D : a.dbias;
             if (cols.ok[0]) out[cols.d[0]] = t.x;
             if (cols.ok[1]) out[cols.d[1]] = t.y;
         }
