@@ -11,7 +11,7 @@
  *    Rows that start on 16-byte boundaries (scan: one 4-byte (bf16) or 8-byte (fp32) pair) take
  *    wider loads; nothing else depends on it.
  *  - Pitches.  A pitch is the distance in elements between the first elements of consecutive
- *    rows (tokens); 0 means dense.  Tensors may be slices of one wider buffer, outputs too, as long
+ *    rows (tokens); 0 means dense.  Gated scan: rows are at most 2^24 - 1 bytes apart.  Tensors may be slices of one wider buffer, outputs too, as long
  *    as no element is written twice or is both read and written, except where a call allows it.
  *  - Workspaces are scratch: nothing in them has to survive the call or to be cleared before it.
  *    Two calls that may run at the same time (on two streams, or in two graphs that are replayed at

@@ -78,10 +78,10 @@ m3_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t n
 
 // ------------------------------------------------------------------------------- gated scan
 struct ScanPlan {
-    int64_t T = 0, nchunks = 1, seq_chunks = 1;
+    int64_t T = 0, ntiles = 1, seq_tiles = 1, blocks = 1, seq_blocks = 1;
     int ncols = 0;
     bool per_seq = false;
-    size_t words_off = 256, part_off = 0, fwd_bytes = 0, bwd_bytes = 0;
+    size_t words_off = 256, part_off = 0, bytes = 0;
 };
 
 m3_status check_scan_dims(const m3_scan_dims* d) {
@@ -94,27 +94,29 @@ m3_status check_scan_dims(const m3_scan_dims* d) {
     return M3_OK;
 }
 
-m3_status plan_scan(const m3_scan_dims* d, bool packed, ScanPlan* p) {
+// The tiles of the forward or the backward pass, and the blocks that have a row of `states`.
+m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan* p) {
     M3_TRY(check_scan_dims(d));
-    constexpr int64_t tile = m3::kScanTile;
+    constexpr int64_t block = m3::kScanBlock;
+    const int64_t tile = d->io != M3_BF16 ? m3::kScanTileF32 : backward ? m3::kScanBwdTileBf16 : m3::kScanTileBf16;
     p->T = packed ? d->seqlen : d->batch * d->seqlen;
-    p->per_seq = !packed && d->batch > 0 && d->seqlen > tile;
+    p->per_seq = !packed && d->batch > 0 && d->seqlen > block;
     if (p->per_seq) {
-        p->seq_chunks = (d->seqlen + tile - 1) / tile;
-        p->nchunks = d->batch * p->seq_chunks;
+        p->seq_tiles = (d->seqlen + tile - 1) / tile;
+        p->seq_blocks = (d->seqlen + block - 1) / block;
+        p->ntiles = d->batch * p->seq_tiles;
+        p->blocks = d->batch * p->seq_blocks;
     } else {
-        p->nchunks = (p->T + tile - 1) / tile;
+        p->ntiles = std::max<int64_t>(1, (p->T + tile - 1) / tile);
+        p->blocks = std::max<int64_t>(1, (p->T + block - 1) / block);
     }
-    if (p->nchunks < 1) p->nchunks = 1;
     p->ncols = (int)((d->width + m3::kScanCols - 1) / m3::kScanCols);
-    if (p->nchunks >= kMaxCount || p->nchunks * p->ncols >= kMaxCount)
-        return fail(M3_E_DIMS, "%lld tokens of %lld channels: more than 2^31 tiles", (long long)p->T,
-                    (long long)d->width);
-    if (p->nchunks > 1) {
-        const size_t words = round256((size_t)p->nchunks * p->ncols * m3::kScanCols * 8);
-        p->part_off = p->words_off + words;
-        p->fwd_bytes = p->part_off;
-        p->bwd_bytes = p->part_off + (size_t)p->nchunks * d->width * 4;
+    if (p->blocks >= kMaxCount || p->blocks * p->ncols >= kMaxCount)
+        return fail(M3_E_DIMS, "%lld tokens of %lld channels: more than 2^31 blocks of 64 tokens and 128 channels",
+                    (long long)p->T, (long long)d->width);
+    if (p->ntiles > 1) {
+        p->part_off = p->words_off + round256((size_t)p->ntiles * p->ncols * m3::kScanCols * 8);
+        p->bytes = p->part_off + (backward ? (size_t)p->ntiles * d->width * 4 : 0);
     }
     return M3_OK;
 }
@@ -125,13 +127,23 @@ void scan_args(const m3_scan_dims* d, const ScanPlan& p, const int32_t* cu, void
     a->L = d->seqlen;
     a->T = p.T;
     a->D = d->width;
-    a->nchunks = p.nchunks;
-    a->seq_chunks = p.seq_chunks;
+    a->ntiles = p.ntiles;
+    a->seq_tiles = (uint32_t)p.seq_tiles;
+    a->seq_blocks = (uint32_t)p.seq_blocks;
     a->ncols = p.ncols;
     a->per_seq = p.per_seq ? 1 : 0;
     a->ticket = (unsigned*)ws;
     a->words = (uint64_t*)((char*)ws + p.words_off);
     a->part = (float*)((char*)ws + p.part_off);
+}
+
+// A tile's rows are addressed with 31-bit offsets from its first one.
+constexpr int64_t kMaxScanPitch = ((int64_t)1 << 31) / m3::kScanTileBf16;   // bytes
+m3_status check_scan_pitch(int64_t pitch, int64_t rows, int64_t width, int64_t es, const char* name, int64_t* bytes) {
+    M3_TRY(check_pitch(pitch, rows, width, es, name, bytes));
+    if (*bytes >= kMaxScanPitch)
+        return fail(M3_E_DIMS, "%s: rows are %lld bytes apart, the limit is 2^24", name, (long long)*bytes);
+    return M3_OK;
 }
 
 // Two channels per access: an even width, and rows that start on whole pairs.
@@ -302,17 +314,17 @@ extern "C" {
 
 int64_t m3_gated_scan_chunks(const m3_scan_dims* d, int packed) {
     ScanPlan p;
-    return plan_scan(d, packed != 0, &p) == M3_OK ? p.nchunks : 0;
+    return plan_scan(d, packed != 0, true, &p) == M3_OK ? p.blocks : 0;
 }
 
 size_t m3_gated_scan_workspace_bytes(const m3_scan_dims* d, int packed) {
     ScanPlan p;
-    return plan_scan(d, packed != 0, &p) == M3_OK ? p.fwd_bytes : 0;
+    return plan_scan(d, packed != 0, false, &p) == M3_OK ? p.bytes : 0;
 }
 
 size_t m3_gated_scan_backward_workspace_bytes(const m3_scan_dims* d, int packed) {
     ScanPlan p;
-    return plan_scan(d, packed != 0, &p) == M3_OK ? p.bwd_bytes : 0;
+    return plan_scan(d, packed != 0, true, &p) == M3_OK ? p.bytes : 0;
 }
 
 m3_status m3_gated_scan(const m3_scan_dims* d, const int32_t* cu_seqlens, const void* gate, const void* x,
@@ -320,21 +332,21 @@ m3_status m3_gated_scan(const m3_scan_dims* d, const int32_t* cu_seqlens, const 
                         size_t workspace_bytes, hipStream_t stream) {
     ScanPlan p;
     const bool packed = cu_seqlens != nullptr;
-    M3_TRY(plan_scan(d, packed, &p));
+    M3_TRY(plan_scan(d, packed, false, &p));
     const int64_t es = d->io == M3_BF16 ? 2 : 4, D = d->width, b = d->batch;
     int64_t gp, xp, yp;
-    M3_TRY(check_pitch(d->gate_pitch, p.T, D, es, "gate_pitch", &gp));
-    M3_TRY(check_pitch(d->x_pitch, p.T, D, es, "x_pitch", &xp));
-    M3_TRY(check_pitch(d->y_pitch, p.T, D, es, "y_pitch", &yp));
+    M3_TRY(check_scan_pitch(d->gate_pitch, p.T, D, es, "gate_pitch", &gp));
+    M3_TRY(check_scan_pitch(d->x_pitch, p.T, D, es, "x_pitch", &xp));
+    M3_TRY(check_scan_pitch(d->y_pitch, p.T, D, es, "y_pitch", &yp));
     const Region rg{gate, p.T, D * es, gp, "gate"}, rx{x, p.T, D * es, xp, "x"}, ry{y, p.T, D * es, yp, "y"};
     const Region rb{bias, 1, D * 4, D * 4, "bias"}, rhi{h_in, b, D * 4, D * 4, "h_in"};
-    const Region rho{h_out, b, D * 4, D * 4, "h_out"}, rst{states, p.nchunks, D * 4, D * 4, "states"};
+    const Region rho{h_out, b, D * 4, D * 4, "h_out"}, rst{states, p.blocks, D * 4, D * 4, "states"};
     const Region rcu{cu_seqlens, packed ? b + 1 : 0, 4, 4, "cu_seqlens"};
-    const Region rws{workspace, 1, (int64_t)p.fwd_bytes, (int64_t)p.fwd_bytes, "workspace"};
+    const Region rws{workspace, 1, (int64_t)p.bytes, (int64_t)p.bytes, "workspace"};
     for (const Region* r : {&rg, &rx, &ry, &rho}) M3_TRY(check_need(*r));
     for (const Region* r : {&rg, &rx, &ry}) M3_TRY(check_aligned(r->p, (size_t)es, r->name));
     for (const Region* r : {&rb, &rhi, &rho, &rst, &rcu}) M3_TRY(check_aligned(r->p, 4, r->name));
-    M3_TRY(check_workspace("m3_gated_scan", workspace, workspace_bytes, p.fwd_bytes));
+    M3_TRY(check_workspace("m3_gated_scan", workspace, workspace_bytes, p.bytes));
     const Region* outs[] = {&ry, &rho, &rst, &rws};
     for (int i = 0; i < 4; ++i) {
         for (const Region* in : {&rg, &rx, &rb, &rcu}) M3_TRY(check_clash(*outs[i], *in, false));
@@ -358,9 +370,9 @@ m3_status m3_gated_scan_step(const m3_scan_dims* d, const void* gate, const void
     const int64_t es = d->io == M3_BF16 ? 2 : 4, D = d->width, b = d->batch;
     if (b * D >= (int64_t)1 << 38) return fail(M3_E_DIMS, "size out of range");
     int64_t gp, xp, yp;
-    M3_TRY(check_pitch(d->gate_pitch, b, D, es, "gate_pitch", &gp));
-    M3_TRY(check_pitch(d->x_pitch, b, D, es, "x_pitch", &xp));
-    M3_TRY(check_pitch(d->y_pitch, b, D, es, "y_pitch", &yp));
+    M3_TRY(check_scan_pitch(d->gate_pitch, b, D, es, "gate_pitch", &gp));
+    M3_TRY(check_scan_pitch(d->x_pitch, b, D, es, "x_pitch", &xp));
+    M3_TRY(check_scan_pitch(d->y_pitch, b, D, es, "y_pitch", &yp));
     const Region rg{gate, b, D * es, gp, "gate"}, rx{x, b, D * es, xp, "x"}, ry{y, b, D * es, yp, "y"};
     const Region rb{bias, 1, D * 4, D * 4, "bias"}, rhi{h, b, D * 4, D * 4, "h"}, rho{h_out, b, D * 4, D * 4, "h_out"};
     for (const Region* r : {&rg, &rx, &ry, &rhi, &rho}) M3_TRY(check_need(*r));
@@ -386,25 +398,25 @@ m3_status m3_gated_scan_backward(const m3_scan_dims* d, const int32_t* cu_seqlen
                                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
     ScanPlan p;
     const bool packed = cu_seqlens != nullptr;
-    M3_TRY(plan_scan(d, packed, &p));
+    M3_TRY(plan_scan(d, packed, true, &p));
     const int64_t es = d->io == M3_BF16 ? 2 : 4, D = d->width, b = d->batch;
     int64_t gp, xp, yp, dgp, dxp;
-    M3_TRY(check_pitch(d->gate_pitch, p.T, D, es, "gate_pitch", &gp));
-    M3_TRY(check_pitch(d->x_pitch, p.T, D, es, "x_pitch", &xp));
-    M3_TRY(check_pitch(d->y_pitch, p.T, D, es, "y_pitch", &yp));
-    M3_TRY(check_pitch(d->dgate_pitch, p.T, D, es, "dgate_pitch", &dgp));
-    M3_TRY(check_pitch(d->dx_pitch, p.T, D, es, "dx_pitch", &dxp));
+    M3_TRY(check_scan_pitch(d->gate_pitch, p.T, D, es, "gate_pitch", &gp));
+    M3_TRY(check_scan_pitch(d->x_pitch, p.T, D, es, "x_pitch", &xp));
+    M3_TRY(check_scan_pitch(d->y_pitch, p.T, D, es, "y_pitch", &yp));
+    M3_TRY(check_scan_pitch(d->dgate_pitch, p.T, D, es, "dgate_pitch", &dgp));
+    M3_TRY(check_scan_pitch(d->dx_pitch, p.T, D, es, "dx_pitch", &dxp));
     const Region rg{gate, p.T, D * es, gp, "gate"}, rx{x, p.T, D * es, xp, "x"}, rdy{dy, p.T, D * es, yp, "dy"};
     const Region rdg{dgate, p.T, D * es, dgp, "dgate"}, rdx{dx, p.T, D * es, dxp, "dx"};
     const Region rb{bias, 1, D * 4, D * 4, "bias"}, rhi{h_in, b, D * 4, D * 4, "h_in"};
-    const Region rst{states, p.nchunks, D * 4, D * 4, "states"}, rdho{dh_out, b, D * 4, D * 4, "dh_out"};
+    const Region rst{states, p.blocks, D * 4, D * 4, "states"}, rdho{dh_out, b, D * 4, D * 4, "dh_out"};
     const Region rdb{dbias, 1, D * 4, D * 4, "dbias"}, rdhi{dh_in, b, D * 4, D * 4, "dh_in"};
     const Region rcu{cu_seqlens, packed ? b + 1 : 0, 4, 4, "cu_seqlens"};
-    const Region rws{workspace, 1, (int64_t)p.bwd_bytes, (int64_t)p.bwd_bytes, "workspace"};
+    const Region rws{workspace, 1, (int64_t)p.bytes, (int64_t)p.bytes, "workspace"};
     for (const Region* r : {&rg, &rx, &rdy, &rdg, &rdx, &rst}) M3_TRY(check_need(*r));
     for (const Region* r : {&rg, &rx, &rdy, &rdg, &rdx}) M3_TRY(check_aligned(r->p, (size_t)es, r->name));
     for (const Region* r : {&rb, &rhi, &rst, &rdho, &rdb, &rdhi, &rcu}) M3_TRY(check_aligned(r->p, 4, r->name));
-    M3_TRY(check_workspace("m3_gated_scan_backward", workspace, workspace_bytes, p.bwd_bytes));
+    M3_TRY(check_workspace("m3_gated_scan_backward", workspace, workspace_bytes, p.bytes));
     const Region* outs[] = {&rdg, &rdx, &rdb, &rdhi, &rws};
     for (int i = 0; i < 5; ++i) {
         for (const Region* in : {&rg, &rx, &rdy, &rb, &rhi, &rst, &rdho, &rcu}) M3_TRY(check_clash(*outs[i], *in, false));

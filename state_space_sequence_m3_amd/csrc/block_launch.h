@@ -10,10 +10,11 @@
 namespace m3 {
 
 // ---------------------------------------------------------------------------- gated scan
-// A tile is kScanTile tokens x kScanCols channels, one workgroup.  Dense batches of sequences
-// longer than a tile are cut sequence by sequence (`per_seq`); shorter sequences and packed batches
-// are cut along the flat token axis, so a tile can hold many sequences.
-constexpr int kScanTile = 128;
+// A tile is kScanTile* tokens x kScanCols channels, worked on by one workgroup; `states` has a row per
+// block of kScanBlock tokens, whatever the type.  Dense batches of sequences longer than a block are
+// cut sequence by sequence (`per_seq`); shorter ones and packed batches are cut along the flat token
+// axis, so a tile can hold many sequences.
+constexpr int kScanTileBf16 = 128, kScanBwdTileBf16 = 64, kScanTileF32 = 64, kScanBlock = 64;
 constexpr int kScanCols = 128;
 
 struct GatedScanArgs {
@@ -24,7 +25,7 @@ struct GatedScanArgs {
     const float* h_in;
     void* y;
     float* h_out;
-    float* states;          // [nchunks, D] state each tile starts from (forward: out, nullable)
+    float* states;          // [blocks, D] state each block starts from (forward: out, nullable)
     // backward
     const void* dy;
     const float* dh_out;
@@ -32,14 +33,15 @@ struct GatedScanArgs {
     void* dx;
     float* dbias;
     float* dh_in;
-    float* part;            // [nchunks, D] each tile's share of dbias (nchunks > 1)
+    float* part;            // [ntiles, D] each tile's share of dbias (ntiles > 1)
     int64_t b, L, T;        // sequences; tokens of each (dense); tokens of all
     int64_t D;
     int64_t gate_p, x_p, y_p, dgate_p, dx_p;   // pitches in bytes
-    uint64_t* words;        // [nchunks, ncols * kScanCols] chain words (nchunks > 1)
+    uint64_t* words;        // [ntiles, ncols * kScanCols] chain words (ntiles > 1)
     unsigned* ticket;
-    int64_t nchunks;
-    int64_t seq_chunks;     // tiles per sequence (per_seq)
+    int64_t ntiles;
+    uint32_t seq_tiles;     // tiles, and blocks, per sequence (per_seq)
+    uint32_t seq_blocks;
     int ncols;              // column blocks
     int per_seq;
 };

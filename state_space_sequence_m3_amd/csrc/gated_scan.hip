@@ -11,84 +11,131 @@
 namespace m3 {
 namespace {
 
-constexpr int kWaves = 8;                        // waves per tile
-constexpr int kSteps = kScanTile / kWaves;       // consecutive tokens of one wave
-constexpr int kFwdWavesPerSimd = 4, kBwdWavesPerSimd = 2;
+constexpr int kWaves = 8;   // waves per tile; each holds kSteps consecutive tokens in registers
+template <typename T> constexpr int kFwdSteps = sizeof(T) == 2 ? 16 : 8;
+template <typename T> constexpr int kBwdSteps = sizeof(T) == 2 ? kScanBwdTileBf16 / kWaves : 8;
+constexpr uint32_t kTogether = 4;
+template <typename T> constexpr int kFwdOcc = 4;   // waves per SIMD to leave registers for
+template <typename T> constexpr int kBwdOcc = 4;
+static_assert(kWaves * kFwdSteps<bf16> == kScanTileBf16 && kWaves * kFwdSteps<float> == kScanTileF32 &&
+              kWaves * kBwdSteps<float> == kScanTileF32,
+              "tile heights of block_launch.h");
 
-// z = sigmoid(u) and 1 - z, each to a few units in its last place: the smaller one is e^-|u| / (1 + e^-|u|),
-// not a difference from 1.  fp32 io carries the rounding of u log2(e) along; with bf16 io the
-// logit's own rounding is larger than that.
+// z = sigmoid(u) and keep = 1 - z, both to a few units in their last place: with e = e^-|u| the larger of
+// the two is 1 / (1 + e) and the smaller one e / (1 + e), never a difference from 1.  The logit comes
+// in parts, gate + bias, since with bf16 gates u log2(e) is one fused multiply-add (the gate's own
+// rounding is larger than that one's); fp32 carries the rounding of u log2(e) along.
+constexpr float kLog2eLo = 1.925963033500e-8f;   // log2(e) - kLog2e
 template <typename T>
-__device__ __forceinline__ void gate_of(float u, float& z, float& keep) {
-    const float m = -fabsf(u);
-    const float t = m * kLog2e;
-    float e = fast_exp2(t);
-    if constexpr (sizeof(T) == 4) {
-        const float lo = fmaf(m, kLog2e, -t) + m * 1.925963033500e-8f;   // log2(e) - kLog2e
-        e = fmaf(e, lo * 0.6931471805599453f, e);
-        e = t < -126.f ? fast_exp2(t) : e;
+__device__ __forceinline__ float gate_exp(float g, float bias, bool& up) {
+    if constexpr (sizeof(T) == 2) {
+        const float t = fmaf(g, kLog2e, bias * kLog2e);
+        up = t >= 0.f;
+        return fast_exp2(-fabsf(t));
+    } else {
+        const float u = g + bias, m = -fabsf(u), t = m * kLog2e;
+        const float e = fast_exp2(t), lo = fmaf(m, kLog2e, -t) + m * kLog2eLo;
+        up = u >= 0.f;
+        return t < -126.f ? e : fmaf(e, lo * 0.6931471805599453f, e);
     }
-    const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
-    z = u >= 0.f ? big : small;
-    keep = u >= 0.f ? small : big;
 }
-
-// Two channels of one token per lane.  VEC: neighbours 2 lane, 2 lane + 1 in one load; else
-// lane and lane + 64, element by element.
+template <typename T>
+__device__ __forceinline__ void gate_of(float g, float bias, float& z, float& keep) {
+    bool up;
+    const float e = gate_exp<T>(g, bias, up);
+    const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+    z = up ? big : small;
+    keep = up ? small : big;
+}
+// Two channels of one token per lane.  VEC: neighbours 2 lane, 2 lane + 1 in one access; else lane and
+// lane + 64, element by element.  Rows are addressed through a descriptor of the tile's first row, a
+// lane's byte offset in the row and the row's scalar offset: no vector arithmetic, and a lane offset of
+// kNowhere (beyond the descriptor's 2^31 bytes) reads zero and stores nothing.
+constexpr uint32_t kNowhere = 0xfffffff0u;
+__device__ __forceinline__ rsrc_t rows_at(const void* base, int64_t bytes) {
+    return make_rsrc((const char*)base + bytes, 0x80000000u);
+}
 template <typename T, bool VEC> struct Pair;
 template <> struct Pair<float, true> {
-    float2 v;
-    __device__ __forceinline__ void load(const char* row, uint32_t o0, uint32_t) { v = *(const float2*)(row + o0); }
-    __device__ __forceinline__ float get(int i) const { return i ? v.y : v.x; }
+    u32x2 v;
+    __device__ __forceinline__ void zero() { v = (u32x2){0, 0}; }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t o0, uint32_t, int row) {
+        v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)o0, row, 0);
+    }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v.y : v.x); }
 };
 template <> struct Pair<bf16, true> {
     uint32_t v;
-    __device__ __forceinline__ void load(const char* row, uint32_t o0, uint32_t) { v = *(const uint32_t*)(row + o0); }
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t o0, uint32_t, int row) {
+        v = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o0, row, 0);
+    }
     __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
 };
 template <> struct Pair<float, false> {
-    float v[2];
-    __device__ __forceinline__ void load(const char* row, uint32_t o0, uint32_t o1) {
-        v[0] = *(const float*)(row + o0);
-        v[1] = *(const float*)(row + o1);
+    uint32_t v[2];
+    __device__ __forceinline__ void zero() { v[0] = v[1] = 0; }
+    __device__ __forceinline__ void hide() {
+        asm volatile("" : "+v"(v[0]));
+        asm volatile("" : "+v"(v[1]));
     }
-    __device__ __forceinline__ float get(int i) const { return v[i]; }
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t o0, uint32_t o1, int row) {
+        v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o0, row, 0);
+        v[1] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o1, row, 0);
+    }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(v[i]); }
 };
 template <> struct Pair<bf16, false> {
     uint16_t v[2];
-    __device__ __forceinline__ void load(const char* row, uint32_t o0, uint32_t o1) {
-        v[0] = *(const uint16_t*)(row + o0);
-        v[1] = *(const uint16_t*)(row + o1);
+    __device__ __forceinline__ void zero() { v[0] = v[1] = 0; }
+    __device__ __forceinline__ void hide() {
+        asm volatile("" : "+v"(v[0]));
+        asm volatile("" : "+v"(v[1]));
+    }
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t o0, uint32_t o1, int row) {
+        v[0] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)o0, row, 0);
+        v[1] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)o1, row, 0);
     }
     __device__ __forceinline__ float get(int i) const { return __uint_as_float((uint32_t)v[i] << 16); }
 };
 
+// Makes the compiler unpack rows again from here on, where it would carry the elements in registers.
+template <int N, typename T, bool VEC>
+__device__ __forceinline__ void forget(Pair<T, VEC> (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i].hide();
+}
+
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_pair(char* row, uint32_t o0, uint32_t o1, bool ok0, bool ok1, float v0, float v1) {
-    if constexpr (VEC) {
-        if (ok0) {
-            if constexpr (sizeof(T) == 4) *(float2*)(row + o0) = make_float2(v0, v1);
-            else *(uint32_t*)(row + o0) = pack_bf16x2(v0, v1);
-        }
+__device__ __forceinline__ void store_pair(rsrc_t r, uint32_t o0, uint32_t o1, int row, float v0, float v1) {
+    if constexpr (VEC && sizeof(T) == 2) {
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(v0, v1), r, (int)o0, row, 0);
+    } else if constexpr (VEC) {
+        __builtin_amdgcn_raw_buffer_store_b64((u32x2){__float_as_uint(v0), __float_as_uint(v1)}, r, (int)o0, row, 0);
+    } else if constexpr (sizeof(T) == 2) {
+        __builtin_amdgcn_raw_buffer_store_b16(bf16_bits_rne(v0), r, (int)o0, row, 0);
+        __builtin_amdgcn_raw_buffer_store_b16(bf16_bits_rne(v1), r, (int)o1, row, 0);
     } else {
-        if (ok0) *(T*)(row + o0) = from_f32<T>(v0);
-        if (ok1) *(T*)(row + o1) = from_f32<T>(v1);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v0), r, (int)o0, row, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v1), r, (int)o1, row, 0);
     }
 }
 
 // Where a lane's two channels are.
 template <typename T, bool VEC>
 struct Cols {
-    int64_t d[2];       // channels, possibly past D
+    int d[2];           // channels, possibly past D
     bool ok[2];
-    uint32_t off[2];    // byte offsets in a row, clamped into it (lanes past D read valid data)
+    uint32_t off[2];    // byte offsets in a row, kNowhere past D
     __device__ __forceinline__ Cols(int col, int lane, int64_t D) {
-        d[0] = (int64_t)col * kScanCols + (VEC ? 2 * lane : lane);
+        d[0] = col * kScanCols + (VEC ? 2 * lane : lane);
         d[1] = d[0] + (VEC ? 1 : 64);
+#pragma unroll
         for (int v = 0; v < 2; ++v) {
             ok[v] = d[v] < D;
-            const int64_t last = VEC ? D - 2 + v : D - 1;
-            off[v] = (uint32_t)((d[v] < last ? d[v] : last) * (int64_t)sizeof(T));
+            off[v] = ok[v] ? (uint32_t)d[v] * (uint32_t)sizeof(T) : kNowhere;
         }
     }
 };
@@ -113,57 +160,60 @@ __device__ __forceinline__ int64_t seq_of(const GatedScanArgs& a, int64_t t) {
     return lo;
 }
 
-// A tile's place: tokens [t0, t0 + nv), its neighbours in the chain, and its row of `states`.
+// A tile's place: tokens [t0, t0 + nv) of sequence seq (FLAT: of any), its number, and the tiles of the
+// same chain before and after it.
 struct Tile {
-    int64_t t0, prev, next, row;
-    uint32_t links_before, links_after;   // tiles of the same chain
+    int64_t t0;
+    uint32_t c, seq, before, after;
+    int link;        // the number of the tile after it in its chain is c + link
     int nv;
 };
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
-    return (int64_t)(((uint64_t)hi << 32) | lo);
-}
 __device__ __forceinline__ uint32_t uniform32(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
+template <int TILE, bool FLAT>
 __device__ __forceinline__ Tile tile_of(const GatedScanArgs& a, uint32_t c) {
     Tile t;
-    if (a.per_seq) {
-        // tiles in the order (place in the sequence, sequence): the tiles that run at the same time
-        // belong to as many sequences as there are, and a chain link waits less
-        const uint32_t b = (uint32_t)a.b, j = uniform32(c / b), s = c - j * b, n = (uint32_t)a.seq_chunks;
-        t.t0 = (int64_t)s * a.L + (int64_t)j * kScanTile;
-        const int64_t left = a.L - (int64_t)j * kScanTile;
-        t.nv = (int)(left < kScanTile ? left : kScanTile);
-        t.prev = j > 0 ? (int64_t)c - b : -1;
-        t.next = j + 1 < n ? (int64_t)c + b : -1;
-        t.links_before = j;
-        t.links_after = n - 1 - j;
-        t.row = (int64_t)s * n + j;
+    t.c = c;
+    int64_t left;
+    if constexpr (!FLAT) {
+        // kTogether sequences side by side, tile by tile, then the next ones: of the tiles that run at the
+        // same time fewer belong to one chain.
+        const uint32_t n = a.seq_tiles, group = uniform32(c / (kTogether * n)), r = c - group * (kTogether * n);
+        const uint32_t left_over = (uint32_t)a.b - group * kTogether, size = left_over < kTogether ? left_over : kTogether;
+        const uint32_t j = uniform32(r / size);
+        t.seq = group * kTogether + (r - j * size);
+        t.link = (int)size;
+        t.t0 = (int64_t)t.seq * a.L + (int64_t)j * TILE;
+        left = a.L - (int64_t)j * TILE;
+        t.before = j;
+        t.after = a.seq_tiles - 1 - j;
     } else {
-        const int64_t total = a.cu ? seq_start(a, a.b) : a.T;
-        t.t0 = (int64_t)c * kScanTile;
-        const int64_t left = total - t.t0;
-        t.nv = (int)(left < 0 ? 0 : (left < kScanTile ? left : kScanTile));
-        t.prev = (int64_t)c - 1;
-        t.next = (int64_t)c + 1 < a.nchunks ? (int64_t)c + 1 : -1;
-        t.links_before = c;
-        t.links_after = (uint32_t)a.nchunks - 1 - c;
-        t.row = c;
+        t.seq = 0;
+        t.link = 1;
+        t.t0 = (int64_t)c * TILE;
+        left = (a.cu ? seq_start(a, a.b) : a.T) - t.t0;
+        t.before = c;
+        t.after = (uint32_t)a.ntiles - 1 - c;
     }
+    t.nv = (int)(left < 0 ? 0 : (left < TILE ? left : TILE));
     return t;
 }
+// the row of `states` that token 0 of the tile starts from
+template <int TILE, bool FLAT>
+__device__ __forceinline__ uint32_t state_row(const GatedScanArgs& a, const Tile& t) {
+    return (FLAT ? 0 : t.seq * a.seq_blocks) + t.before * (TILE / kScanBlock);
+}
 
-// Which tokens of a tile start or end a sequence.  A tile of one long sequence (per_seq) knows by its
-// place; else one thread per token looks its sequence up, and all threads must come here.
+// FLAT: which tokens of a tile start or end a sequence.  One thread per token looks its sequence up.
+template <int TILE>
 struct Marks {
-    int seq[kScanTile];                          // the sequence of each token
-    uint64_t starts[kScanTile / 64], ends[kScanTile / 64];
+    int seq[TILE];                                     // the sequence of each token
+    uint64_t starts[(TILE + 63) / 64], ends[(TILE + 63) / 64];
 };
-__device__ __forceinline__ void find_marks(const GatedScanArgs& a, const Tile& tile, Marks& m) {
-    if (a.per_seq) return;
+template <int TILE>
+__device__ __forceinline__ void find_marks(const GatedScanArgs& a, const Tile& tile, Marks<TILE>& m) {
     const int i = threadIdx.x;
-    if (i < kScanTile) {
+    if (i < TILE) {
         bool start = false, end = false;
         if (i < tile.nv) {
             const int64_t t = tile.t0 + i, s = seq_of(a, t);
@@ -179,22 +229,13 @@ __device__ __forceinline__ void find_marks(const GatedScanArgs& a, const Tile& t
     }
     __syncthreads();
 }
-// the kSteps tokens of wave w, as bits
-__device__ __forceinline__ uint32_t wave_starts(const GatedScanArgs& a, const Tile& tile, const Marks& m, int w) {
-    if (a.per_seq) return w == 0 && tile.prev < 0 ? 1u : 0u;
-    return uniform32((uint32_t)(m.starts[w * kSteps / 64] >> (w * kSteps % 64))) & ((1u << kSteps) - 1);
+// N of a mask's bits, from token i of the tile on
+template <int N>
+__device__ __forceinline__ uint32_t mark_bits(const uint64_t* m, int i) {
+    return uniform32((uint32_t)(m[i / 64] >> (i % 64))) & ((1u << N) - 1);
 }
-__device__ __forceinline__ uint32_t wave_ends(const GatedScanArgs& a, const Tile& tile, const Marks& m, int w) {
-    if (a.per_seq) {
-        const int last = tile.nv - 1 - w * kSteps;
-        return tile.next < 0 && last >= 0 && last < kSteps ? 1u << last : 0u;
-    }
-    return uniform32((uint32_t)(m.ends[w * kSteps / 64] >> (w * kSteps % 64))) & ((1u << kSteps) - 1);
-}
-// the sequence of token i of wave w (a start or an end)
-__device__ __forceinline__ int64_t mark_seq(const GatedScanArgs& a, const Tile& tile, const Marks& m, int w, int i) {
-    return a.per_seq ? tile.row / a.seq_chunks : (int64_t)uniform32((uint32_t)m.seq[w * kSteps + i]);
-}
+template <int TILE>
+__device__ __forceinline__ int64_t mark_seq(const Marks<TILE>& m, int i) { return uniform32((uint32_t)m.seq[i]); }
 
 // ------------------------------------------------------------------------------ chain words
 // Tiles of one sequence are chained through 64-bit words, one per tile and channel, each written
@@ -215,7 +256,6 @@ __device__ __forceinline__ uint64_t get_word(const uint64_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-constexpr int kWindow = 4;            // words looked at together
 constexpr int kMaxPolls = 1 << 22;    // some seconds: a wait that long means a workspace in use twice
 
 // The state that enters a tile whose neighbour in the chain is `first`, the one after that
@@ -225,16 +265,17 @@ constexpr int kMaxPolls = 1 << 22;    // some seconds: a wait that long means a 
 // chain order, so every tile waited for here is held by a workgroup that runs (or is done) and
 // itself waits for earlier ones only; the first tile of a chain waits for none.  A wait that
 // outlasts kMaxPolls gives NaN.
+template <int kWindow>   // words looked at together
 __device__ __forceinline__ void chain_wait(const uint64_t* words, int64_t stride, int64_t first, int64_t step,
-                                           uint32_t links, const int64_t (&d)[2], float (&carry)[2]) {
+                                           uint32_t links, const int (&d)[2], float (&carry)[2]) {
     for (int poll = 0; poll < kMaxPolls; ++poll) {
         uint64_t w[kWindow][2];
 #pragma unroll
         for (int k = 0; k < kWindow; ++k) {
             if ((uint32_t)k < links) {
-                const uint64_t* row = words + (first + k * step) * stride;
-                w[k][0] = get_word(row + d[0]);
-                w[k][1] = get_word(row + d[1]);
+                const char* row = (const char*)(words + (first + k * step) * stride);
+                w[k][0] = get_word((const uint64_t*)(row + (uint32_t)d[0] * 8u));
+                w[k][1] = get_word((const uint64_t*)(row + (uint32_t)d[1] * 8u));
             } else {
                 w[k][0] = w[k][1] = ~0ull;
             }
@@ -268,107 +309,131 @@ __global__ __launch_bounds__(256) void chain_reset_kernel(uint4* words, int64_t 
 }
 
 // ---------------------------------------------------------------------------------- forward
-// The tile a workgroup works on, and its columns: the workgroup's place in the grid, or, where tiles
-// wait for each other, a number from a counter, so that tiles start in chain order.
+// The number of a workgroup's tile and column: its place in the grid, or, where tiles wait for each
+// other, from a counter, so that tiles are begun in chain order whatever order workgroups start in.
+// The lowest tile that is not done is then always held by a workgroup that waits for nothing.
 __device__ __forceinline__ bool take_item(const GatedScanArgs& a, unsigned& s_ticket, uint32_t& c, int& col) {
     uint32_t item = blockIdx.x;
-    if (a.nchunks > 1) {
+    if (a.ntiles > 1) {
         if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u);
         __syncthreads();
         item = uniform32(s_ticket);
-        if (item >= (uint32_t)a.nchunks * (uint32_t)a.ncols) return false;
+        if (item >= (uint32_t)a.ntiles * (uint32_t)a.ncols) return false;
     }
     c = uniform32(item / (uint32_t)a.ncols);
     col = (int)(item - c * (uint32_t)a.ncols);
     return true;
 }
 
+// N rows of pitch `pitch`, of which nv exist: rows past the last one read the last one again.
+template <int N, typename T, bool VEC>
+__device__ __forceinline__ void load_rows(Pair<T, VEC> (&r)[N], rsrc_t base, int pitch, int nv,
+                                          const Cols<T, VEC>& cols) {
+    int row = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        r[i].load(base, cols.off[0], cols.off[1], row);
+        row += i + 1 < nv ? pitch : 0;
+    }
+}
+__device__ __forceinline__ int clamp_rows(int left, int n) { return left < 0 ? 0 : (left < n ? left : n); }
+
+// the values of sequence seq in a [b, D] tensor, 0 without one
 template <typename T, bool VEC>
-__global__ __launch_bounds__(kWaves * 64, kFwdWavesPerSimd) void gated_scan_kernel(const GatedScanArgs a) {
+__device__ __forceinline__ void from_seq(const float* p, int64_t seq, int64_t D, const Cols<T, VEC>& cols, float (&o)[2]) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) o[v] = p && cols.ok[v] ? p[seq * D + cols.d[v]] : 0.f;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void to_seq(float* p, int64_t seq, int64_t D, const Cols<T, VEC>& cols, const float (&o)[2]) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+        if (cols.ok[v]) p[seq * D + cols.d[v]] = o[v];
+}
+// empty sequences pass `from` (0 without one) through to `to`
+template <typename T, bool VEC>
+__device__ __forceinline__ void pass_empty(const GatedScanArgs& a, uint32_t c, const Cols<T, VEC>& cols, const float* from,
+                                           float* to) {
+    if (a.cu == nullptr && a.L != 0) return;
+    for (int64_t s = c; s < a.b; s += a.ntiles) {
+        if (seq_start(a, s + 1) > seq_start(a, s)) continue;
+        float v[2];
+        from_seq(from, s, a.D, cols, v);
+        to_seq(to, s, a.D, cols, v);
+    }
+}
+
+template <typename T, bool VEC, bool FLAT>
+__global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(const GatedScanArgs a) {
+    constexpr int N = kFwdSteps<T>, TILE = kWaves * N;
     __shared__ float2 sA[kWaves][64], sB[kWaves][64], sCarry[64];
     __shared__ int sHard[kWaves];   // bit 0: the wave's tokens hold a sequence start; bit 1: its first token is one
-    __shared__ Marks sMarks;
+    __shared__ Marks<FLAT ? TILE : 1> marks;
     __shared__ unsigned sTicket;
     const int lane = threadIdx.x & 63;
     const int w = uniform32(threadIdx.x >> 6);
     uint32_t c;
     int col;
     if (!take_item(a, sTicket, c, col)) return;
-    const Tile tile = tile_of(a, c);
+    const Tile tile = tile_of<TILE, FLAT>(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
-    const int64_t tw = tile.t0 + w * kSteps;
-    const int left = tile.nv - w * kSteps;
-    const int nv = left < 0 ? 0 : (left < kSteps ? left : kSteps);
-
-    // rows past the last one are read as the last one again, and do nothing
-    Pair<T, VEC> rg[kSteps], rx[kSteps];
-    if (nv > 0) {
-        const char* gp = (const char*)a.gate + tw * a.gate_p;
-        const char* xp = (const char*)a.x + tw * a.x_p;
+    const int64_t tw = tile.t0 + w * N;
+    const int nv = clamp_rows(tile.nv - w * N, N);
+    float keep[N][2], add[N][2];               // h <- keep h + add
+    float bias[2];
+    from_seq(a.bias, 0, 0, cols, bias);
+    uint32_t starts = 0, ends = 0;
+    {
+        Pair<T, VEC> g[N], x[N];
+        if (nv > 0) {
+            load_rows(g, rows_at(a.gate, tw * a.gate_p), (int)a.gate_p, nv, cols);
+            load_rows(x, rows_at(a.x, tw * a.x_p), (int)a.x_p, nv, cols);
+        }
+        if constexpr (FLAT) {
+            find_marks(a, tile, marks);
+            starts = mark_bits<N>(marks.starts, w * N);
+            ends = mark_bits<N>(marks.ends, w * N);
+        } else {                               // a sequence's first and last token
+            if (w == 0 && tile.before == 0) starts = 1;
+            if (tile.after == 0 && nv > 0 && w * N + nv == tile.nv) ends = 1u << (nv - 1);
+        }
+        if (nv > 0) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            rg[i].load(gp, cols.off[0], cols.off[1]);
-            rx[i].load(xp, cols.off[0], cols.off[1]);
-            gp += i + 1 < nv ? a.gate_p : 0;
-            xp += i + 1 < nv ? a.x_p : 0;
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    float z;
+                    gate_of<T>(g[i].get(v), bias[v], z, keep[i][v]);
+                    add[i][v] = z * x[i].get(v);
+                }
         }
     }
-    float bias[2] = {0.f, 0.f};
-    if (a.bias) {
-        bias[0] = a.bias[cols.off[0] / sizeof(T)];
-        bias[1] = a.bias[cols.off[1] / sizeof(T)];
-    }
-    find_marks(a, tile, sMarks);
-    const uint32_t starts = wave_starts(a, tile, sMarks, w);
-    float keep[kSteps][2], add[kSteps][2];
-    float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};   // the wave's map
-    if (nv > 0) {
+    if (nv < N) {                              // tokens that are not there: keep = 1, nothing added
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                float z;
-                gate_of<T>(rg[i].get(v) + bias[v], z, keep[i][v]);
-                add[i][v] = z * rx[i].get(v);
-            }
-    }
-    if (nv < kSteps) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < N; ++i)
             if (i >= nv) {
                 keep[i][0] = keep[i][1] = 1.f;
                 add[i][0] = add[i][1] = 0.f;
             }
     }
-    if (starts == 0) {
+    auto seq_at = [&](int i) -> int64_t {
+        if constexpr (FLAT) return mark_seq(marks, w * N + i);
+        else return tile.seq;
+    };
+    float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};   // the wave's map
+    auto step = [&](int i, float (&h)[2]) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i)
+        for (int v = 0; v < 2; ++v) h[v] = fmaf(keep[i][v], h[v], add[i][v]);
+    };
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                A[v] *= keep[i][v];
-                B[v] = fmaf(keep[i][v], B[v], add[i][v]);
-            }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            if ((starts >> i) & 1) {
-                if (a.h_in) {
-                    const float* h = a.h_in + mark_seq(a, tile, sMarks, w, i) * a.D;
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-                        if (cols.ok[v]) add[i][v] = fmaf(keep[i][v], h[cols.d[v]], add[i][v]);
-                }
-                A[0] = A[1] = 0.f;
-                B[0] = add[i][0];
-                B[1] = add[i][1];
-            } else {
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    A[v] *= keep[i][v];
-                    B[v] = fmaf(keep[i][v], B[v], add[i][v]);
-                }
-            }
+    for (int i = 0; i < N; ++i) {
+        if ((FLAT || i == 0) && ((starts >> i) & 1)) {
+            A[0] = A[1] = 0.f;
+            from_seq(a.h_in, seq_at(i), a.D, cols, B);
         }
+        A[0] *= keep[i][0];
+        A[1] *= keep[i][1];
+        step(i, B);
     }
     sA[w][lane] = make_float2(A[0], A[1]);
     sB[w][lane] = make_float2(B[0], B[1]);
@@ -376,7 +441,7 @@ __global__ __launch_bounds__(kWaves * 64, kFwdWavesPerSimd) void gated_scan_kern
     __syncthreads();
     // the map of the waves before this one
     float Ap[2] = {1.f, 1.f}, Bp[2] = {0.f, 0.f};
-    bool hard = false;
+    bool hard = false;                         // a start among them: what came before does not matter
     auto compose = [&](int k) {
         const float2 A = sA[k][lane], B = sB[k][lane];
         if (uniform32(sHard[k]) & 1) {
@@ -391,31 +456,29 @@ __global__ __launch_bounds__(kWaves * 64, kFwdWavesPerSimd) void gated_scan_kern
             Bp[1] = fmaf(A.y, Bp[1], B.y);
         }
     };
+#pragma unroll 2
     for (int k = 0; k < w; ++k) compose(k);
-    float carry[2] = {0.f, 0.f};
-    if (w == kWaves - 1) {
+    if (w == kWaves - 1) {                     // the last one does the chaining
         const float A0[2] = {Ap[0], Ap[1]}, B0[2] = {Bp[0], Bp[1]};
         const bool hard0 = hard;
+        float carry[2] = {0.f, 0.f};
         compose(w);
-        if (a.nchunks > 1) {
+        if (a.ntiles > 1) {
             const int64_t stride = (int64_t)a.ncols * kScanCols;
             uint64_t* mine = a.words + c * stride;
 #pragma unroll
             for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], hard ? final_word(Bp[v]) : map_word(Ap[v], Bp[v]));
             const bool starts_here = (uniform32(sHard[0]) & 2) != 0;
-            if (tile.prev >= 0 && tile.nv > 0 && !starts_here)
-                chain_wait(a.words, stride, tile.prev, a.per_seq ? -a.b : -1, tile.links_before, cols.d, carry);
+            if (tile.before > 0 && tile.nv > 0 && !starts_here) {
+                const int64_t step = -tile.link;
+                chain_wait<sizeof(T) == 2 ? 4 : 8>(a.words, stride, c + step, step, tile.before, cols.d, carry);
+            }
             if (!hard) {
 #pragma unroll
                 for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], final_word(fmaf(Ap[v], carry[v], Bp[v])));
             }
         }
         sCarry[lane] = make_float2(carry[0], carry[1]);
-        if (a.states) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-                if (cols.ok[v]) a.states[tile.row * a.D + cols.d[v]] = carry[v];
-        }
         Ap[0] = A0[0]; Ap[1] = A0[1];
         Bp[0] = B0[0]; Bp[1] = B0[1];
         hard = hard0;
@@ -427,167 +490,139 @@ __global__ __launch_bounds__(kWaves * 64, kFwdWavesPerSimd) void gated_scan_kern
         h[0] = hard ? Bp[0] : fmaf(Ap[0], cy.x, Bp[0]);
         h[1] = hard ? Bp[1] : fmaf(Ap[1], cy.y, Bp[1]);
     }
-    const uint32_t ends = wave_ends(a, tile, sMarks, w);
-    char* yp = (char*)a.y + tw * a.y_p;
-    if (nv == kSteps && (starts | ends) == 0) {
+    if (a.states && nv > 0 && w * N % kScanBlock == 0)
+        to_seq(a.states, (int64_t)state_row<TILE, FLAT>(a, tile) + w * N / kScanBlock, a.D, cols, h);
+    const rsrc_t yr = rows_at(a.y, tw * a.y_p);
+    int row = 0;
+    if (nv == N && (starts | ends) == 0) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) h[v] = fmaf(keep[i][v], h[v], add[i][v]);
-            store_pair<T, VEC>(yp, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], h[0], h[1]);
-            yp += a.y_p;
+        for (int i = 0; i < N; ++i) {
+            step(i, h);
+            store_pair<T, VEC>(yr, cols.off[0], cols.off[1], row, h[0], h[1]);
+            row += (int)a.y_p;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
+        for (int i = 0; i < N; ++i) {
             if (i < nv) {
-                if ((starts >> i) & 1) h[0] = h[1] = 0.f;   // and the carried state is in add
-#pragma unroll
-                for (int v = 0; v < 2; ++v) h[v] = fmaf(keep[i][v], h[v], add[i][v]);
-                store_pair<T, VEC>(yp, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], h[0], h[1]);
-                yp += a.y_p;
-                if ((ends >> i) & 1) {
-                    float* o = a.h_out + mark_seq(a, tile, sMarks, w, i) * a.D;
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-                        if (cols.ok[v]) o[cols.d[v]] = h[v];
-                }
+                if ((starts >> i) & 1) from_seq(a.h_in, seq_at(i), a.D, cols, h);
+                step(i, h);
+                store_pair<T, VEC>(yr, cols.off[0], cols.off[1], row, h[0], h[1]);
+                row += (int)a.y_p;
+                if ((ends >> i) & 1) to_seq(a.h_out, seq_at(i), a.D, cols, h);
             }
         }
     }
-    // empty sequences: the carried state passes through
-    if (w == 0 && (a.cu != nullptr || a.L == 0)) {
-        for (int64_t s = c; s < a.b; s += a.nchunks) {
-            if (seq_start(a, s + 1) > seq_start(a, s)) continue;
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-                if (cols.ok[v]) a.h_out[s * a.D + cols.d[v]] = a.h_in ? a.h_in[s * a.D + cols.d[v]] : 0.f;
-        }
-    }
+    if (FLAT && w == 0) pass_empty(a, c, cols, a.h_in, a.h_out);
 }
 
 // --------------------------------------------------------------------------------- backward
 // With G_t = (1 - z_t) l_t, what flows from token t to h_{t-1}: l_t = dy_t + G_{t+1}, so backwards
 // G_t = keep_t G_{t+1} + keep_t dy_t, an affine map again, and the same chain in the other
 // direction.  A sequence's last token takes dh_out for G_{t+1}.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(kWaves * 64, kBwdWavesPerSimd) void gated_scan_backward_kernel(const GatedScanArgs a) {
+template <typename T, bool VEC, bool FLAT>
+__global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_kernel(const GatedScanArgs a) {
+    constexpr int N = kBwdSteps<T>, TILE = kWaves * N;
     __shared__ float2 sA[kWaves][64], sB[kWaves][64], sRA[kWaves][64], sRB[kWaves][64], sCarry[64];
     __shared__ int sHard[kWaves];   // bit 0: holds a sequence start; 1: holds an end; 2: its last token is an end
-    __shared__ Marks sMarks;
+    __shared__ Marks<FLAT ? TILE : 1> marks;
     __shared__ unsigned sTicket;
     const int lane = threadIdx.x & 63;
     const int w = uniform32(threadIdx.x >> 6);
     uint32_t c;
     int col;
     if (!take_item(a, sTicket, c, col)) return;
-    c = (uint32_t)a.nchunks - 1 - c;   // from the last tile to the first
-    const Tile tile = tile_of(a, c);
+    c = (uint32_t)a.ntiles - 1 - c;            // from the last tile to the first
+    const Tile tile = tile_of<TILE, FLAT>(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
-    const int64_t tw = tile.t0 + w * kSteps;
-    const int left = tile.nv - w * kSteps;
-    const int nv = left < 0 ? 0 : (left < kSteps ? left : kSteps);
-
-    Pair<T, VEC> rg[kSteps], rx[kSteps], rd[kSteps];
-    if (nv > 0) {
-        const char* gp = (const char*)a.gate + tw * a.gate_p;
-        const char* xp = (const char*)a.x + tw * a.x_p;
-        const char* dp = (const char*)a.dy + tw * a.y_p;
+    const int64_t tw = tile.t0 + w * N;
+    const int nv = clamp_rows(tile.nv - w * N, N);
+    Pair<T, VEC> x[N], dy[N];
+    float z[N][2], keep[N][2];
+    float bias[2], h[2];
+    from_seq(a.bias, 0, 0, cols, bias);
+    from_seq(a.states, state_row<TILE, FLAT>(a, tile), a.D, cols, h);
+    uint32_t starts = 0, ends = 0;
+    {
+        Pair<T, VEC> g[N];
+        if (nv > 0) {
+            load_rows(g, rows_at(a.gate, tw * a.gate_p), (int)a.gate_p, nv, cols);
+            load_rows(x, rows_at(a.x, tw * a.x_p), (int)a.x_p, nv, cols);
+            load_rows(dy, rows_at(a.dy, tw * a.y_p), (int)a.y_p, nv, cols);
+        }
+        if constexpr (FLAT) {
+            find_marks(a, tile, marks);
+            starts = mark_bits<N>(marks.starts, w * N);
+            ends = mark_bits<N>(marks.ends, w * N);
+        } else {                               // a sequence's first and last token
+            if (w == 0 && tile.before == 0) starts = 1;
+            if (tile.after == 0 && nv > 0 && w * N + nv == tile.nv) ends = 1u << (nv - 1);
+        }
+        if (nv > 0) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            rg[i].load(gp, cols.off[0], cols.off[1]);
-            rx[i].load(xp, cols.off[0], cols.off[1]);
-            rd[i].load(dp, cols.off[0], cols.off[1]);
-            gp += i + 1 < nv ? a.gate_p : 0;
-            xp += i + 1 < nv ? a.x_p : 0;
-            dp += i + 1 < nv ? a.y_p : 0;
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) gate_of<T>(g[i].get(v), bias[v], z[i][v], keep[i][v]);
         }
     }
-    float h[2], bias[2] = {0.f, 0.f};
+    if (nv < N) {                              // tokens that are not there: keep = 1, nothing added
 #pragma unroll
-    for (int v = 0; v < 2; ++v) h[v] = cols.ok[v] ? a.states[tile.row * a.D + cols.d[v]] : 0.f;
-    if (a.bias) {
-        bias[0] = a.bias[cols.off[0] / sizeof(T)];
-        bias[1] = a.bias[cols.off[1] / sizeof(T)];
-    }
-    find_marks(a, tile, sMarks);
-    const uint32_t starts = wave_starts(a, tile, sMarks, w), ends = wave_ends(a, tile, sMarks, w);
-
-    float z[kSteps][2], keep[kSteps][2], xs[kSteps][2], lam[kSteps][2];   // lam: dy
-    if (nv > 0) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                gate_of<T>(rg[i].get(v) + bias[v], z[i][v], keep[i][v]);
-                xs[i][v] = rx[i].get(v);
-                lam[i][v] = rd[i].get(v);
-            }
-    }
-    if (nv < kSteps) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < N; ++i)
             if (i >= nv) {
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    z[i][v] = 0.f;
-                    keep[i][v] = 1.f;
-                    xs[i][v] = 0.f;
-                    lam[i][v] = 0.f;
-                }
+                z[i][0] = z[i][1] = 0.f;
+                keep[i][0] = keep[i][1] = 1.f;
+                x[i].zero();
+                dy[i].zero();
             }
     }
-    const bool marked = (starts | ends) != 0;
-    if (ends != 0 && a.dh_out) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-            if ((ends >> i) & 1) {
-                const float* d = a.dh_out + mark_seq(a, tile, sMarks, w, i) * a.D;
-#pragma unroll
-                for (int v = 0; v < 2; ++v)
-                    if (cols.ok[v]) lam[i][v] += d[cols.d[v]];
-            }
-    }
+    auto seq_at = [&](int i) -> int64_t {
+        if constexpr (FLAT) return mark_seq(marks, w * N + i);
+        else return tile.seq;
+    };
     {   // the wave's maps, forwards and backwards
         float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f}, RA[2] = {1.f, 1.f}, RB[2] = {0.f, 0.f};
-        if (!marked) {
+        if (starts == 0) {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     A[v] *= keep[i][v];
-                    B[v] = fmaf(keep[i][v], B[v], z[i][v] * xs[i][v]);
+                    B[v] = fmaf(keep[i][v], B[v], z[i][v] * x[i].get(v));
                 }
-            RA[0] = A[0];
-            RA[1] = A[1];
-#pragma unroll
-            for (int i = kSteps - 1; i >= 0; --i)
-#pragma unroll
-                for (int v = 0; v < 2; ++v) RB[v] = keep[i][v] * (RB[v] + lam[i][v]);
         } else {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                if ((starts >> i) & 1) {
-                    A[0] = A[1] = B[0] = B[1] = 0.f;
-                    if (a.h_in) {
-                        const float* hi = a.h_in + mark_seq(a, tile, sMarks, w, i) * a.D;
-#pragma unroll
-                        for (int v = 0; v < 2; ++v) B[v] = cols.ok[v] ? hi[cols.d[v]] : 0.f;
-                    }
+            for (int i = 0; i < N; ++i) {
+                if ((FLAT || i == 0) && ((starts >> i) & 1)) {
+                    A[0] = A[1] = 0.f;
+                    from_seq(a.h_in, seq_at(i), a.D, cols, B);
                 }
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     A[v] *= keep[i][v];
-                    B[v] = fmaf(keep[i][v], B[v], z[i][v] * xs[i][v]);
+                    B[v] = fmaf(keep[i][v], B[v], z[i][v] * x[i].get(v));
                 }
             }
+        }
+        forget(x);
+        if (ends == 0) {
 #pragma unroll
-            for (int i = kSteps - 1; i >= 0; --i) {
-                if ((ends >> i) & 1) RA[0] = RA[1] = RB[0] = RB[1] = 0.f;
+            for (int i = N - 1; i >= 0; --i)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     RA[v] *= keep[i][v];
-                    RB[v] = keep[i][v] * (RB[v] + lam[i][v]);
+                    RB[v] = keep[i][v] * (RB[v] + dy[i].get(v));
+                }
+        } else {
+#pragma unroll
+            for (int i = N - 1; i >= 0; --i) {
+                if ((ends >> i) & 1) {
+                    RA[0] = RA[1] = 0.f;
+                    from_seq(a.dh_out, seq_at(i), a.D, cols, RB);
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    RA[v] *= keep[i][v];
+                    RB[v] = keep[i][v] * (RB[v] + dy[i].get(v));
                 }
             }
         }
@@ -598,14 +633,9 @@ __global__ __launch_bounds__(kWaves * 64, kBwdWavesPerSimd) void gated_scan_back
         if (lane == 0)
             sHard[w] = (starts != 0 ? 1 : 0) | (ends != 0 ? 2 : 0) | (nv > 0 && ((ends >> (nv - 1)) & 1) ? 4 : 0);
     }
+    forget(x);
+    forget(dy);
     __syncthreads();
-    // state that enters this wave
-    for (int k = 0; k < w; ++k) {
-        const float2 A = sA[k][lane], B = sB[k][lane];
-        const bool cut = uniform32(sHard[k]) & 1;
-        h[0] = cut ? B.x : fmaf(A.x, h[0], B.x);
-        h[1] = cut ? B.y : fmaf(A.y, h[1], B.y);
-    }
     // map of the waves after this one, backwards
     float Ap[2] = {1.f, 1.f}, Bp[2] = {0.f, 0.f};
     bool hard = false;
@@ -623,23 +653,26 @@ __global__ __launch_bounds__(kWaves * 64, kBwdWavesPerSimd) void gated_scan_back
             Bp[1] = fmaf(A.y, Bp[1], B.y);
         }
     };
+#pragma unroll 2
     for (int k = kWaves - 1; k > w; --k) compose(k);
-    float carry[2] = {0.f, 0.f};
-    if (w == 0) {
+    if (w == 0) {                              // the first one does the chaining
         const float A0[2] = {Ap[0], Ap[1]}, B0[2] = {Bp[0], Bp[1]};
         const bool hard0 = hard;
+        float carry[2] = {0.f, 0.f};
         compose(0);
-        if (a.nchunks > 1) {
+        if (a.ntiles > 1) {
             const int64_t stride = (int64_t)a.ncols * kScanCols;
             uint64_t* mine = a.words + c * stride;
 #pragma unroll
             for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], hard ? final_word(Bp[v]) : map_word(Ap[v], Bp[v]));
             // nothing enters from behind when the tile's last token ends a sequence, or tokens end here
             int last = 0;
-            for (int k = 0; k < kWaves; ++k) last = tile.nv > k * kSteps ? sHard[k] : last;
+            for (int k = 0; k < kWaves; ++k) last = tile.nv > k * N ? sHard[k] : last;
             const bool ends_here = tile.nv == 0 || (uniform32(last) & 4) != 0;
-            if (tile.next >= 0 && !ends_here)
-                chain_wait(a.words, stride, tile.next, a.per_seq ? a.b : 1, tile.links_after, cols.d, carry);
+            if (tile.after > 0 && !ends_here) {
+                const int64_t step = tile.link;
+                chain_wait<4>(a.words, stride, c + step, step, tile.after, cols.d, carry);
+            }
             if (!hard) {
 #pragma unroll
                 for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], final_word(fmaf(Ap[v], carry[v], Bp[v])));
@@ -650,30 +683,24 @@ __global__ __launch_bounds__(kWaves * 64, kBwdWavesPerSimd) void gated_scan_back
         Bp[0] = B0[0]; Bp[1] = B0[1];
         hard = hard0;
     }
-    // forwards: what dgate is of l_t, in the place of x
-    if (starts == 0) {
+    // state that enters this wave
+#pragma unroll 2
+    for (int k = 0; k < w; ++k) {
+        const float2 A = sA[k][lane], B = sB[k][lane];
+        const bool cut = uniform32(sHard[k]) & 1;
+        h[0] = cut ? B.x : fmaf(A.x, h[0], B.x);
+        h[1] = cut ? B.y : fmaf(A.y, h[1], B.y);
+    }
+    // forwards: what dgate is of l_t
+    float fac[N][2];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i)
+    for (int i = 0; i < N; ++i) {
+        if ((FLAT || i == 0) && ((starts >> i) & 1)) from_seq(a.h_in, seq_at(i), a.D, cols, h);
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const float x = xs[i][v];
-                xs[i][v] = z[i][v] * keep[i][v] * (x - h[v]);
-                h[v] = fmaf(keep[i][v], h[v], z[i][v] * x);
-            }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            if ((starts >> i) & 1) {
-                const float* hi = a.h_in ? a.h_in + mark_seq(a, tile, sMarks, w, i) * a.D : nullptr;
-#pragma unroll
-                for (int v = 0; v < 2; ++v) h[v] = hi && cols.ok[v] ? hi[cols.d[v]] : 0.f;
-            }
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const float x = xs[i][v];
-                xs[i][v] = z[i][v] * keep[i][v] * (x - h[v]);
-                h[v] = fmaf(keep[i][v], h[v], z[i][v] * x);
-            }
+        for (int v = 0; v < 2; ++v) {
+            const float xv = x[i].get(v);
+            fac[i][v] = z[i][v] * keep[i][v] * (xv - h[v]);
+            h[v] = fmaf(keep[i][v], h[v], z[i][v] * xv);
         }
     }
     __syncthreads();
@@ -685,65 +712,51 @@ __global__ __launch_bounds__(kWaves * 64, kBwdWavesPerSimd) void gated_scan_back
     }
     // backwards
     float sum[2] = {0.f, 0.f};
-    char* gp = (char*)a.dgate + (tw + nv - 1) * a.dgate_p;
-    char* xp = (char*)a.dx + (tw + nv - 1) * a.dx_p;
+    const rsrc_t gr = rows_at(a.dgate, tw * a.dgate_p), xr = rows_at(a.dx, tw * a.dx_p);
+    int grow = (nv - 1) * (int)a.dgate_p, xrow = (nv - 1) * (int)a.dx_p;
     auto token = [&](int i) {
         float dg[2], dx[2];
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            const float l = lam[i][v] + G[v];
+            const float l = dy[i].get(v) + G[v];
             dx[v] = z[i][v] * l;
-            dg[v] = xs[i][v] * l;
+            dg[v] = fac[i][v] * l;
             sum[v] += dg[v];
             G[v] = keep[i][v] * l;
         }
-        store_pair<T, VEC>(gp, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], dg[0], dg[1]);
-        store_pair<T, VEC>(xp, cols.off[0], cols.off[1], cols.ok[0], cols.ok[1], dx[0], dx[1]);
-        gp -= a.dgate_p;
-        xp -= a.dx_p;
+        store_pair<T, VEC>(gr, cols.off[0], cols.off[1], grow, dg[0], dg[1]);
+        store_pair<T, VEC>(xr, cols.off[0], cols.off[1], xrow, dx[0], dx[1]);
+        grow -= (int)a.dgate_p;
+        xrow -= (int)a.dx_p;
     };
-    if (nv == kSteps && !marked) {
+    if (nv == N && (starts | ends) == 0) {
 #pragma unroll
-        for (int i = kSteps - 1; i >= 0; --i) token(i);
+        for (int i = N - 1; i >= 0; --i) token(i);
     } else {
 #pragma unroll
-        for (int i = kSteps - 1; i >= 0; --i) {
+        for (int i = N - 1; i >= 0; --i) {
             if (i < nv) {
-                if ((ends >> i) & 1) G[0] = G[1] = 0.f;
+                if ((ends >> i) & 1) from_seq(a.dh_out, seq_at(i), a.D, cols, G);
                 token(i);
-                if (((starts >> i) & 1) && a.dh_in) {
-                    float* o = a.dh_in + mark_seq(a, tile, sMarks, w, i) * a.D;
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-                        if (cols.ok[v]) o[cols.d[v]] = G[v];
-                }
+                if ((FLAT || i == 0) && ((starts >> i) & 1) && a.dh_in) to_seq(a.dh_in, seq_at(i), a.D, cols, G);
             }
         }
     }
     if (a.dbias) {   // the tile's share: waves summed in order
-        sA[w][lane] = make_float2(sum[0], sum[1]);
+        sRA[w][lane] = make_float2(sum[0], sum[1]);
         __syncthreads();
         if (w == 0) {
-            float2 t = sA[0][lane];
+            float2 t = sRA[0][lane];
 #pragma unroll
             for (int k = 1; k < kWaves; ++k) {
-                t.x += sA[k][lane].x;
-                t.y += sA[k][lane].y;
+                t.x += sRA[k][lane].x;
+                t.y += sRA[k][lane].y;
             }
-            float* out = a.nchunks > 1 ? a.part + (int64_t)c * a.D : a.dbias;
-            if (cols.ok[0]) out[cols.d[0]] = t.x;
-            if (cols.ok[1]) out[cols.d[1]] = t.y;
+            const float o[2] = {t.x, t.y};
+            to_seq(a.ntiles > 1 ? a.part : a.dbias, a.ntiles > 1 ? c : 0, a.D, cols, o);
         }
     }
-    // empty sequences: dh_out passes through
-    if (w == 0 && a.dh_in && (a.cu != nullptr || a.L == 0)) {
-        for (int64_t e = c; e < a.b; e += a.nchunks) {
-            if (seq_start(a, e + 1) > seq_start(a, e)) continue;
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-                if (cols.ok[v]) a.dh_in[e * a.D + cols.d[v]] = a.dh_out ? a.dh_out[e * a.D + cols.d[v]] : 0.f;
-        }
-    }
+    if (FLAT && w == 0 && a.dh_in) pass_empty(a, c, cols, a.dh_out, a.dh_in);
 }
 
 // ------------------------------------------------------------------------------- one token
@@ -767,7 +780,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs a, 
 #pragma unroll
     for (int v = 0; v < W; ++v) {
         float z, keep;
-        gate_of<T>(to_f32(g.v[v]) + (a.bias ? a.bias[d + v] : 0.f), z, keep);
+        gate_of<T>(to_f32(g.v[v]), a.bias ? a.bias[d + v] : 0.f, z, keep);
         o.v[v] = fmaf(keep, h.v[v], z * to_f32(x.v[v]));
         y.v[v] = from_f32<T>(o.v[v]);
     }
@@ -802,7 +815,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* part, int
 }
 
 hipError_t reset_chain(const GatedScanArgs& a, hipStream_t s) {
-    const int64_t n16 = a.nchunks * a.ncols * kScanCols / 2;
+    const int64_t n16 = a.ntiles * a.ncols * kScanCols / 2;
     hipLaunchKernelGGL(chain_reset_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, s, (uint4*)a.words, n16,
                        a.ticket);
     return hipGetLastError();
@@ -811,30 +824,40 @@ hipError_t reset_chain(const GatedScanArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_gated_scan(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s) {
-    if (a.nchunks > 1) {
+    if (a.ntiles > 1) {
         const hipError_t e = reset_chain(a, s);
         if (e != hipSuccess) return e;
     }
-    const dim3 grid((unsigned)(a.nchunks * a.ncols)), block(kWaves * 64);
-    if (bf16_io && vec) hipLaunchKernelGGL((gated_scan_kernel<bf16, true>), grid, block, 0, s, a);
-    else if (bf16_io) hipLaunchKernelGGL((gated_scan_kernel<bf16, false>), grid, block, 0, s, a);
-    else if (vec) hipLaunchKernelGGL((gated_scan_kernel<float, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((gated_scan_kernel<float, false>), grid, block, 0, s, a);
+    const dim3 grid((unsigned)(a.ntiles * a.ncols)), block(kWaves * 64);
+    const bool flat = !a.per_seq;
+#define M3_SCAN(T, VEC)                                                                                   \
+    if (flat) hipLaunchKernelGGL((gated_scan_kernel<T, VEC, true>), grid, block, 0, s, a);                \
+    else hipLaunchKernelGGL((gated_scan_kernel<T, VEC, false>), grid, block, 0, s, a)
+    if (bf16_io && vec) { M3_SCAN(bf16, true); }
+    else if (bf16_io) { M3_SCAN(bf16, false); }
+    else if (vec) { M3_SCAN(float, true); }
+    else { M3_SCAN(float, false); }
+#undef M3_SCAN
     return hipGetLastError();
 }
 
 hipError_t launch_gated_scan_backward(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s) {
-    if (a.nchunks > 1) {
+    if (a.ntiles > 1) {
         const hipError_t e = reset_chain(a, s);
         if (e != hipSuccess) return e;
     }
-    const dim3 grid((unsigned)(a.nchunks * a.ncols)), block(kWaves * 64);
-    if (bf16_io && vec) hipLaunchKernelGGL((gated_scan_backward_kernel<bf16, true>), grid, block, 0, s, a);
-    else if (bf16_io) hipLaunchKernelGGL((gated_scan_backward_kernel<bf16, false>), grid, block, 0, s, a);
-    else if (vec) hipLaunchKernelGGL((gated_scan_backward_kernel<float, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((gated_scan_backward_kernel<float, false>), grid, block, 0, s, a);
+    const dim3 grid((unsigned)(a.ntiles * a.ncols)), block(kWaves * 64);
+    const bool flat = !a.per_seq;
+#define M3_SCAN(T, VEC)                                                                                   \
+    if (flat) hipLaunchKernelGGL((gated_scan_backward_kernel<T, VEC, true>), grid, block, 0, s, a);                \
+    else hipLaunchKernelGGL((gated_scan_backward_kernel<T, VEC, false>), grid, block, 0, s, a)
+    if (bf16_io && vec) { M3_SCAN(bf16, true); }
+    else if (bf16_io) { M3_SCAN(bf16, false); }
+    else if (vec) { M3_SCAN(float, true); }
+    else { M3_SCAN(float, false); }
+#undef M3_SCAN
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.dbias && a.nchunks > 1) e = launch_column_sum(a.part, a.nchunks, a.D, a.dbias, s);
+    if (e == hipSuccess && a.dbias && a.ntiles > 1) e = launch_column_sum(a.part, a.ntiles, a.D, a.dbias, s);
     return e;
 }
 

@@ -29,7 +29,7 @@ def scan(gate, x, bias, h_in, lens, dy=None, dh_out=None):
     largest |x|, |h_in|, a step adds an error of at most H ((9 + z (2 |u| + 24)) U32), and an error
     dies away as the product of the keeps: over a run e <- keep e + that.  The tile's maps
     are composed instead of applied in order: 2 more units per composition, of which there are at most 8
-    in a tile and one per tile: 32 + 2 T / 128 units of H, everywhere."""
+    in a tile and one per tile of at least 64 tokens: 32 + 2 T / 64 units of H, everywhere."""
     t_all, d = x.shape
     g64, x64 = gate.double(), x.double()
     u = g64 + (0.0 if bias is None else bias.double())
@@ -39,7 +39,7 @@ def scan(gate, x, bias, h_in, lens, dy=None, dh_out=None):
     top = torch.maximum(x64.abs().amax(0) if t_all else torch.zeros(d, dtype=torch.float64),
                         h0.abs().amax(0) if b else torch.zeros(d, dtype=torch.float64))
     per_step = top * (9 + z * (2 * u.abs() + 24)) * U32
-    flat = top * (32 + 2 * t_all / 128) * U32
+    flat = top * (32 + 2 * t_all / 64) * U32
     prev, h_all, err = torch.zeros(t_all, d).double(), torch.zeros(t_all, d).double(), torch.zeros(t_all, d).double()
     h_out, e_out = h0.clone(), torch.zeros(b, d).double()
     off = offsets(lens)
@@ -66,7 +66,7 @@ def scan(gate, x, bias, h_in, lens, dy=None, dh_out=None):
         for t in reversed(range(off[s], off[s + 1])):
             lam, mag = dy64[t] + G, dy64[t].abs() + size          # mag bounds every |l_t| on the way
             rel = (9 + z[t] * (2 * u[t].abs() + 24)) * U32
-            e_lam = e + mag * (34 + 2 * t_all / 128) * U32
+            e_lam = e + mag * (34 + 2 * t_all / 64) * U32
             dx[t] = z[t] * lam
             tx[t] = z[t] * e_lam + (u[t].abs() + 12) * U32 * z[t] * mag
             f = z[t] * keep[t]
@@ -76,11 +76,11 @@ def scan(gate, x, bias, h_in, lens, dy=None, dh_out=None):
                          (2 * u[t].abs() + 24) * U32 * wide * mag)
             G, size, e = keep[t] * lam, keep[t] * mag, keep[t] * e + rel * mag
         dh_in[s] = G
-        t_in[s] = e + size * (34 + 2 * t_all / 128) * U32
+        t_in[s] = e + size * (34 + 2 * t_all / 64) * U32
     out.update(dx=dx, dgate=dg, dh_in=dh_in, dbias=dg.sum(0))
-    # the sum: 16 additions in a wave, 8 over waves, then T / 128 tiles (64 at a time) and 20 more
+    # the sum: 16 additions in a wave, 8 over waves, then T / 64 tiles (64 at a time) and 20 more
     out["tol"].update(dx=tx, dgate=tg, dh_in=t_in,
-                      dbias=tg.sum(0) + dg.abs().sum(0) * (48 + t_all / 128 / 64) * U32)
+                      dbias=tg.sum(0) + dg.abs().sum(0) * (48 + t_all / 64 / 64) * U32)
     return out
 
 

@@ -203,6 +203,7 @@ def test_pitches_and_sizes():
     assert FWD(dims=scan_dims(batch=big, seqlen=big), cu=0) == m3scan.M3_E_DIMS
     assert FWD(dims=scan_dims(batch=1 << 31)) == m3scan.M3_E_DIMS
     assert FWD(dims=scan_dims(batch=1, seqlen=1 << 30, x_pitch=big)) == m3scan.M3_E_DIMS
+    assert FWD(dims=scan_dims(y_pitch=1 << 23)) == m3scan.M3_E_DIMS and "2^24" in m3scan.last_error()
     assert m3block.load().m3_gated_scan_workspace_bytes(ctypes.byref(scan_dims(batch=big, seqlen=big)), 0) == 0
     assert STEP(dims=scan_dims(seqlen=2)) == m3scan.M3_E_DIMS
     assert NORM(dims=norm_dims(width=16385)) == m3scan.M3_E_UNSUPPORTED
@@ -220,13 +221,20 @@ def test_norm_outputs():
 def test_workspaces():
     lib = m3block.load()
     r = lambda n: (n + 255) // 256 * 256
-    for dims, packed, chunks in ((scan_dims(), 0, 6), (scan_dims(seqlen=128), 0, 2), (scan_dims(seqlen=3), 0, 1),
-                                 (scan_dims(seqlen=1000), 1, 8), (scan_dims(seqlen=0), 0, 1), (scan_dims(batch=0), 0, 1)):
-        ref = ctypes.byref(dims)
-        assert lib.m3_gated_scan_chunks(ref, packed) == chunks
-        fwd = 256 + r(chunks * 256 * 8) if chunks > 1 else 0       # 130 channels: 2 columns of 128
-        assert lib.m3_gated_scan_workspace_bytes(ref, packed) == fwd
-        assert lib.m3_gated_scan_backward_workspace_bytes(ref, packed) == (fwd + chunks * 130 * 4 if fwd else 0)
+    # `states` has a row per 64 tokens of a sequence (of the batch, where sequences are not longer or packed); the
+    # workspace a 64-bit word per tile and channel (130 channels: 2 columns of 128) after 256 bytes, backward also a
+    # row of partial sums; bf16 forward tiles hold 128 tokens, the others 64
+    for dims, packed, rows, tiles in ((scan_dims(), 0, 10, 6), (scan_dims(seqlen=128), 0, 4, 2),
+                                      (scan_dims(seqlen=3), 0, 1, 1), (scan_dims(seqlen=1000), 1, 16, 8),
+                                      (scan_dims(seqlen=0), 0, 1, 1), (scan_dims(batch=0), 0, 1, 1)):
+        for io in (m3block.M3_BF16, m3block.M3_F32):
+            dims.io = io
+            ref = ctypes.byref(dims)
+            n = tiles if io == m3block.M3_BF16 else rows
+            assert lib.m3_gated_scan_chunks(ref, packed) == rows
+            assert lib.m3_gated_scan_workspace_bytes(ref, packed) == (256 + r(n * 256 * 8) if n > 1 else 0)
+            assert lib.m3_gated_scan_backward_workspace_bytes(ref, packed) == \
+                (256 + r(rows * 256 * 8) + rows * 130 * 4 if rows > 1 else 0)
     for call in (FWD, BWD):
         need = getattr(lib, call.fn + "_workspace_bytes")(ctypes.byref(call.dims), 0)
         assert call(cu=0, ws_bytes=need - 1) == m3scan.M3_E_WORKSPACE
