@@ -12,7 +12,6 @@ dense, and the rows before it evenly spaced.
 from __future__ import annotations
 
 import array
-import contextlib
 import ctypes
 
 import torch
@@ -82,65 +81,71 @@ def _check(status):
 
 
 def _io_code(t, name):
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return M3_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return M3_F32
     raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
 
 
-def _scope(dev, stream):
-    """Makes `dev` current, and `stream` too when one is given."""
+# A call with small tensors takes a few microseconds on the GPU, so the host's share of it counts: the
+# checks below try the ordinary case first, and device and stream are asked for as plain numbers.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _here(t, stream):
+    """The index of t's device if calls for it can be made as things are: it is the current device, and the
+    current stream is meant.  -1: not so (see _scope)."""
+    index = t.get_device()
+    return index if stream is None and index >= 0 and index == _current_device() else -1
+
+
+def _scope(t, stream):
+    """Makes t's device current, and `stream` too when one is given."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a GPU, got %s" % t.device)
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, dev))
+        if stream.device != t.device:
+            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
         return torch.cuda.stream(stream)
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on a GPU, got %s" % dev)
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
-def _raw_stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch.cuda.device(t.device)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _dense(t, name, shape, dtype, dev):
+def _alike(t, name, shape, dtype, index):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, "cuda:%d" % index if index >= 0 else "the CPU"))
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _dense(t, name, shape, dtype, index):
+    """Checks a dense tensor (None passes) and returns its address."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
-    if t.dtype != dtype:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    _alike(t, name, shape, dtype, index)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return t
+    return t.data_ptr()
 
 
-def _pitch(t, name, shape, dtype, dev):
-    """Distance in elements between the rows of `t` (0 when there is at most one)."""
+def _pitch(t, name, shape, dtype, index):
+    """Checks a tensor of rows (None passes) and returns the distance in elements between them (0: dense)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
-    if t.dtype != dtype:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.is_contiguous():
+    _alike(t, name, shape, dtype, index)
+    if t.is_contiguous() or t.numel() == 0:
         return 0
     *rows, d = shape
-    if t.numel() == 0:
-        return 0
     stride = t.stride()
     pitch, rest = None, 1   # rows counted from the innermost dimension outwards
     for n, s in zip(reversed(rows), reversed(stride[:-1])):
@@ -155,27 +160,27 @@ def _pitch(t, name, shape, dtype, dev):
     return pitch or 0
 
 
-def _workspace(workspace, need, dev):
+def _workspace(workspace, need, x):
     if need == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous and on %s" % dev)
+        return x.new_empty(need, dtype=torch.uint8), need
+    if workspace.get_device() != x.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on %s" % x.device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _scan_shape(x, cu_seqlens, h_in):
+def _scan_dims(x, cu_seqlens):
     """(batch, seqlen, D) of x [b, L, D], or [T, D] with offsets [b + 1]."""
     if cu_seqlens is None:
         if x.dim() != 3:
             raise ValueError("x must be [b, L, D] (or [T, D] with cu_seqlens), got %s" % (tuple(x.shape),))
-        return tuple(x.shape)
+        return x.shape
     if x.dim() != 2:
         raise ValueError("x must be [T, D] with cu_seqlens, got %s" % (tuple(x.shape),))
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [b + 1], got %s" % (tuple(cu_seqlens.shape),))
-    _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, x.device)
+    _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, x.get_device())
     return cu_seqlens.shape[0] - 1, x.shape[0], x.shape[1]
 
 
@@ -184,51 +189,56 @@ def m3_gated_scan(gate, x, bias=None, h_in=None, cu_seqlens=None, y=None, h_out=
     """h_t = (1 - z_t) h_{t-1} + z_t x_t with z_t = sigmoid(gate_t + bias), over [b, L, D] or, with
     cu_seqlens [b + 1] int32, a packed [T, D].  bias [D], h_in [b, D] f32.  Returns (y, h_out), and
     with save_states (or states given) also the states m3_gated_scan_backward reads."""
-    lib = load()
-    b, L, D = _scan_shape(x, cu_seqlens, h_in)
-    dev, io, shape = x.device, x.dtype, x.shape
-    dims = M3ScanDims(b, L, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev), 0, 0, 0,
-                      _io_code(x, "x"), 0)
-    _dense(bias, "bias", (D,), torch.float32, dev)
-    _dense(h_in, "h_in", (b, D), torch.float32, dev)
+    lib = _lib or load()
+    b, L, D = _scan_dims(x, cu_seqlens)
+    io, shape, dev, f32 = x.dtype, x.shape, x.get_device(), torch.float32
     packed = cu_seqlens is not None
-    with _scope(dev, stream):
-        if y is None:
-            y = torch.empty(shape, dtype=io, device=dev)
-        dims.y_pitch = _pitch(y, "y", shape, io, dev)
-        if h_out is None:
-            h_out = torch.empty((b, D), dtype=torch.float32, device=dev)
-        _dense(h_out, "h_out", (b, D), torch.float32, dev)
-        if states is not None or save_states:
-            want = (lib.m3_gated_scan_chunks(ctypes.byref(dims), packed), D)
-            if states is None:
-                states = torch.empty(want, dtype=torch.float32, device=dev)
-            _dense(states, "states", want, torch.float32, dev)
-        workspace, ws_bytes = _workspace(workspace, lib.m3_gated_scan_workspace_bytes(ctypes.byref(dims), packed), dev)
-        _check(lib.m3_gated_scan(ctypes.byref(dims), _ptr(cu_seqlens), _ptr(gate), _ptr(x), _ptr(bias), _ptr(h_in),
-                                 _ptr(y), _ptr(h_out), _ptr(states), _ptr(workspace), ws_bytes, _raw_stream(dev)))
+    dims = M3ScanDims(b, L, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
+                      _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
+    bias_p, h_in_p = _dense(bias, "bias", (D,), f32, dev), _dense(h_in, "h_in", (b, D), f32, dev)
+    h_out_p = _dense(h_out, "h_out", (b, D), f32, dev)
+    at = _here(x, stream)
+    if at < 0:
+        with _scope(x, stream):
+            return m3_gated_scan(gate, x, bias, h_in, cu_seqlens, y, h_out, states, save_states, workspace)
+    ref = ctypes.byref(dims)
+    if y is None:
+        y = x.new_empty(shape)
+    if h_out is None:
+        h_out = x.new_empty((b, D), dtype=f32)
+        h_out_p = h_out.data_ptr()
+    if states is not None or save_states:
+        want = (lib.m3_gated_scan_chunks(ref, packed), D)
+        if states is None:
+            states = x.new_empty(want, dtype=f32)
+        else:
+            _dense(states, "states", want, f32, dev)
+    workspace, ws_bytes = _workspace(workspace, lib.m3_gated_scan_workspace_bytes(ref, packed), x)
+    _check(lib.m3_gated_scan(ref, _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, y.data_ptr(), h_out_p,
+                             _ptr(states), _ptr(workspace), ws_bytes, _raw_stream(at)))
     return (y, h_out) if states is None else (y, h_out, states)
 
 
 def m3_gated_scan_step(gate, x, h, bias=None, y=None, h_out=None, stream=None):
     """One token: gate, x [b, D], state h [b, D] f32, updated in place unless h_out is given.
     Returns y."""
-    lib = load()
-    if x.dim() != 2:
-        raise ValueError("x must be [b, D], got %s" % (tuple(x.shape),))
-    dev, io, shape = x.device, x.dtype, x.shape
+    lib = _lib or load()
+    shape, io, dev, f32 = x.shape, x.dtype, x.get_device(), torch.float32
+    if len(shape) != 2:
+        raise ValueError("x must be [b, D], got %s" % (tuple(shape),))
     b, D = shape
-    dims = M3ScanDims(b, 1, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev), 0, 0, 0,
-                      _io_code(x, "x"), 0)
-    _dense(bias, "bias", (D,), torch.float32, dev)
-    _dense(h, "h", shape, torch.float32, dev)
-    _dense(h_out, "h_out", shape, torch.float32, dev)
-    with _scope(dev, stream):
-        if y is None:
-            y = torch.empty(shape, dtype=io, device=dev)
-        dims.y_pitch = _pitch(y, "y", shape, io, dev)
-        _check(lib.m3_gated_scan_step(ctypes.byref(dims), _ptr(gate), _ptr(x), _ptr(bias), _ptr(h), _ptr(y),
-                                      _ptr(h if h_out is None else h_out), _raw_stream(dev)))
+    dims = M3ScanDims(b, 1, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
+                      _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
+    bias_p, h_p = _dense(bias, "bias", (D,), f32, dev), _dense(h, "h", shape, f32, dev)
+    h_out_p = h_p if h_out is None else _dense(h_out, "h_out", shape, f32, dev)
+    at = _here(x, stream)
+    if at < 0:
+        with _scope(x, stream):
+            return m3_gated_scan_step(gate, x, h, bias, y, h_out)
+    if y is None:
+        y = x.new_empty(shape)
+    _check(lib.m3_gated_scan_step(ctypes.byref(dims), gate.data_ptr(), x.data_ptr(), bias_p, h_p, y.data_ptr(), h_out_p,
+                                  _raw_stream(at)))
     return y
 
 
@@ -237,34 +247,36 @@ def m3_gated_scan_backward(gate, x, dy, states, bias=None, h_in=None, dh_out=Non
     """Gradients of m3_gated_scan, from the states it saved.  dy like x; dh_out [b, D] f32 (None: 0).
     Returns a dict keyed by input name (gate, x, and bias, h_in where they were given); ``grads`` may
     supply preallocated tensors under those names."""
-    lib = load()
-    b, L, D = _scan_shape(x, cu_seqlens, h_in)
-    dev, io, shape = x.device, x.dtype, x.shape
-    f32 = torch.float32
-    dims = M3ScanDims(b, L, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
-                      _pitch(dy, "dy", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
+    lib = _lib or load()
+    b, L, D = _scan_dims(x, cu_seqlens)
+    io, shape, dev, f32 = x.dtype, x.shape, x.get_device(), torch.float32
     packed = cu_seqlens is not None
-    _dense(bias, "bias", (D,), f32, dev)
-    _dense(h_in, "h_in", (b, D), f32, dev)
-    _dense(dh_out, "dh_out", (b, D), f32, dev)
-    _dense(states, "states", (lib.m3_gated_scan_chunks(ctypes.byref(dims), packed), D), f32, dev)
-    g = dict(grads or {})
-    with _scope(dev, stream):
-        for k in ("gate", "x"):
-            if g.get(k) is None:
-                g[k] = torch.empty(shape, dtype=io, device=dev)
-        for k, given, want in (("bias", bias, (D,)), ("h_in", h_in, (b, D))):
-            if g.get(k) is None and given is not None:
-                g[k] = torch.empty(want, dtype=f32, device=dev)
-            _dense(g.get(k), "grad " + k, want, f32, dev)
-        dims.dgate_pitch = _pitch(g["gate"], "grad gate", shape, io, dev)
-        dims.dx_pitch = _pitch(g["x"], "grad x", shape, io, dev)
-        workspace, ws_bytes = _workspace(
-            workspace, lib.m3_gated_scan_backward_workspace_bytes(ctypes.byref(dims), packed), dev)
-        _check(lib.m3_gated_scan_backward(
-            ctypes.byref(dims), _ptr(cu_seqlens), _ptr(gate), _ptr(x), _ptr(bias), _ptr(h_in), _ptr(states), _ptr(dy),
-            _ptr(dh_out), _ptr(g["gate"]), _ptr(g["x"]), _ptr(g.get("bias")), _ptr(g.get("h_in")), _ptr(workspace),
-            ws_bytes, _raw_stream(dev)))
+    g = dict(grads) if grads else {}
+    dims = M3ScanDims(b, L, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
+                      _pitch(dy, "dy", shape, io, dev), _pitch(g.get("gate"), "grad gate", shape, io, dev),
+                      _pitch(g.get("x"), "grad x", shape, io, dev), _io_code(x, "x"), 0)
+    bias_p, h_in_p = _dense(bias, "bias", (D,), f32, dev), _dense(h_in, "h_in", (b, D), f32, dev)
+    dh_out_p = _dense(dh_out, "dh_out", (b, D), f32, dev)
+    _dense(g.get("bias"), "grad bias", (D,), f32, dev)
+    _dense(g.get("h_in"), "grad h_in", (b, D), f32, dev)
+    ref = ctypes.byref(dims)
+    states_p = _dense(states, "states", (lib.m3_gated_scan_chunks(ref, packed), D), f32, dev)
+    at = _here(x, stream)
+    if at < 0:
+        with _scope(x, stream):
+            return m3_gated_scan_backward(gate, x, dy, states, bias, h_in, dh_out, cu_seqlens, grads, workspace)
+    for k in ("gate", "x"):
+        if g.get(k) is None:
+            g[k] = x.new_empty(shape)
+    if bias is not None and g.get("bias") is None:
+        g["bias"] = x.new_empty((D,), dtype=f32)
+    if h_in is not None and g.get("h_in") is None:
+        g["h_in"] = x.new_empty((b, D), dtype=f32)
+    workspace, ws_bytes = _workspace(workspace, lib.m3_gated_scan_backward_workspace_bytes(ref, packed), x)
+    _check(lib.m3_gated_scan_backward(
+        ref, _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, states_p, dy.data_ptr(), dh_out_p,
+        g["gate"].data_ptr(), g["x"].data_ptr(), _ptr(g.get("bias")), _ptr(g.get("h_in")), _ptr(workspace), ws_bytes,
+        _raw_stream(at)))
     return g
 
 
@@ -274,32 +286,35 @@ def m3_rmsnorm(x, residual=None, weight=None, eps=1e-5, want_y=True, quant=False
     q, scale): y = n (None without want_y), r_out = r (None where there is no residual and none was
     passed), q = n / scale in float8_e4m3fn with scale f32 [..., 1] (group 0), or one for each `group`
     elements (both None without quant)."""
-    lib = load()
-    if x.dim() < 1:
+    lib = _lib or load()
+    io, shape, dev, f32 = x.dtype, x.shape, x.get_device(), torch.float32
+    if not shape:
         raise ValueError("x must have at least one dimension")
-    dev, io, shape = x.device, x.dtype, x.shape
     D = shape[-1]
-    rows = x.numel() // D if D else 0
-    dims = M3NormDims(rows, D, _pitch(x, "x", shape, io, dev), _pitch(residual, "residual", shape, io, dev), 0, 0, 0,
-                      group, _io_code(x, "x"), 0, eps)
-    _dense(weight, "weight", (D,), torch.float32, dev)
-    with _scope(dev, stream):
-        if r_out is None and residual is not None:
-            r_out = torch.empty(shape, dtype=io, device=dev)
-        if y is None and want_y:
-            y = torch.empty(shape, dtype=io, device=dev)
-        if quant or q is not None or scale is not None:
-            n = (-(-D // group) if group > 0 else 1) if D else 0
-            if q is None:
-                q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
-            if scale is None:
-                scale = torch.empty((*shape[:-1], n), dtype=torch.float32, device=dev)
+    dims = M3NormDims(x.numel() // D if D else 0, D, _pitch(x, "x", shape, io, dev),
+                      _pitch(residual, "residual", shape, io, dev), _pitch(r_out, "r_out", shape, io, dev),
+                      _pitch(y, "y", shape, io, dev), 0, group, _io_code(x, "x"), 0, eps)
+    weight_p = _dense(weight, "weight", (D,), f32, dev)
+    at = _here(x, stream)
+    if at < 0:
+        with _scope(x, stream):
+            return m3_rmsnorm(x, residual, weight, eps, want_y, quant, group, r_out, y, q, scale)
+    if r_out is None and residual is not None:
+        r_out = x.new_empty(shape)
+    if y is None and want_y:
+        y = x.new_empty(shape)
+    if quant or q is not None or scale is not None:
+        sshape = (*shape[:-1], (-(-D // group) if group > 0 else 1) if D else 0)
+        if q is None:
+            q = x.new_empty(shape, dtype=torch.float8_e4m3fn)
+        else:
             _dense(q, "q", shape, torch.float8_e4m3fn, dev)
-            _dense(scale, "scale", (*shape[:-1], n), torch.float32, dev)
-        dims.r_pitch = _pitch(r_out, "r_out", shape, io, dev)
-        dims.y_pitch = _pitch(y, "y", shape, io, dev)
-        _check(lib.m3_rmsnorm(ctypes.byref(dims), _ptr(x), _ptr(residual), _ptr(weight), _ptr(r_out), _ptr(y), _ptr(q),
-                              _ptr(scale), _raw_stream(dev)))
+        if scale is None:
+            scale = x.new_empty(sshape, dtype=f32)
+        else:
+            _dense(scale, "scale", sshape, f32, dev)
+    _check(lib.m3_rmsnorm(ctypes.byref(dims), x.data_ptr(), _ptr(residual), weight_p, _ptr(r_out), _ptr(y), _ptr(q),
+                          _ptr(scale), _raw_stream(at)))
     return y, r_out, q, scale
 
 
@@ -308,62 +323,74 @@ def m3_rmsnorm_backward(r, dy, weight=None, dr_out=None, eps=1e-5, dx=None, dwei
     """Gradients of the norm of r (m3_rmsnorm's r_out, or its x where there was no residual): dx, which is
     the gradient of x and of residual alike and takes the residual stream's dr_out in, and dweight
     (None where there is no weight and none was passed)."""
-    lib = load()
-    if r.dim() < 1:
+    lib = _lib or load()
+    io, shape, dev, f32 = r.dtype, r.shape, r.get_device(), torch.float32
+    if not shape:
         raise ValueError("r must have at least one dimension")
-    dev, io, shape = r.device, r.dtype, r.shape
     D = shape[-1]
-    rows = r.numel() // D if D else 0
-    dims = M3NormDims(rows, D, 0, _pitch(dr_out, "dr_out", shape, io, dev), _pitch(r, "r", shape, io, dev),
-                      _pitch(dy, "dy", shape, io, dev), 0, 0, _io_code(r, "r"), 0, eps)
-    _dense(weight, "weight", (D,), torch.float32, dev)
-    with _scope(dev, stream):
-        if dx is None:
-            dx = torch.empty(shape, dtype=io, device=dev)
-        dims.dx_pitch = _pitch(dx, "dx", shape, io, dev)
-        if dweight is None and weight is not None:
-            dweight = torch.empty((D,), dtype=torch.float32, device=dev)
-        _dense(dweight, "dweight", (D,), torch.float32, dev)
-        need = lib.m3_rmsnorm_backward_workspace_bytes(ctypes.byref(dims)) if dweight is not None else 0
-        workspace, ws_bytes = _workspace(workspace, need, dev)
-        _check(lib.m3_rmsnorm_backward(ctypes.byref(dims), _ptr(r), _ptr(weight), _ptr(dy), _ptr(dr_out), _ptr(dx),
-                                       _ptr(dweight), _ptr(workspace), ws_bytes, _raw_stream(dev)))
+    dims = M3NormDims(r.numel() // D if D else 0, D, 0, _pitch(dr_out, "dr_out", shape, io, dev),
+                      _pitch(r, "r", shape, io, dev), _pitch(dy, "dy", shape, io, dev),
+                      _pitch(dx, "dx", shape, io, dev), 0, _io_code(r, "r"), 0, eps)
+    weight_p = _dense(weight, "weight", (D,), f32, dev)
+    _dense(dweight, "dweight", (D,), f32, dev)
+    at = _here(r, stream)
+    if at < 0:
+        with _scope(r, stream):
+            return m3_rmsnorm_backward(r, dy, weight, dr_out, eps, dx, dweight, workspace)
+    if dx is None:
+        dx = r.new_empty(shape)
+    if dweight is None and weight is not None:
+        dweight = r.new_empty((D,), dtype=f32)
+    ref = ctypes.byref(dims)
+    need = lib.m3_rmsnorm_backward_workspace_bytes(ref) if dweight is not None else 0
+    workspace, ws_bytes = _workspace(workspace, need, r)
+    _check(lib.m3_rmsnorm_backward(ref, r.data_ptr(), weight_p, dy.data_ptr(), _ptr(dr_out), dx.data_ptr(), _ptr(dweight),
+                                   _ptr(workspace), ws_bytes, _raw_stream(at)))
     return dx, dweight
 
 
-def _grad_call(name, grads, max_norm, out, stats, workspace, stream):
-    lib = load()
-    pairs = []   # (gradient, where it goes)
+def _grad_call(fn, grads, max_norm, out, stats, workspace, stream):
+    lib = _lib or load()
     if isinstance(grads, dict):
         if out is not None and not isinstance(out, dict):
             raise TypeError("out must be a dict like grads")
-        pairs = [(k, g, g if out is None else out[k]) for k, g in grads.items() if g is not None]
+        names = [k for k, g in grads.items() if g is not None]
+        src, dst = [grads[k] for k in names], None if out is None else [out[k] for k in names]
     else:
-        grads = list(grads)
-        dst = grads if out is None else list(out)
-        if len(dst) != len(grads):
-            raise ValueError("%d gradients, %d outputs" % (len(grads), len(dst)))
-        pairs = [(i, g, o) for i, (g, o) in enumerate(zip(grads, dst)) if g is not None]
-    dev = pairs[0][1].device if pairs else (stats.device if stats is not None else torch.device(
-        "cuda", torch.cuda.current_device()))
-    table = []
-    for k, g, o in pairs:
-        code = _io_code(g, "gradient %s" % k)
-        if g.device != dev:
-            raise ValueError("gradient %s is on %s, expected %s" % (k, g.device, dev))
-        if not g.is_contiguous():
-            raise ValueError("gradient %s must be contiguous" % k)
-        if o is not g:
-            _dense(o, "output %s" % k, g.shape, g.dtype, dev)
-        table += (g.data_ptr(), o.data_ptr(), g.numel(), code)
-    buf = array.array("Q", table)   # the fields of M3GradTensor, io and pad as one little-endian word
-    ptr = buf.buffer_info()[0] if table else None
-    with _scope(dev, stream):
-        if stats is None:
-            stats = torch.empty(2, dtype=torch.float32, device=dev)
-        _dense(stats, "stats", (2,), torch.float32, dev)
-        workspace, ws_bytes = _workspace(workspace, lib.m3_grad_workspace_bytes(ptr, len(pairs)), dev)
-        _check(getattr(lib, name)(ptr, len(pairs), max_norm, _ptr(stats), _ptr(workspace), ws_bytes, _raw_stream(dev)))
+        if out is not None and len(out) != len(grads):
+            raise ValueError("%d gradients, %d outputs" % (len(grads), len(out)))
+        names = [i for i, g in enumerate(grads) if g is not None]
+        src, dst = [grads[i] for i in names], None if out is None else [out[i] for i in names]
+    if not src and stats is None:
+        stats = torch.empty(2, dtype=torch.float32, device="cuda")
+    first = src[0] if src else stats
+    dev, f32, bf16 = first.get_device(), torch.float32, torch.bfloat16
+    table = []   # the fields of M3GradTensor, io and pad as one little-endian word
+    for i, g in enumerate(src):
+        dtype = g.dtype
+        if (dtype is not f32 and dtype is not bf16) or g.get_device() != dev or not g.is_contiguous():
+            _io_code(g, "gradient %s" % names[i])
+            _dense(g, "gradient %s" % names[i], g.shape, dtype, dev)
+        p = g.data_ptr()
+        if dst is None or dst[i] is g:
+            o = p
+        else:
+            o = _dense(dst[i], "output %s" % names[i], g.shape, dtype, dev)
+            if o is None:
+                raise ValueError("output %s is None" % names[i])
+        table += (p, o, g.numel(), M3_F32 if dtype is f32 else M3_BF16)
+    stats_p = _dense(stats, "stats", (2,), f32, dev)
+    at = _here(first, stream)
+    if at < 0:
+        with _scope(first, stream):
+            return _grad_call(fn, grads, max_norm, out, stats, workspace, None)
+    if stats is None:
+        stats = first.new_empty(2, dtype=f32)
+        stats_p = stats.data_ptr()
+    buf = array.array("Q", table)
+    ptr = buf.buffer_info()[0] if src else None
+    workspace, ws_bytes = _workspace(workspace, lib.m3_grad_workspace_bytes(ptr, len(src)), first)
+    _check(getattr(lib, fn)(ptr, len(src), max_norm, stats_p, _ptr(workspace), ws_bytes, _raw_stream(at)))
     return stats
 
 
@@ -371,13 +398,17 @@ def m3_grad_norm(grads, max_norm=float("inf"), stats=None, workspace=None, strea
     """2-norm over all elements of ``grads`` (a sequence, or a dict as the backward calls return; None
     entries are left out), and the factor that brings it to max_norm: returns stats = [norm, coef] f32
     on the device."""
+    if not isinstance(grads, (dict, list, tuple)):
+        grads = list(grads)
     return _grad_call("m3_grad_norm", grads, max_norm, None, stats, workspace, stream)
 
 
 def m3_grad_clip(grads, max_norm, out=None, stats=None, workspace=None, stream=None):
     """Scales all gradients by coef = min(1, max_norm / (norm + 1e-6)), in place or into ``out`` (tensors
     like them in a container like theirs).  Returns (grads or out, stats = [norm, coef])."""
-    if not isinstance(grads, dict):
+    if not isinstance(grads, (dict, list, tuple)):
         grads = list(grads)
+    if out is not None and not isinstance(out, (dict, list, tuple)):
+        out = list(out)
     stats = _grad_call("m3_grad_clip", grads, max_norm, out, stats, workspace, stream)
     return (grads if out is None else out), stats
