@@ -85,10 +85,13 @@ struct RmsNormArgs {
     int group;                 // 0: the row
     int ngroups;
     float eps;
+    int cus;                   // compute units
+    int stream;                // outputs go past the caches
 };
 hipError_t launch_rmsnorm(const RmsNormArgs& a, bool bf16_io, hipStream_t s);
 hipError_t launch_rmsnorm_backward(const RmsNormArgs& a, bool bf16_io, hipStream_t s);
-int64_t rmsnorm_backward_parts(int64_t rows, int64_t D);   // rows of dweight partial sums
+// rows of dweight partial sums
+int64_t rmsnorm_backward_parts(int64_t rows, int64_t D, bool bf16_io, int cus);
 
 // ----------------------------------------------------------------- column sums, gradient norm
 // out[d] = sum over i < n of part[i * D + d], in a fixed order
@@ -96,7 +99,8 @@ hipError_t launch_column_sum(const float* part, int64_t n, int64_t D, float* out
 
 constexpr int kGradBatch = 96;           // tensors per launch (their table is a kernel argument)
 constexpr int64_t kGradChunk = 16384;    // elements per unit of work
-constexpr int kGradBlocks = 1024;        // workgroups, and partial sums, per launch at most
+constexpr int kGradBlocks = 2048;        // workgroups, and partial sums, per launch at most
+constexpr int64_t kGradSmall = 65536;    // as many elements in one table are left to a single workgroup
 
 struct GradBatch {
     const void* src[kGradBatch];
@@ -105,6 +109,7 @@ struct GradBatch {
     uint32_t first[kGradBatch + 1];      // first unit of work of each tensor, and their number
     uint32_t is_bf16[(kGradBatch + 31) / 32];
     int n;
+    int stream;                          // outputs go past the caches
 };
 inline int grad_blocks(const GradBatch& b) {
     const uint32_t units = b.first[b.n];
@@ -117,5 +122,7 @@ hipError_t launch_grad_stats(const double* part, int64_t n, float max_norm, floa
 // dst = coef src, coef from n partial sums; with stats, also {norm, coef} there
 hipError_t launch_grad_scale(const GradBatch& b, const double* part, int n, float max_norm, float* stats,
                              hipStream_t s);
+// all of it, by one workgroup
+hipError_t launch_grad_small(const GradBatch& b, bool write, float max_norm, float* stats, hipStream_t s);
 
 }  // namespace m3

@@ -52,6 +52,9 @@ __device__ __forceinline__ void gate_of(float g, float bias, float& z, float& ke
 // lane's byte offset in the row and the row's scalar offset: no vector arithmetic, and a lane offset of
 // kNowhere (beyond the descriptor's 2^31 bytes) reads zero and stores nothing.
 constexpr uint32_t kNowhere = 0xfffffff0u;
+// Inputs are read once: non-temporal, which leaves the caches to y's rows and the chain (b8 L2048 D4096 bf16:
+// forward 94 -> 89 us, backward 170 -> 158 us; no difference seen on small batches).
+constexpr int kStream = 2;
 __device__ __forceinline__ rsrc_t rows_at(const void* base, int64_t bytes) {
     return make_rsrc((const char*)base + bytes, 0x80000000u);
 }
@@ -61,7 +64,7 @@ template <> struct Pair<float, true> {
     __device__ __forceinline__ void zero() { v = (u32x2){0, 0}; }
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
     __device__ __forceinline__ void load(rsrc_t r, uint32_t o0, uint32_t, int row) {
-        v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)o0, row, 0);
+        v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)o0, row, kStream);
     }
     __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v.y : v.x); }
 };
@@ -70,7 +73,7 @@ template <> struct Pair<bf16, true> {
     __device__ __forceinline__ void zero() { v = 0; }
     __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
     __device__ __forceinline__ void load(rsrc_t r, uint32_t o0, uint32_t, int row) {
-        v = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o0, row, 0);
+        v = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o0, row, kStream);
     }
     __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
 };
@@ -82,8 +85,8 @@ template <> struct Pair<float, false> {
         asm volatile("" : "+v"(v[1]));
     }
     __device__ __forceinline__ void load(rsrc_t r, uint32_t o0, uint32_t o1, int row) {
-        v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o0, row, 0);
-        v[1] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o1, row, 0);
+        v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o0, row, kStream);
+        v[1] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o1, row, kStream);
     }
     __device__ __forceinline__ float get(int i) const { return __uint_as_float(v[i]); }
 };
@@ -95,8 +98,8 @@ template <> struct Pair<bf16, false> {
         asm volatile("" : "+v"(v[1]));
     }
     __device__ __forceinline__ void load(rsrc_t r, uint32_t o0, uint32_t o1, int row) {
-        v[0] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)o0, row, 0);
-        v[1] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)o1, row, 0);
+        v[0] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)o0, row, kStream);
+        v[1] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)o1, row, kStream);
     }
     __device__ __forceinline__ float get(int i) const { return __uint_as_float((uint32_t)v[i] << 16); }
 };

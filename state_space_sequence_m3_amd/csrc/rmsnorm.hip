@@ -14,7 +14,9 @@ namespace {
 // byte address, at the cost of the extra line they touch).
 struct __attribute__((packed, aligned(2))) Bf16x8 { uint32_t v[4]; };
 struct __attribute__((packed, aligned(4))) F32x4 { float v[4]; };
-struct __attribute__((packed, aligned(1))) Byte8 { uint32_t v[2]; };
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
 
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16> {
@@ -53,41 +55,51 @@ __device__ __forceinline__ void load8(Raw8<T>& r, const char* row, int e, int D)
     else if (e < D) r.load_some(p, D - e);
     else r.zero();
 }
+// STREAM: non-temporal.  A template argument, since the compiler makes one ordinary store of two that differ
+// in nothing else.
+template <bool STREAM, typename V, typename P>
+__device__ __forceinline__ void put(P* p, V v) {
+    if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+template <bool STREAM>
 __device__ __forceinline__ void store8(char* row, int e, int D, const float (&f)[8], bf16) {
     uint16_t* p = (uint16_t*)(row + (int64_t)e * 2);
     if (e + 8 <= D) {
-        Bf16x8 v;
-        for (int k = 0; k < 4; ++k) v.v[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
-        *(Bf16x8*)p = v;
+        u32x4 v;
+        for (int k = 0; k < 4; ++k) v[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+        put<STREAM>((u32x4_at2*)p, v);
     } else {
         for (int k = 0; k < 8; ++k)
             if (e + k < D) p[k] = bf16_bits_rne(f[k]);
     }
 }
+template <bool STREAM>
 __device__ __forceinline__ void store8(char* row, int e, int D, const float (&f)[8], float) {
     float* p = (float*)(row + (int64_t)e * 4);
     if (e + 8 <= D) {
-        F32x4 a, b;
+        u32x4 a, b;
         for (int k = 0; k < 4; ++k) {
-            a.v[k] = f[k];
-            b.v[k] = f[k + 4];
+            a[k] = __float_as_uint(f[k]);
+            b[k] = __float_as_uint(f[k + 4]);
         }
-        *(F32x4*)p = a;
-        *(F32x4*)(p + 4) = b;
+        put<STREAM>((u32x4_at4*)p, a);
+        put<STREAM>((u32x4_at4*)(p + 4), b);
     } else {
         for (int k = 0; k < 8; ++k)
             if (e + k < D) p[k] = f[k];
     }
 }
+template <bool STREAM>
 __device__ __forceinline__ void store_q8(uint8_t* p, int e, int D, const float (&f)[8]) {
-    uint32_t v[2];
+    u32x2 v;
     for (int k = 0; k < 2; ++k) {
         int u = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k], f[4 * k + 1], 0, false);
         v[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k + 2], f[4 * k + 3], u, true);
     }
     p += e;
     if (e + 8 <= D) {
-        *(Byte8*)p = Byte8{{v[0], v[1]}};
+        put<STREAM>((u32x2_at1*)p, v);
     } else {
         for (int k = 0; k < 8; ++k)
             if (e + k < D) p[k] = (uint8_t)(v[k >> 2] >> (8 * (k & 3)));
@@ -117,10 +129,15 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v, int R) {
 }
 
 template <int TPR> constexpr int wg_threads() { return TPR < 256 ? 256 : TPR; }
+// Waves per SIMD that registers are left for, and with it the workgroups that are resident: the grid is
+// that many, each takes every gridDim-th row.
+template <typename T, int TPR, int C> constexpr int kFwdOcc = C > 1 ? 4 : 6;
+template <typename T, int TPR, int C> constexpr int kBwdOcc = C > 1 || sizeof(T) == 4 ? 4 : 5;
+constexpr int resident(int occ, int threads) { return occ * 256 / threads > 0 ? occ * 256 / threads : 1; }
 
 // ---------------------------------------------------------------------------------- forward
-template <typename T, int TPR, int C>
-__global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_kernel(const RmsNormArgs a) {
+template <typename T, int TPR, int C, bool STREAM>
+__global__ __launch_bounds__(wg_threads<TPR>(), (kFwdOcc<T, TPR, C>)) void rmsnorm_kernel(const RmsNormArgs a) {
     constexpr int NT = wg_threads<TPR>(), RPW = NT / TPR, WPR = TPR / 64;   // rows per workgroup, waves per row
     __shared__ float s_sum[2][WPR > 1 ? WPR : 1];
     __shared__ uint32_t s_max[2][WPR > 1 ? WPR : 1];
@@ -135,12 +152,9 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_kernel(const RmsNor
             wt[c][k] = a.weight && e < a.D ? a.weight[e] : 1.f;
         }
     const float inv_d = 1.f / (float)a.D;
-    int flip = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * RPW; row0 < a.rows; row0 += (int64_t)gridDim.x * RPW) {
-        const int64_t row = row0 + slot;
-        const bool live = row < a.rows;
-        const int D = live ? a.D : 0;      // a row past the end reads and writes nothing
-        Raw8<T> rx[C], rr[C];
+    Raw8<T> rx[C], rr[C];
+    auto load = [&](int64_t row) {             // a row past the end reads nothing
+        const int D = row < a.rows ? a.D : 0;
         const char* xp = (const char*)a.x + row * a.x_p;
         const char* pp = (const char*)a.residual + row * a.res_p;
 #pragma unroll
@@ -148,6 +162,12 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_kernel(const RmsNor
             load8<T>(rx[c], xp, (c * TPR + t) * 8, D);
             if (a.residual) load8<T>(rr[c], pp, (c * TPR + t) * 8, D);
         }
+    };
+    int flip = 0;
+    load((int64_t)blockIdx.x * RPW + slot);
+    for (int64_t row0 = (int64_t)blockIdx.x * RPW; row0 < a.rows; row0 += (int64_t)gridDim.x * RPW) {
+        const int64_t row = row0 + slot;
+        const int D = row < a.rows ? a.D : 0;  // and writes nothing
         float r[C][8];
         float ss = 0.f;
 #pragma unroll
@@ -157,6 +177,9 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_kernel(const RmsNor
                 r[c][k] = rx[c].get(k) + (a.residual ? rr[c].get(k) : 0.f);
                 ss = fmaf(r[c][k], r[c][k], ss);
             }
+        // the next row travels while this one is worked on; its places are read before they are written
+        // (outputs may lie over inputs, row on row)
+        if (row0 + (int64_t)gridDim.x * RPW < a.rows) load(row + (int64_t)gridDim.x * RPW);
         ss = group_sum(ss, TPR < 64 ? TPR : 64);
         if constexpr (WPR > 1) {
             if ((threadIdx.x & 63) == 0) s_sum[flip][threadIdx.x >> 6] = ss;
@@ -169,7 +192,7 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_kernel(const RmsNor
             char* op = (char*)a.r_out + row * a.r_p;
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                if ((c * TPR + t) * 8 < D) store8(op, (c * TPR + t) * 8, D, r[c], T{});
+                if ((c * TPR + t) * 8 < D) store8<STREAM>(op, (c * TPR + t) * 8, D, r[c], T{});
         }
         const float rs = 1.f / sqrtf(ss * inv_d + a.eps);
         uint32_t top[C], all = 0;
@@ -187,7 +210,7 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_kernel(const RmsNor
             char* op = (char*)a.y + row * a.y_p;
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                if ((c * TPR + t) * 8 < D) store8(op, (c * TPR + t) * 8, D, r[c], T{});
+                if ((c * TPR + t) * 8 < D) store8<STREAM>(op, (c * TPR + t) * 8, D, r[c], T{});
         }
         if (a.q) {
             if (a.group == 0) {
@@ -214,7 +237,7 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_kernel(const RmsNor
                     for (int k = 0; k < 8; ++k) qv[k] = r[c][k] / scale;
                 }
                 if (e < D) {
-                    store_q8(a.q + row * (int64_t)a.D, e, D, qv);
+                    store_q8<STREAM>(a.q + row * (int64_t)a.D, e, D, qv);
                     if (a.group == 0) {
                         if (e == 0) a.scale[row] = scale;
                     } else if (e % a.group == 0) {
@@ -230,8 +253,8 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_kernel(const RmsNor
 // --------------------------------------------------------------------------------- backward
 // Each workgroup takes rows blockIdx, blockIdx + grid, ... and keeps its share of dweight in
 // registers; the shares are added in a second launch.
-template <typename T, int TPR, int C>
-__global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_backward_kernel(const RmsNormArgs a) {
+template <typename T, int TPR, int C, bool STREAM>
+__global__ __launch_bounds__(wg_threads<TPR>(), (kBwdOcc<T, TPR, C>)) void rmsnorm_backward_kernel(const RmsNormArgs a) {
     constexpr int NT = wg_threads<TPR>(), RPW = NT / TPR, WPR = TPR / 64;
     __shared__ float2 s_sum[2][WPR > 1 ? WPR : 1];
     const int t = threadIdx.x % TPR;
@@ -295,7 +318,7 @@ __global__ __launch_bounds__(wg_threads<TPR>()) void rmsnorm_backward_kernel(con
                 if (a.dr_out) o[k] += rd[c].get(k);
                 if (live) dw[c][k] = fmaf(dy, r * rs, dw[c][k]);
             }
-            if ((c * TPR + t) * 8 < D) store8(op, (c * TPR + t) * 8, D, o, T{});
+            if ((c * TPR + t) * 8 < D) store8<STREAM>(op, (c * TPR + t) * 8, D, o, T{});
         }
         flip ^= 1;
     }
@@ -324,57 +347,75 @@ Plan plan_of(int64_t D) {
     if (D <= 8192) return {1024, 1};
     return {1024, 2};
 }
-int rows_per_wg(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
+constexpr int rows_per_wg(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
 
-unsigned blocks_for(int64_t rows, int tpr, int most) {
-    const int64_t n = (rows + rows_per_wg(tpr) - 1) / rows_per_wg(tpr);
+// f<TPR, C>() for the plan
+template <typename F>
+auto with_plan(const Plan& p, F&& f) {
+    if (p.tpr == 16) return f.template operator()<16, 1>();
+    if (p.tpr == 64 && p.chunks == 1) return f.template operator()<64, 1>();
+    if (p.tpr == 64) return f.template operator()<64, 2>();
+    if (p.tpr == 256) return f.template operator()<256, 1>();
+    if (p.tpr == 512) return f.template operator()<512, 1>();
+    if (p.chunks == 1) return f.template operator()<1024, 1>();
+    return f.template operator()<1024, 2>();
+}
+unsigned grid_of(int64_t rows, int tpr, int per_cu, int cus) {
+    const int64_t n = (rows + rows_per_wg(tpr) - 1) / rows_per_wg(tpr), most = (int64_t)per_cu * cus;
     return (unsigned)(n < most ? n : most);
 }
-int forward_most(int tpr) { return tpr >= 1024 ? 512 : tpr >= 512 ? 1024 : 2048; }
-int backward_most(int tpr) { return tpr >= 1024 ? 256 : 512; }
-
 template <typename T>
-hipError_t forward(const RmsNormArgs& a, hipStream_t s) {
-    const Plan p = plan_of(a.D);
-    const dim3 grid(blocks_for(a.rows, p.tpr, forward_most(p.tpr))), block(p.tpr < 256 ? 256 : p.tpr);
-    if (p.tpr == 16) hipLaunchKernelGGL((rmsnorm_kernel<T, 16, 1>), grid, block, 0, s, a);
-    else if (p.tpr == 64 && p.chunks == 1) hipLaunchKernelGGL((rmsnorm_kernel<T, 64, 1>), grid, block, 0, s, a);
-    else if (p.tpr == 64) hipLaunchKernelGGL((rmsnorm_kernel<T, 64, 2>), grid, block, 0, s, a);
-    else if (p.tpr == 256) hipLaunchKernelGGL((rmsnorm_kernel<T, 256, 1>), grid, block, 0, s, a);
-    else if (p.tpr == 512) hipLaunchKernelGGL((rmsnorm_kernel<T, 512, 1>), grid, block, 0, s, a);
-    else if (p.chunks == 1) hipLaunchKernelGGL((rmsnorm_kernel<T, 1024, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((rmsnorm_kernel<T, 1024, 2>), grid, block, 0, s, a);
-    return hipGetLastError();
-}
+struct Forward {
+    const RmsNormArgs& a;
+    hipStream_t s;
+    template <int TPR, int C>
+    hipError_t operator()() {
+        constexpr int NT = wg_threads<TPR>();
+        const dim3 grid(grid_of(a.rows, TPR, resident(kFwdOcc<T, TPR, C>, NT), a.cus));
+        if (a.stream) hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, C, true>), grid, dim3(NT), 0, s, a);
+        else hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, C, false>), grid, dim3(NT), 0, s, a);
+        return hipGetLastError();
+    }
+};
 template <typename T>
-hipError_t backward(const RmsNormArgs& a, hipStream_t s) {
-    const Plan p = plan_of(a.D);
-    const dim3 grid(blocks_for(a.rows, p.tpr, backward_most(p.tpr))), block(p.tpr < 256 ? 256 : p.tpr);
-    if (p.tpr == 16) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, 16, 1>), grid, block, 0, s, a);
-    else if (p.tpr == 64 && p.chunks == 1) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, 64, 1>), grid, block, 0, s, a);
-    else if (p.tpr == 64) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, 64, 2>), grid, block, 0, s, a);
-    else if (p.tpr == 256) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, 256, 1>), grid, block, 0, s, a);
-    else if (p.tpr == 512) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, 512, 1>), grid, block, 0, s, a);
-    else if (p.chunks == 1) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, 1024, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((rmsnorm_backward_kernel<T, 1024, 2>), grid, block, 0, s, a);
-    return hipGetLastError();
-}
+struct Backward {
+    const RmsNormArgs& a;
+    hipStream_t s;
+    bool launch;
+    int64_t* parts;        // rows of dweight partial sums
+    template <int TPR, int C>
+    hipError_t operator()() {
+        constexpr int NT = wg_threads<TPR>();
+        const dim3 grid(grid_of(a.rows, TPR, resident(kBwdOcc<T, TPR, C>, NT), a.cus));
+        *parts = (int64_t)grid.x * rows_per_wg(TPR);
+        if (!launch) return hipSuccess;
+        if (a.stream) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, TPR, C, true>), grid, dim3(NT), 0, s, a);
+        else hipLaunchKernelGGL((rmsnorm_backward_kernel<T, TPR, C, false>), grid, dim3(NT), 0, s, a);
+        return hipGetLastError();
+    }
+};
 
 }  // namespace
 
-int64_t rmsnorm_backward_parts(int64_t rows, int64_t D) {
-    const Plan p = plan_of(D);
-    return (int64_t)blocks_for(rows, p.tpr, backward_most(p.tpr)) * rows_per_wg(p.tpr);
+int64_t rmsnorm_backward_parts(int64_t rows, int64_t D, bool bf16_io, int cus) {
+    RmsNormArgs a{};
+    a.rows = rows;
+    a.cus = cus;
+    int64_t parts = 0;
+    if (bf16_io) with_plan(plan_of(D), Backward<bf16>{a, nullptr, false, &parts});
+    else with_plan(plan_of(D), Backward<float>{a, nullptr, false, &parts});
+    return parts;
 }
 
 hipError_t launch_rmsnorm(const RmsNormArgs& a, bool bf16_io, hipStream_t s) {
-    return bf16_io ? forward<bf16>(a, s) : forward<float>(a, s);
+    return bf16_io ? with_plan(plan_of(a.D), Forward<bf16>{a, s}) : with_plan(plan_of(a.D), Forward<float>{a, s});
 }
 
 hipError_t launch_rmsnorm_backward(const RmsNormArgs& a, bool bf16_io, hipStream_t s) {
-    hipError_t e = bf16_io ? backward<bf16>(a, s) : backward<float>(a, s);
-    if (e == hipSuccess && a.dweight)
-        e = launch_column_sum(a.part, rmsnorm_backward_parts(a.rows, a.D), a.D, a.dweight, s);
+    int64_t parts = 0;
+    hipError_t e = bf16_io ? with_plan(plan_of(a.D), Backward<bf16>{a, s, true, &parts})
+                           : with_plan(plan_of(a.D), Backward<float>{a, s, true, &parts});
+    if (e == hipSuccess && a.dweight) e = launch_column_sum(a.part, parts, a.D, a.dweight, s);
     return e;
 }
 

@@ -132,6 +132,9 @@ def _dense(t, name, shape, dtype, index):
     """Checks a dense tensor (None passes) and returns its address."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
     _alike(t, name, shape, dtype, index)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -141,6 +144,9 @@ def _dense(t, name, shape, dtype, index):
 def _pitch(t, name, shape, dtype, index):
     """Checks a tensor of rows (None passes) and returns the distance in elements between them (0: dense)."""
     if t is None:
+        return 0
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape \
+            and t.is_contiguous():
         return 0
     _alike(t, name, shape, dtype, index)
     if t.is_contiguous() or t.numel() == 0:

@@ -304,7 +304,7 @@ def test_gradient_workspace():
     size = lambda n: lib.m3_grad_workspace_bytes(ctypes.cast(table, P), n)
     assert size(0) == 0 and size(1) == 16 and size(96) == 97 * 8 and size(200) == 201 * 8
     table[0].numel = 16384 * 5000
-    assert size(1) == 1025 * 8
+    assert size(1) == 2049 * 8
     table[0].numel = 0
     assert size(1) == 0 and size(3) == 24
     assert lib.m3_grad_workspace_bytes(None, 3) == 0
