@@ -84,7 +84,7 @@ m3_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t n
 struct ScanPlan {
     int64_t T = 0, ntiles = 1, seq_tiles = 1, blocks = 1, seq_blocks = 1;
     int ncols = 0;
-    bool per_seq = false;
+    bool per_seq = false, chain = false;
     size_t words_off = 256, part_off = 0, bytes = 0;
 };
 
@@ -98,13 +98,18 @@ m3_status check_scan_dims(const m3_scan_dims* d) {
     return M3_OK;
 }
 
+constexpr int64_t kMaxLoneTiles = 512;   // two workgroups on each of 256 compute units
 // The tiles of the forward or the backward pass, and the blocks that have a row of `states`.
 m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan* p) {
     M3_TRY(check_scan_dims(d));
     constexpr int64_t block = m3::kScanBlock;
     const int64_t tile = d->io != M3_BF16 ? m3::kScanTileF32 : backward ? m3::kScanBwdTileBf16 : m3::kScanTileBf16;
     p->T = packed ? d->seqlen : d->batch * d->seqlen;
-    p->per_seq = !packed && d->batch > 0 && d->seqlen > block;
+    p->ncols = (int)((d->width + m3::kScanCols - 1) / m3::kScanCols);
+    // Short sequences share tiles, unless they are so few that a tile each, and no chain between tiles, costs
+    // less: up to one round of workgroups (11 x 11 tokens of 64 channels: 12.8 -> FILL us a call).
+    p->per_seq = !packed && d->batch > 0 && d->seqlen > 0 &&
+                 (d->seqlen > block || d->batch * p->ncols <= kMaxLoneTiles);
     if (p->per_seq) {
         p->seq_tiles = (d->seqlen + tile - 1) / tile;
         p->seq_blocks = (d->seqlen + block - 1) / block;
@@ -114,14 +119,12 @@ m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan*
         p->ntiles = std::max<int64_t>(1, (p->T + tile - 1) / tile);
         p->blocks = std::max<int64_t>(1, (p->T + block - 1) / block);
     }
-    p->ncols = (int)((d->width + m3::kScanCols - 1) / m3::kScanCols);
+    p->chain = (p->per_seq ? p->seq_tiles : p->ntiles) > 1;
     if (p->blocks >= kMaxCount || p->blocks * p->ncols >= kMaxCount)
         return fail(M3_E_DIMS, "%lld tokens of %lld channels: more than 2^31 blocks of 64 tokens and 128 channels",
                     (long long)p->T, (long long)d->width);
-    if (p->ntiles > 1) {
-        p->part_off = p->words_off + round256((size_t)p->ntiles * p->ncols * m3::kScanCols * 8);
-        p->bytes = p->part_off + (backward ? (size_t)p->ntiles * d->width * 4 : 0);
-    }
+    if (p->chain) p->part_off = p->words_off + round256((size_t)p->ntiles * p->ncols * m3::kScanCols * 8);
+    p->bytes = p->part_off + (backward && p->ntiles > 1 ? (size_t)p->ntiles * d->width * 4 : 0);
     return M3_OK;
 }
 
@@ -136,6 +139,7 @@ void scan_args(const m3_scan_dims* d, const ScanPlan& p, const int32_t* cu, void
     a->seq_blocks = (uint32_t)p.seq_blocks;
     a->ncols = p.ncols;
     a->per_seq = p.per_seq ? 1 : 0;
+    a->chain = p.chain ? 1 : 0;
     a->ticket = (unsigned*)ws;
     a->words = (uint64_t*)((char*)ws + p.words_off);
     a->part = (float*)((char*)ws + p.part_off);
@@ -268,8 +272,9 @@ GradPlan plan_grads(const m3_grad_tensor* t, int64_t n) {
     });
     return p;
 }
+bool grad_small(const GradPlan& p) { return p.batches == 1 && p.elements <= m3::kGradSmall; }
 // partial sums, and their sum
-size_t grad_bytes(const GradPlan& p) { return p.parts == 0 ? 0 : (size_t)(p.parts + 1) * 8; }
+size_t grad_bytes(const GradPlan& p) { return p.parts == 0 || grad_small(p) ? 0 : (size_t)(p.parts + 1) * 8; }
 
 // As many partial sums are added again by every workgroup of the scaling pass; more are added once, by a
 // launch of their own.
@@ -286,7 +291,7 @@ m3_status grads(const char* fn, bool write, const m3_grad_tensor* t, int64_t n, 
     const Extent more[] = {{(uintptr_t)stats, (uintptr_t)stats + 8, -1, true},
                            {(uintptr_t)ws, (uintptr_t)ws + grad_bytes(p), -1, true}};
     if (write) {
-        M3_TRY(check_grad_overlap(t, n, more, p.parts ? 2 : 1));
+        M3_TRY(check_grad_overlap(t, n, more, grad_bytes(p) ? 2 : 1));
     } else {
         for (int64_t i = 0; i < n; ++i)
             for (const Extent& x : more)
@@ -296,7 +301,7 @@ m3_status grads(const char* fn, bool write, const m3_grad_tensor* t, int64_t n, 
     }
     M3_TRY(check_device());
     double* part = (double*)ws;
-    if (p.batches == 1 && p.elements <= m3::kGradSmall)
+    if (grad_small(p))
         return for_batches(t, n, false, false, [&](const m3::GradBatch& b, int64_t) {
             return launched(m3::launch_grad_small(b, write, max_norm, stats, stream), fn);
         });

@@ -12,8 +12,8 @@ namespace m3 {
 // ---------------------------------------------------------------------------- gated scan
 // A tile is kScanTile* tokens x kScanCols channels, worked on by one workgroup; `states` has a row per
 // block of kScanBlock tokens, whatever the type.  Dense batches of sequences longer than a block are
-// cut sequence by sequence (`per_seq`); shorter ones and packed batches are cut along the flat token
-// axis, so a tile can hold many sequences.
+// cut sequence by sequence (`per_seq`), and so are few shorter ones; many shorter ones and packed batches
+// are cut along the flat token axis, so a tile can hold many sequences.
 constexpr int kScanTileBf16 = 128, kScanBwdTileBf16 = 64, kScanTileF32 = 64, kScanBlock = 64;
 constexpr int kScanCols = 128;
 
@@ -37,13 +37,14 @@ struct GatedScanArgs {
     int64_t b, L, T;        // sequences; tokens of each (dense); tokens of all
     int64_t D;
     int64_t gate_p, x_p, y_p, dgate_p, dx_p;   // pitches in bytes
-    uint64_t* words;        // [ntiles, ncols * kScanCols] chain words (ntiles > 1)
+    uint64_t* words;        // [ntiles, ncols * kScanCols] chain words (chain)
     unsigned* ticket;
     int64_t ntiles;
     uint32_t seq_tiles;     // tiles, and blocks, per sequence (per_seq)
     uint32_t seq_blocks;
     int ncols;              // column blocks
     int per_seq;
+    int chain;              // tiles wait for others: words and ticket are there
 };
 
 hipError_t launch_gated_scan(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s);

@@ -317,7 +317,7 @@ __global__ __launch_bounds__(256) void chain_reset_kernel(uint4* words, int64_t 
 // The lowest tile that is not done is then always held by a workgroup that waits for nothing.
 __device__ __forceinline__ bool take_item(const GatedScanArgs& a, unsigned& s_ticket, uint32_t& c, int& col) {
     uint32_t item = blockIdx.x;
-    if (a.ntiles > 1) {
+    if (a.chain) {
         if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u);
         __syncthreads();
         item = uniform32(s_ticket);
@@ -459,14 +459,13 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
             Bp[1] = fmaf(A.y, Bp[1], B.y);
         }
     };
-#pragma unroll 2
     for (int k = 0; k < w; ++k) compose(k);
     if (w == kWaves - 1) {                     // the last one does the chaining
         const float A0[2] = {Ap[0], Ap[1]}, B0[2] = {Bp[0], Bp[1]};
         const bool hard0 = hard;
         float carry[2] = {0.f, 0.f};
         compose(w);
-        if (a.ntiles > 1) {
+        if (a.chain) {
             const int64_t stride = (int64_t)a.ncols * kScanCols;
             uint64_t* mine = a.words + c * stride;
 #pragma unroll
@@ -656,14 +655,13 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
             Bp[1] = fmaf(A.y, Bp[1], B.y);
         }
     };
-#pragma unroll 2
     for (int k = kWaves - 1; k > w; --k) compose(k);
     if (w == 0) {                              // the first one does the chaining
         const float A0[2] = {Ap[0], Ap[1]}, B0[2] = {Bp[0], Bp[1]};
         const bool hard0 = hard;
         float carry[2] = {0.f, 0.f};
         compose(0);
-        if (a.ntiles > 1) {
+        if (a.chain) {
             const int64_t stride = (int64_t)a.ncols * kScanCols;
             uint64_t* mine = a.words + c * stride;
 #pragma unroll
@@ -687,7 +685,6 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
         hard = hard0;
     }
     // state that enters this wave
-#pragma unroll 2
     for (int k = 0; k < w; ++k) {
         const float2 A = sA[k][lane], B = sB[k][lane];
         const bool cut = uniform32(sHard[k]) & 1;
@@ -827,7 +824,7 @@ hipError_t reset_chain(const GatedScanArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_gated_scan(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s) {
-    if (a.ntiles > 1) {
+    if (a.chain) {
         const hipError_t e = reset_chain(a, s);
         if (e != hipSuccess) return e;
     }
@@ -845,7 +842,7 @@ hipError_t launch_gated_scan(const GatedScanArgs& a, bool bf16_io, bool vec, hip
 }
 
 hipError_t launch_gated_scan_backward(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s) {
-    if (a.ntiles > 1) {
+    if (a.chain) {
         const hipError_t e = reset_chain(a, s);
         if (e != hipSuccess) return e;
     }

@@ -80,6 +80,9 @@ def _check(status):
         raise M3Error(status, m3scan.last_error())
 
 
+_new = torch.empty_like
+
+
 def _io_code(t, name):
     if t.dtype is torch.bfloat16:
         return M3_BF16
@@ -145,9 +148,12 @@ def _pitch(t, name, shape, dtype, index):
     """Checks a tensor of rows (None passes) and returns the distance in elements between them (0: dense)."""
     if t is None:
         return 0
-    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape \
-            and t.is_contiguous():
-        return 0
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape:
+        if t.is_contiguous():
+            return 0
+        stride = t.stride()
+        if len(stride) == 2 and stride[1] == 1 and stride[0] >= shape[1] and shape[0] > 1:
+            return stride[0]
     _alike(t, name, shape, dtype, index)
     if t.is_contiguous() or t.numel() == 0:
         return 0
@@ -233,18 +239,22 @@ def m3_gated_scan_step(gate, x, h, bias=None, y=None, h_out=None, stream=None):
     if len(shape) != 2:
         raise ValueError("x must be [b, D], got %s" % (tuple(shape),))
     b, D = shape
-    dims = M3ScanDims(b, 1, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
-                      _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
-    bias_p, h_p = _dense(bias, "bias", (D,), f32, dev), _dense(h, "h", shape, f32, dev)
-    h_out_p = h_p if h_out is None else _dense(h_out, "h_out", shape, f32, dev)
-    at = _here(x, stream)
-    if at < 0:
+    dense = x.is_contiguous()
+    xp = 0 if dense else _pitch(x, "x", shape, io, dev)
+    dims = M3ScanDims(b, 1, D, _pitch(gate, "gate", shape, io, dev), xp, 0 if y is None else _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
+    bias_p = None if bias is None else _dense(bias, "bias", (D,), f32, dev)
+    h_p = h_out_p = _dense(h, "h", shape, f32, dev)
+    if h_out is not None:
+        h_out_p = _dense(h_out, "h_out", shape, f32, dev)
+    if stream is not None or dev < 0 or dev != _current_device():
         with _scope(x, stream):
             return m3_gated_scan_step(gate, x, h, bias, y, h_out)
     if y is None:
-        y = x.new_empty(shape)
-    _check(lib.m3_gated_scan_step(ctypes.byref(dims), gate.data_ptr(), x.data_ptr(), bias_p, h_p, y.data_ptr(), h_out_p,
-                                  _raw_stream(at)))
+        y = _new(x) if dense else x.new_empty(shape)
+    status = lib.m3_gated_scan_step(ctypes.byref(dims), gate.data_ptr(), x.data_ptr(), bias_p, h_p, y.data_ptr(),
+                                    h_out_p, _raw_stream(dev))
+    if status:
+        _check(status)
     return y
 
 
@@ -297,18 +307,20 @@ def m3_rmsnorm(x, residual=None, weight=None, eps=1e-5, want_y=True, quant=False
     if not shape:
         raise ValueError("x must have at least one dimension")
     D = shape[-1]
-    dims = M3NormDims(x.numel() // D if D else 0, D, _pitch(x, "x", shape, io, dev),
-                      _pitch(residual, "residual", shape, io, dev), _pitch(r_out, "r_out", shape, io, dev),
-                      _pitch(y, "y", shape, io, dev), 0, group, _io_code(x, "x"), 0, eps)
-    weight_p = _dense(weight, "weight", (D,), f32, dev)
-    at = _here(x, stream)
-    if at < 0:
+    dense = x.is_contiguous()
+    xp = 0 if dense else _pitch(x, "x", shape, io, dev)
+    pp = 0 if residual is None else _pitch(residual, "residual", shape, io, dev)
+    rp = 0 if r_out is None else _pitch(r_out, "r_out", shape, io, dev)
+    yp = 0 if y is None else _pitch(y, "y", shape, io, dev)
+    dims = M3NormDims(x.numel() // D if D else 0, D, xp, pp, rp, yp, 0, group, _io_code(x, "x"), 0, eps)
+    weight_p = None if weight is None else _dense(weight, "weight", (D,), f32, dev)
+    if stream is not None or dev < 0 or dev != _current_device():
         with _scope(x, stream):
             return m3_rmsnorm(x, residual, weight, eps, want_y, quant, group, r_out, y, q, scale)
     if r_out is None and residual is not None:
-        r_out = x.new_empty(shape)
+        r_out = _new(x) if dense else x.new_empty(shape)
     if y is None and want_y:
-        y = x.new_empty(shape)
+        y = _new(x) if dense else x.new_empty(shape)
     if quant or q is not None or scale is not None:
         sshape = (*shape[:-1], (-(-D // group) if group > 0 else 1) if D else 0)
         if q is None:
@@ -319,8 +331,10 @@ def m3_rmsnorm(x, residual=None, weight=None, eps=1e-5, want_y=True, quant=False
             scale = x.new_empty(sshape, dtype=f32)
         else:
             _dense(scale, "scale", sshape, f32, dev)
-    _check(lib.m3_rmsnorm(ctypes.byref(dims), x.data_ptr(), _ptr(residual), weight_p, _ptr(r_out), _ptr(y), _ptr(q),
-                          _ptr(scale), _raw_stream(at)))
+    status = lib.m3_rmsnorm(ctypes.byref(dims), x.data_ptr(), _ptr(residual), weight_p, _ptr(r_out), _ptr(y), _ptr(q),
+                            _ptr(scale), _raw_stream(dev))
+    if status:
+        _check(status)
     return y, r_out, q, scale
 
 
@@ -377,13 +391,13 @@ def _grad_call(fn, grads, max_norm, out, stats, workspace, stream):
         if (dtype is not f32 and dtype is not bf16) or g.get_device() != dev or not g.is_contiguous():
             _io_code(g, "gradient %s" % names[i])
             _dense(g, "gradient %s" % names[i], g.shape, dtype, dev)
-        p = g.data_ptr()
-        if dst is None or dst[i] is g:
-            o = p
-        else:
-            o = _dense(dst[i], "output %s" % names[i], g.shape, dtype, dev)
-            if o is None:
+        p = o = g.data_ptr()
+        if dst is not None:
+            t = dst[i]
+            if t is None:
                 raise ValueError("output %s is None" % names[i])
+            if t is not g:
+                o = _dense(t, "output", g.shape, dtype, dev)
         table += (p, o, g.numel(), M3_F32 if dtype is f32 else M3_BF16)
     stats_p = _dense(stats, "stats", (2,), f32, dev)
     at = _here(first, stream)

@@ -223,18 +223,23 @@ def test_workspaces():
     r = lambda n: (n + 255) // 256 * 256
     # `states` has a row per 64 tokens of a sequence (of the batch, where sequences are not longer or packed); the
     # workspace a 64-bit word per tile and channel (130 channels: 2 columns of 128) after 256 bytes, backward also a
-    # row of partial sums; bf16 forward tiles hold 128 tokens, the others 64
-    for dims, packed, rows, tiles in ((scan_dims(), 0, 10, 6), (scan_dims(seqlen=128), 0, 4, 2),
-                                      (scan_dims(seqlen=3), 0, 1, 1), (scan_dims(seqlen=1000), 1, 16, 8),
-                                      (scan_dims(seqlen=0), 0, 1, 1), (scan_dims(batch=0), 0, 1, 1)):
+    # row of partial sums; bf16 forward tiles hold 128 tokens, the others 64.  Few short sequences have a tile each,
+    # which needs no words
+    for dims, packed, rows, tiles in ((scan_dims(), 0, 10, 6), (scan_dims(seqlen=128), 0, 4, 0),
+                                      (scan_dims(batch=300, seqlen=3), 0, 15, 8), (scan_dims(seqlen=1000), 1, 16, 8),
+                                      (scan_dims(seqlen=0), 0, 1, 0), (scan_dims(batch=0), 0, 1, 0)):
         for io in (m3block.M3_BF16, m3block.M3_F32):
             dims.io = io
             ref = ctypes.byref(dims)
-            n = tiles if io == m3block.M3_BF16 else rows
+            n = tiles if io == m3block.M3_BF16 else rows          # tiles in chains
             assert lib.m3_gated_scan_chunks(ref, packed) == rows
             assert lib.m3_gated_scan_workspace_bytes(ref, packed) == (256 + r(n * 256 * 8) if n > 1 else 0)
             assert lib.m3_gated_scan_backward_workspace_bytes(ref, packed) == \
                 (256 + r(rows * 256 * 8) + rows * 130 * 4 if rows > 1 else 0)
+    short = scan_dims(batch=200, seqlen=3)
+    assert lib.m3_gated_scan_chunks(ctypes.byref(short), 0) == 200
+    assert lib.m3_gated_scan_workspace_bytes(ctypes.byref(short), 0) == 0
+    assert lib.m3_gated_scan_backward_workspace_bytes(ctypes.byref(short), 0) == 200 * 130 * 4
     for call in (FWD, BWD):
         need = getattr(lib, call.fn + "_workspace_bytes")(ctypes.byref(call.dims), 0)
         assert call(cu=0, ws_bytes=need - 1) == m3scan.M3_E_WORKSPACE
@@ -262,7 +267,7 @@ A0, A1, A2 = BASE, BASE + STRIDE, BASE + 2 * STRIDE
 
 @pytest.mark.parametrize("name", ["m3_grad_norm", "m3_grad_clip"])
 def test_gradient_refusals(name):
-    ok = [(A0, A0, 100, F), (A1, A1, 50, H)]
+    ok = [(A0, A0, 100000, F), (A1, A1, 50, H)]
     clip = name == "m3_grad_clip"
     assert grad_call(name, [(A0, A0, 100, 7)]) == m3scan.M3_E_DTYPE
     assert grad_call(name, [(A0, A0, -1, F)]) == m3scan.M3_E_DIMS
@@ -276,7 +281,7 @@ def test_gradient_refusals(name):
     assert grad_call(name, ok, stats=0) == m3scan.M3_E_NULL
     assert grad_call(name, ok, stats=BASE + 90 * STRIDE + 2) == m3scan.M3_E_ALIGN
     assert grad_call(name, ok, ws=0) == m3scan.M3_E_WORKSPACE
-    assert grad_call(name, ok, ws_bytes=16) == m3scan.M3_E_WORKSPACE        # two partial sums and their sum
+    assert grad_call(name, ok, ws_bytes=63) == m3scan.M3_E_WORKSPACE        # 7 + 1 partial sums and their sum: 72
     assert grad_call(name, ok, ws=BASE + 91 * STRIDE + 8) == m3scan.M3_E_ALIGN
     assert grad_call(name, ok, stats=A0 + 8) == m3scan.M3_E_ALIAS
     assert grad_call(name, ok, ws=A1 + 32) == m3scan.M3_E_ALIAS
@@ -302,11 +307,14 @@ def test_gradient_workspace():
     for i, t in enumerate(table):
         t.src, t.dst, t.numel, t.io = A0 + i * 4096, A0 + i * 4096, 10, F
     size = lambda n: lib.m3_grad_workspace_bytes(ctypes.cast(table, P), n)
-    assert size(0) == 0 and size(1) == 16 and size(96) == 97 * 8 and size(200) == 201 * 8
+    assert size(0) == 0 and size(1) == 0 and size(96) == 0          # few elements: one workgroup, no partial sums
+    assert size(200) == 201 * 8                                     # more tables than one
+    table[0].numel = 65537
+    assert size(1) == 6 * 8 and size(2) == 7 * 8
     table[0].numel = 16384 * 5000
     assert size(1) == 2049 * 8
     table[0].numel = 0
-    assert size(1) == 0 and size(3) == 24
+    assert size(1) == 0 and size(3) == 0
     assert lib.m3_grad_workspace_bytes(None, 3) == 0
 
 
