@@ -84,7 +84,8 @@ m3_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t n
 struct ScanPlan {
     int64_t T = 0, ntiles = 1, seq_tiles = 1, blocks = 1, seq_blocks = 1;
     int ncols = 0;
-    bool per_seq = false, chain = false;
+    bool per_seq = false, serial = false;
+    int64_t parts = 1;
     size_t words_off = 256, part_off = 0, bytes = 0;
 };
 
@@ -98,7 +99,18 @@ m3_status check_scan_dims(const m3_scan_dims* d) {
     return M3_OK;
 }
 
+// When a workgroup works its sequence off tile by tile instead of chaining tiles that run at the same time.
+// Bf16, D 4096, forward (backward): two tiles of few sequences 14.5 -> 12.9 us (4 x 256 tokens; four tiles lose: 23.1 ->
+// 25.1 us); many sequences, which fill the GPU anyway, 88 -> 79 us (161 -> 140) at 64 x 256 tokens, 91 -> 83 us at
+// 16 x 1024, but 162 -> 172 us at 8 x 2048 x 8192 channels, 16 tiles.  Packed batches never gain: their tiles wait
+// for the search of their sequences, which then adds up.
 constexpr int64_t kMaxLoneTiles = 512;   // two workgroups on each of 256 compute units
+constexpr int64_t kMaxSerialTiles = 2, kMaxFullSerialTiles = 8;
+// Workgroups that keep the GPU full: no last round of two to a compute unit that is mostly empty.
+bool fills_rounds(int64_t wgs) {
+    const int64_t slots = 2 * (int64_t)m3::device_cus(), rounds = (wgs + slots - 1) / slots;
+    return rounds > 0 && wgs * 100 >= rounds * slots * 85;
+}
 // The tiles of the forward or the backward pass, and the blocks that have a row of `states`.
 m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan* p) {
     M3_TRY(check_scan_dims(d));
@@ -106,8 +118,8 @@ m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan*
     const int64_t tile = d->io != M3_BF16 ? m3::kScanTileF32 : backward ? m3::kScanBwdTileBf16 : m3::kScanTileBf16;
     p->T = packed ? d->seqlen : d->batch * d->seqlen;
     p->ncols = (int)((d->width + m3::kScanCols - 1) / m3::kScanCols);
-    // Short sequences share tiles, unless they are so few that a tile each, and no chain between tiles, costs
-    // less: up to one round of workgroups (11 x 11 tokens of 64 channels: 12.8 -> FILL us a call).
+    // Short sequences share tiles, unless they are so few that all can have a tile of their own at the same time
+    // (then no tile waits for another, and a call is one launch).
     p->per_seq = !packed && d->batch > 0 && d->seqlen > 0 &&
                  (d->seqlen > block || d->batch * p->ncols <= kMaxLoneTiles);
     if (p->per_seq) {
@@ -119,12 +131,15 @@ m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan*
         p->ntiles = std::max<int64_t>(1, (p->T + tile - 1) / tile);
         p->blocks = std::max<int64_t>(1, (p->T + block - 1) / block);
     }
-    p->chain = (p->per_seq ? p->seq_tiles : p->ntiles) > 1;
     if (p->blocks >= kMaxCount || p->blocks * p->ncols >= kMaxCount)
         return fail(M3_E_DIMS, "%lld tokens of %lld channels: more than 2^31 blocks of 64 tokens and 128 channels",
                     (long long)p->T, (long long)d->width);
-    if (p->chain) p->part_off = p->words_off + round256((size_t)p->ntiles * p->ncols * m3::kScanCols * 8);
-    p->bytes = p->part_off + (backward && p->ntiles > 1 ? (size_t)p->ntiles * d->width * 4 : 0);
+    const int64_t wgs = p->per_seq ? d->batch * p->ncols : p->ncols;
+    p->serial = p->per_seq ? p->seq_tiles <= kMaxSerialTiles || (p->seq_tiles <= kMaxFullSerialTiles && fills_rounds(wgs))
+                           : p->ntiles <= 1;
+    p->parts = p->serial ? (p->per_seq ? d->batch : 1) : p->ntiles;
+    if (!p->serial) p->part_off = p->words_off + round256((size_t)p->ntiles * p->ncols * m3::kScanCols * 8);
+    p->bytes = p->part_off + (backward && p->parts > 1 ? (size_t)p->parts * d->width * 4 : 0);
     return M3_OK;
 }
 
@@ -139,7 +154,8 @@ void scan_args(const m3_scan_dims* d, const ScanPlan& p, const int32_t* cu, void
     a->seq_blocks = (uint32_t)p.seq_blocks;
     a->ncols = p.ncols;
     a->per_seq = p.per_seq ? 1 : 0;
-    a->chain = p.chain ? 1 : 0;
+    a->serial = p.serial ? 1 : 0;
+    a->parts = p.parts;
     a->ticket = (unsigned*)ws;
     a->words = (uint64_t*)((char*)ws + p.words_off);
     a->part = (float*)((char*)ws + p.part_off);

@@ -33,18 +33,19 @@ struct GatedScanArgs {
     void* dx;
     float* dbias;
     float* dh_in;
-    float* part;            // [ntiles, D] each tile's share of dbias (ntiles > 1)
+    float* part;            // [parts, D] each workgroup's share of dbias (parts > 1)
+    int64_t parts;
     int64_t b, L, T;        // sequences; tokens of each (dense); tokens of all
     int64_t D;
     int64_t gate_p, x_p, y_p, dgate_p, dx_p;   // pitches in bytes
-    uint64_t* words;        // [ntiles, ncols * kScanCols] chain words (chain)
+    uint64_t* words;        // [ntiles, ncols * kScanCols] chain words (not serial)
     unsigned* ticket;
     int64_t ntiles;
     uint32_t seq_tiles;     // tiles, and blocks, per sequence (per_seq)
     uint32_t seq_blocks;
     int ncols;              // column blocks
     int per_seq;
-    int chain;              // tiles wait for others: words and ticket are there
+    int serial;             // a workgroup takes a sequence (flat: the batch) tile by tile; else tiles are chained
 };
 
 hipError_t launch_gated_scan(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s);

@@ -14,7 +14,7 @@ namespace {
 constexpr int kWaves = 8;   // waves per tile; each holds kSteps consecutive tokens in registers
 template <typename T> constexpr int kFwdSteps = sizeof(T) == 2 ? 16 : 8;
 template <typename T> constexpr int kBwdSteps = sizeof(T) == 2 ? kScanBwdTileBf16 / kWaves : 8;
-constexpr uint32_t kTogether = 4;
+constexpr uint32_t kSideBySide = 4;
 template <typename T> constexpr int kFwdOcc = 4;   // waves per SIMD to leave registers for
 template <typename T> constexpr int kBwdOcc = 4;
 static_assert(kWaves * kFwdSteps<bf16> == kScanTileBf16 && kWaves * kFwdSteps<float> == kScanTileF32 &&
@@ -173,14 +173,15 @@ struct Tile {
 };
 __device__ __forceinline__ uint32_t uniform32(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <int TILE, bool FLAT>
+template <int TILE, bool FLAT, bool SERIAL>
 __device__ __forceinline__ Tile tile_of(const GatedScanArgs& a, uint32_t c) {
     Tile t;
     t.c = c;
     int64_t left;
     if constexpr (!FLAT) {
-        // kTogether sequences side by side, tile by tile, then the next ones: of the tiles that run at the
-        // same time fewer belong to one chain.
+        // Chained: kTogether sequences side by side, tile by tile, then the next ones: of the tiles that run at
+        // the same time fewer belong to one chain.  Serial: sequence by sequence.
+        constexpr uint32_t kTogether = SERIAL ? 1 : kSideBySide;
         const uint32_t n = a.seq_tiles, group = uniform32(c / (kTogether * n)), r = c - group * (kTogether * n);
         const uint32_t left_over = (uint32_t)a.b - group * kTogether, size = left_over < kTogether ? left_over : kTogether;
         const uint32_t j = uniform32(r / size);
@@ -312,17 +313,14 @@ __global__ __launch_bounds__(256) void chain_reset_kernel(uint4* words, int64_t 
 }
 
 // ---------------------------------------------------------------------------------- forward
-// The number of a workgroup's tile and column: its place in the grid, or, where tiles wait for each
-// other, from a counter, so that tiles are begun in chain order whatever order workgroups start in.
-// The lowest tile that is not done is then always held by a workgroup that waits for nothing.
+// Chained tiles: a workgroup's tile and column come from a counter, so that tiles are begun in chain order
+// whatever order workgroups start in.  The lowest tile that is not done is then always held by a
+// workgroup that waits for nothing.
 __device__ __forceinline__ bool take_item(const GatedScanArgs& a, unsigned& s_ticket, uint32_t& c, int& col) {
-    uint32_t item = blockIdx.x;
-    if (a.chain) {
-        if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u);
-        __syncthreads();
-        item = uniform32(s_ticket);
-        if (item >= (uint32_t)a.ntiles * (uint32_t)a.ncols) return false;
-    }
+    if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u);
+    __syncthreads();
+    const uint32_t item = uniform32(s_ticket);
+    if (item >= (uint32_t)a.ntiles * (uint32_t)a.ncols) return false;
     c = uniform32(item / (uint32_t)a.ncols);
     col = (int)(item - c * (uint32_t)a.ncols);
     return true;
@@ -366,19 +364,21 @@ __device__ __forceinline__ void pass_empty(const GatedScanArgs& a, uint32_t c, c
     }
 }
 
-template <typename T, bool VEC, bool FLAT>
-__global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(const GatedScanArgs a) {
+template <typename T, bool FLAT>
+struct FwdShared {
+    float2 sA[kWaves][64], sB[kWaves][64], sCarry[64];
+    int sHard[kWaves];   // bit 0: the wave's tokens hold a sequence start; bit 1: its first token is one
+    Marks<FLAT ? kWaves * kFwdSteps<T> : 1> marks;
+    unsigned sTicket;
+};
+
+// One tile.  SERIAL: `state`, the last wave's, is the state before the tile, and then the one after it; else it
+// comes from the chain.
+template <typename T, bool VEC, bool FLAT, bool SERIAL>
+__device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T, FLAT>& sh, uint32_t c, int col, int lane,
+                                             int w, float (&state)[2]) {
     constexpr int N = kFwdSteps<T>, TILE = kWaves * N;
-    __shared__ float2 sA[kWaves][64], sB[kWaves][64], sCarry[64];
-    __shared__ int sHard[kWaves];   // bit 0: the wave's tokens hold a sequence start; bit 1: its first token is one
-    __shared__ Marks<FLAT ? TILE : 1> marks;
-    __shared__ unsigned sTicket;
-    const int lane = threadIdx.x & 63;
-    const int w = uniform32(threadIdx.x >> 6);
-    uint32_t c;
-    int col;
-    if (!take_item(a, sTicket, c, col)) return;
-    const Tile tile = tile_of<TILE, FLAT>(a, c);
+    const Tile tile = tile_of<TILE, FLAT, SERIAL>(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
     const int64_t tw = tile.t0 + w * N;
     const int nv = clamp_rows(tile.nv - w * N, N);
@@ -393,9 +393,9 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
             load_rows(x, rows_at(a.x, tw * a.x_p), (int)a.x_p, nv, cols);
         }
         if constexpr (FLAT) {
-            find_marks(a, tile, marks);
-            starts = mark_bits<N>(marks.starts, w * N);
-            ends = mark_bits<N>(marks.ends, w * N);
+            find_marks(a, tile, sh.marks);
+            starts = mark_bits<N>(sh.marks.starts, w * N);
+            ends = mark_bits<N>(sh.marks.ends, w * N);
         } else {                               // a sequence's first and last token
             if (w == 0 && tile.before == 0) starts = 1;
             if (tile.after == 0 && nv > 0 && w * N + nv == tile.nv) ends = 1u << (nv - 1);
@@ -420,7 +420,7 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
             }
     }
     auto seq_at = [&](int i) -> int64_t {
-        if constexpr (FLAT) return mark_seq(marks, w * N + i);
+        if constexpr (FLAT) return mark_seq(sh.marks, w * N + i);
         else return tile.seq;
     };
     float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};   // the wave's map
@@ -438,16 +438,16 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
         A[1] *= keep[i][1];
         step(i, B);
     }
-    sA[w][lane] = make_float2(A[0], A[1]);
-    sB[w][lane] = make_float2(B[0], B[1]);
-    if (lane == 0) sHard[w] = (starts != 0 ? 1 : 0) | (starts & 1 ? 2 : 0);
+    sh.sA[w][lane] = make_float2(A[0], A[1]);
+    sh.sB[w][lane] = make_float2(B[0], B[1]);
+    if (lane == 0) sh.sHard[w] = (starts != 0 ? 1 : 0) | (starts & 1 ? 2 : 0);
     __syncthreads();
     // the map of the waves before this one
     float Ap[2] = {1.f, 1.f}, Bp[2] = {0.f, 0.f};
     bool hard = false;                         // a start among them: what came before does not matter
     auto compose = [&](int k) {
-        const float2 A = sA[k][lane], B = sB[k][lane];
-        if (uniform32(sHard[k]) & 1) {
+        const float2 A = sh.sA[k][lane], B = sh.sB[k][lane];
+        if (uniform32(sh.sHard[k]) & 1) {
             hard = true;
             Ap[0] = Ap[1] = 0.f;
             Bp[0] = B.x;
@@ -465,12 +465,19 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
         const bool hard0 = hard;
         float carry[2] = {0.f, 0.f};
         compose(w);
-        if (a.chain) {
+        if constexpr (SERIAL) {
+            const bool starts_here = (uniform32(sh.sHard[0]) & 2) != 0;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                carry[v] = starts_here ? 0.f : state[v];
+                state[v] = hard ? Bp[v] : fmaf(Ap[v], carry[v], Bp[v]);
+            }
+        } else {
             const int64_t stride = (int64_t)a.ncols * kScanCols;
             uint64_t* mine = a.words + c * stride;
 #pragma unroll
             for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], hard ? final_word(Bp[v]) : map_word(Ap[v], Bp[v]));
-            const bool starts_here = (uniform32(sHard[0]) & 2) != 0;
+            const bool starts_here = (uniform32(sh.sHard[0]) & 2) != 0;
             if (tile.before > 0 && tile.nv > 0 && !starts_here) {
                 const int64_t step = -tile.link;
                 chain_wait<sizeof(T) == 2 ? 4 : 8>(a.words, stride, c + step, step, tile.before, cols.d, carry);
@@ -480,7 +487,7 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
                 for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], final_word(fmaf(Ap[v], carry[v], Bp[v])));
             }
         }
-        sCarry[lane] = make_float2(carry[0], carry[1]);
+        sh.sCarry[lane] = make_float2(carry[0], carry[1]);
         Ap[0] = A0[0]; Ap[1] = A0[1];
         Bp[0] = B0[0]; Bp[1] = B0[1];
         hard = hard0;
@@ -488,7 +495,7 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
     __syncthreads();
     float h[2];
     {
-        const float2 cy = sCarry[lane];
+        const float2 cy = sh.sCarry[lane];
         h[0] = hard ? Bp[0] : fmaf(Ap[0], cy.x, Bp[0]);
         h[1] = hard ? Bp[1] : fmaf(Ap[1], cy.y, Bp[1]);
     }
@@ -518,24 +525,47 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
     if (FLAT && w == 0) pass_empty(a, c, cols, a.h_in, a.h_out);
 }
 
+// SERIAL: a workgroup takes one sequence (FLAT: the whole batch) tile by tile: no chain to wait for, none to
+// reset.  For chains so short, or sequences so many, that the tiles need not run at the same time.
+template <typename T, bool VEC, bool FLAT, bool SERIAL>
+__global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(const GatedScanArgs a) {
+    __shared__ FwdShared<T, FLAT> sh;
+    const int lane = threadIdx.x & 63;
+    const int w = uniform32(threadIdx.x >> 6);
+    float state[2] = {0.f, 0.f};
+    if constexpr (SERIAL) {
+        const uint32_t seq = uniform32(blockIdx.x / (uint32_t)a.ncols), n = FLAT ? (uint32_t)a.ntiles : a.seq_tiles;
+        const int col = (int)(blockIdx.x - seq * (uint32_t)a.ncols);
+        for (uint32_t j = 0; j < n; ++j) {
+            if (j > 0) __syncthreads();        // the tile before is done with the shared memory
+            forward_tile<T, VEC, FLAT, true>(a, sh, seq * n + j, col, lane, w, state);
+        }
+    } else {
+        uint32_t c;
+        int col;
+        if (take_item(a, sh.sTicket, c, col)) forward_tile<T, VEC, FLAT, false>(a, sh, c, col, lane, w, state);
+    }
+}
+
 // --------------------------------------------------------------------------------- backward
 // With G_t = (1 - z_t) l_t, what flows from token t to h_{t-1}: l_t = dy_t + G_{t+1}, so backwards
 // G_t = keep_t G_{t+1} + keep_t dy_t, an affine map again, and the same chain in the other
 // direction.  A sequence's last token takes dh_out for G_{t+1}.
-template <typename T, bool VEC, bool FLAT>
-__global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_kernel(const GatedScanArgs a) {
+template <typename T, bool FLAT>
+struct BwdShared {
+    float2 sA[kWaves][64], sB[kWaves][64], sRA[kWaves][64], sRB[kWaves][64], sCarry[64];
+    int sHard[kWaves];   // bit 0: holds a sequence start; 1: holds an end; 2: its last token is an end
+    Marks<FLAT ? kWaves * kBwdSteps<T> : 1> marks;
+    unsigned sTicket;
+};
+
+// One tile.  SERIAL: `state`, the first wave's, is what flows in from behind the tile, and then what flows out
+// of it; else it comes from the chain.  `sum`: the wave's share of dbias grows.
+template <typename T, bool VEC, bool FLAT, bool SERIAL>
+__device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<T, FLAT>& sh, uint32_t c, int col,
+                                              int lane, int w, float (&state)[2], float (&sum)[2]) {
     constexpr int N = kBwdSteps<T>, TILE = kWaves * N;
-    __shared__ float2 sA[kWaves][64], sB[kWaves][64], sRA[kWaves][64], sRB[kWaves][64], sCarry[64];
-    __shared__ int sHard[kWaves];   // bit 0: holds a sequence start; 1: holds an end; 2: its last token is an end
-    __shared__ Marks<FLAT ? TILE : 1> marks;
-    __shared__ unsigned sTicket;
-    const int lane = threadIdx.x & 63;
-    const int w = uniform32(threadIdx.x >> 6);
-    uint32_t c;
-    int col;
-    if (!take_item(a, sTicket, c, col)) return;
-    c = (uint32_t)a.ntiles - 1 - c;            // from the last tile to the first
-    const Tile tile = tile_of<TILE, FLAT>(a, c);
+    const Tile tile = tile_of<TILE, FLAT, SERIAL>(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
     const int64_t tw = tile.t0 + w * N;
     const int nv = clamp_rows(tile.nv - w * N, N);
@@ -553,9 +583,9 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
             load_rows(dy, rows_at(a.dy, tw * a.y_p), (int)a.y_p, nv, cols);
         }
         if constexpr (FLAT) {
-            find_marks(a, tile, marks);
-            starts = mark_bits<N>(marks.starts, w * N);
-            ends = mark_bits<N>(marks.ends, w * N);
+            find_marks(a, tile, sh.marks);
+            starts = mark_bits<N>(sh.marks.starts, w * N);
+            ends = mark_bits<N>(sh.marks.ends, w * N);
         } else {                               // a sequence's first and last token
             if (w == 0 && tile.before == 0) starts = 1;
             if (tile.after == 0 && nv > 0 && w * N + nv == tile.nv) ends = 1u << (nv - 1);
@@ -578,7 +608,7 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
             }
     }
     auto seq_at = [&](int i) -> int64_t {
-        if constexpr (FLAT) return mark_seq(marks, w * N + i);
+        if constexpr (FLAT) return mark_seq(sh.marks, w * N + i);
         else return tile.seq;
     };
     {   // the wave's maps, forwards and backwards
@@ -628,12 +658,12 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
                 }
             }
         }
-        sA[w][lane] = make_float2(A[0], A[1]);
-        sB[w][lane] = make_float2(B[0], B[1]);
-        sRA[w][lane] = make_float2(RA[0], RA[1]);
-        sRB[w][lane] = make_float2(RB[0], RB[1]);
+        sh.sA[w][lane] = make_float2(A[0], A[1]);
+        sh.sB[w][lane] = make_float2(B[0], B[1]);
+        sh.sRA[w][lane] = make_float2(RA[0], RA[1]);
+        sh.sRB[w][lane] = make_float2(RB[0], RB[1]);
         if (lane == 0)
-            sHard[w] = (starts != 0 ? 1 : 0) | (ends != 0 ? 2 : 0) | (nv > 0 && ((ends >> (nv - 1)) & 1) ? 4 : 0);
+            sh.sHard[w] = (starts != 0 ? 1 : 0) | (ends != 0 ? 2 : 0) | (nv > 0 && ((ends >> (nv - 1)) & 1) ? 4 : 0);
     }
     forget(x);
     forget(dy);
@@ -642,8 +672,8 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
     float Ap[2] = {1.f, 1.f}, Bp[2] = {0.f, 0.f};
     bool hard = false;
     auto compose = [&](int k) {
-        const float2 A = sRA[k][lane], B = sRB[k][lane];
-        if (uniform32(sHard[k]) & 2) {
+        const float2 A = sh.sRA[k][lane], B = sh.sRB[k][lane];
+        if (uniform32(sh.sHard[k]) & 2) {
             hard = true;
             Ap[0] = Ap[1] = 0.f;
             Bp[0] = B.x;
@@ -661,15 +691,21 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
         const bool hard0 = hard;
         float carry[2] = {0.f, 0.f};
         compose(0);
-        if (a.chain) {
+        // nothing enters from behind when the tile's last token ends a sequence, or tokens end here
+        int last = 0;
+        for (int k = 0; k < kWaves; ++k) last = tile.nv > k * N ? sh.sHard[k] : last;
+        const bool ends_here = tile.nv == 0 || (uniform32(last) & 4) != 0;
+        if constexpr (SERIAL) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                carry[v] = ends_here ? 0.f : state[v];
+                state[v] = hard ? Bp[v] : fmaf(Ap[v], carry[v], Bp[v]);
+            }
+        } else {
             const int64_t stride = (int64_t)a.ncols * kScanCols;
             uint64_t* mine = a.words + c * stride;
 #pragma unroll
             for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], hard ? final_word(Bp[v]) : map_word(Ap[v], Bp[v]));
-            // nothing enters from behind when the tile's last token ends a sequence, or tokens end here
-            int last = 0;
-            for (int k = 0; k < kWaves; ++k) last = tile.nv > k * N ? sHard[k] : last;
-            const bool ends_here = tile.nv == 0 || (uniform32(last) & 4) != 0;
             if (tile.after > 0 && !ends_here) {
                 const int64_t step = tile.link;
                 chain_wait<4>(a.words, stride, c + step, step, tile.after, cols.d, carry);
@@ -679,15 +715,15 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
                 for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], final_word(fmaf(Ap[v], carry[v], Bp[v])));
             }
         }
-        sCarry[lane] = make_float2(carry[0], carry[1]);
+        sh.sCarry[lane] = make_float2(carry[0], carry[1]);
         Ap[0] = A0[0]; Ap[1] = A0[1];
         Bp[0] = B0[0]; Bp[1] = B0[1];
         hard = hard0;
     }
     // state that enters this wave
     for (int k = 0; k < w; ++k) {
-        const float2 A = sA[k][lane], B = sB[k][lane];
-        const bool cut = uniform32(sHard[k]) & 1;
+        const float2 A = sh.sA[k][lane], B = sh.sB[k][lane];
+        const bool cut = uniform32(sh.sHard[k]) & 1;
         h[0] = cut ? B.x : fmaf(A.x, h[0], B.x);
         h[1] = cut ? B.y : fmaf(A.y, h[1], B.y);
     }
@@ -706,12 +742,11 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
     __syncthreads();
     float G[2];
     {
-        const float2 cy = sCarry[lane];
+        const float2 cy = sh.sCarry[lane];
         G[0] = hard ? Bp[0] : fmaf(Ap[0], cy.x, Bp[0]);
         G[1] = hard ? Bp[1] : fmaf(Ap[1], cy.y, Bp[1]);
     }
     // backwards
-    float sum[2] = {0.f, 0.f};
     const rsrc_t gr = rows_at(a.dgate, tw * a.dgate_p), xr = rows_at(a.dx, tw * a.dx_p);
     int grow = (nv - 1) * (int)a.dgate_p, xrow = (nv - 1) * (int)a.dx_p;
     auto token = [&](int i) {
@@ -742,21 +777,50 @@ __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_k
             }
         }
     }
-    if (a.dbias) {   // the tile's share: waves summed in order
-        sRA[w][lane] = make_float2(sum[0], sum[1]);
-        __syncthreads();
-        if (w == 0) {
-            float2 t = sRA[0][lane];
-#pragma unroll
-            for (int k = 1; k < kWaves; ++k) {
-                t.x += sRA[k][lane].x;
-                t.y += sRA[k][lane].y;
-            }
-            const float o[2] = {t.x, t.y};
-            to_seq(a.ntiles > 1 ? a.part : a.dbias, a.ntiles > 1 ? c : 0, a.D, cols, o);
-        }
-    }
     if (FLAT && w == 0 && a.dh_in) pass_empty(a, c, cols, a.dh_out, a.dh_in);
+}
+
+// the workgroup's share of dbias: its waves' added in order
+template <typename T, bool VEC, bool FLAT>
+__device__ __forceinline__ void add_dbias(const GatedScanArgs& a, BwdShared<T, FLAT>& sh, uint32_t row, int col, int lane,
+                                          int w, const float (&sum)[2]) {
+    if (a.dbias == nullptr) return;
+    __syncthreads();
+    sh.sA[w][lane] = make_float2(sum[0], sum[1]);
+    __syncthreads();
+    if (w != 0) return;
+    float2 t = sh.sA[0][lane];
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) {
+        t.x += sh.sA[k][lane].x;
+        t.y += sh.sA[k][lane].y;
+    }
+    const float o[2] = {t.x, t.y};
+    to_seq(a.parts > 1 ? a.part : a.dbias, a.parts > 1 ? row : 0, a.D, Cols<T, VEC>(col, lane, a.D), o);
+}
+
+template <typename T, bool VEC, bool FLAT, bool SERIAL>
+__global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_kernel(const GatedScanArgs a) {
+    __shared__ BwdShared<T, FLAT> sh;
+    const int lane = threadIdx.x & 63;
+    const int w = uniform32(threadIdx.x >> 6);
+    float state[2] = {0.f, 0.f}, sum[2] = {0.f, 0.f};
+    if constexpr (SERIAL) {
+        const uint32_t seq = uniform32(blockIdx.x / (uint32_t)a.ncols), n = FLAT ? (uint32_t)a.ntiles : a.seq_tiles;
+        const int col = (int)(blockIdx.x - seq * (uint32_t)a.ncols);
+        for (uint32_t j = n; j-- > 0;) {       // from the last tile to the first
+            if (j + 1 < n) __syncthreads();
+            backward_tile<T, VEC, FLAT, true>(a, sh, seq * n + j, col, lane, w, state, sum);
+        }
+        add_dbias<T, VEC>(a, sh, seq, col, lane, w, sum);
+    } else {
+        uint32_t c;
+        int col;
+        if (!take_item(a, sh.sTicket, c, col)) return;
+        c = (uint32_t)a.ntiles - 1 - c;
+        backward_tile<T, VEC, FLAT, false>(a, sh, c, col, lane, w, state, sum);
+        add_dbias<T, VEC>(a, sh, c, col, lane, w, sum);
+    }
 }
 
 // ------------------------------------------------------------------------------- one token
@@ -823,41 +887,48 @@ hipError_t reset_chain(const GatedScanArgs& a, hipStream_t s) {
 
 }  // namespace
 
+#define M3_SCAN(KERNEL, T, VEC)                                                                                  \
+    do {                                                                                                          \
+        if (a.serial && flat) hipLaunchKernelGGL((KERNEL<T, VEC, true, true>), grid, block, 0, s, a);             \
+        else if (a.serial) hipLaunchKernelGGL((KERNEL<T, VEC, false, true>), grid, block, 0, s, a);               \
+        else if (flat) hipLaunchKernelGGL((KERNEL<T, VEC, true, false>), grid, block, 0, s, a);                   \
+        else hipLaunchKernelGGL((KERNEL<T, VEC, false, false>), grid, block, 0, s, a);                            \
+    } while (0)
+#define M3_SCAN_TYPES(KERNEL)                            \
+    do {                                                 \
+        if (bf16_io && vec) M3_SCAN(KERNEL, bf16, true); \
+        else if (bf16_io) M3_SCAN(KERNEL, bf16, false);  \
+        else if (vec) M3_SCAN(KERNEL, float, true);      \
+        else M3_SCAN(KERNEL, float, false);              \
+    } while (0)
+
+namespace {
+dim3 scan_grid(const GatedScanArgs& a) {
+    return dim3((unsigned)((a.serial ? (a.per_seq ? a.b : 1) : a.ntiles) * a.ncols));
+}
+}  // namespace
+
 hipError_t launch_gated_scan(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s) {
-    if (a.chain) {
+    if (!a.serial) {
         const hipError_t e = reset_chain(a, s);
         if (e != hipSuccess) return e;
     }
-    const dim3 grid((unsigned)(a.ntiles * a.ncols)), block(kWaves * 64);
+    const dim3 grid = scan_grid(a), block(kWaves * 64);
     const bool flat = !a.per_seq;
-#define M3_SCAN(T, VEC)                                                                                   \
-    if (flat) hipLaunchKernelGGL((gated_scan_kernel<T, VEC, true>), grid, block, 0, s, a);                \
-    else hipLaunchKernelGGL((gated_scan_kernel<T, VEC, false>), grid, block, 0, s, a)
-    if (bf16_io && vec) { M3_SCAN(bf16, true); }
-    else if (bf16_io) { M3_SCAN(bf16, false); }
-    else if (vec) { M3_SCAN(float, true); }
-    else { M3_SCAN(float, false); }
-#undef M3_SCAN
+    M3_SCAN_TYPES(gated_scan_kernel);
     return hipGetLastError();
 }
 
 hipError_t launch_gated_scan_backward(const GatedScanArgs& a, bool bf16_io, bool vec, hipStream_t s) {
-    if (a.chain) {
+    if (!a.serial) {
         const hipError_t e = reset_chain(a, s);
         if (e != hipSuccess) return e;
     }
-    const dim3 grid((unsigned)(a.ntiles * a.ncols)), block(kWaves * 64);
+    const dim3 grid = scan_grid(a), block(kWaves * 64);
     const bool flat = !a.per_seq;
-#define M3_SCAN(T, VEC)                                                                                   \
-    if (flat) hipLaunchKernelGGL((gated_scan_backward_kernel<T, VEC, true>), grid, block, 0, s, a);                \
-    else hipLaunchKernelGGL((gated_scan_backward_kernel<T, VEC, false>), grid, block, 0, s, a)
-    if (bf16_io && vec) { M3_SCAN(bf16, true); }
-    else if (bf16_io) { M3_SCAN(bf16, false); }
-    else if (vec) { M3_SCAN(float, true); }
-    else { M3_SCAN(float, false); }
-#undef M3_SCAN
+    M3_SCAN_TYPES(gated_scan_backward_kernel);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.dbias && a.ntiles > 1) e = launch_column_sum(a.part, a.ntiles, a.D, a.dbias, s);
+    if (e == hipSuccess && a.dbias && a.parts > 1) e = launch_column_sum(a.part, a.parts, a.D, a.dbias, s);
     return e;
 }
 

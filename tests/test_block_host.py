@@ -56,7 +56,7 @@ def test_structures_match_the_header(tmp_path):
     assert got == want
 
 
-def scan_dims(batch=2, seqlen=300, width=130, io=m3block.M3_BF16, flags=0, **pitch):
+def scan_dims(batch=2, seqlen=1000, width=130, io=m3block.M3_BF16, flags=0, **pitch):
     d = m3block.M3ScanDims(batch, seqlen, width, 0, 0, 0, 0, 0, io, flags)
     for k, v in pitch.items():
         setattr(d, k, v)
@@ -221,25 +221,32 @@ def test_norm_outputs():
 def test_workspaces():
     lib = m3block.load()
     r = lambda n: (n + 255) // 256 * 256
-    # `states` has a row per 64 tokens of a sequence (of the batch, where sequences are not longer or packed); the
-    # workspace a 64-bit word per tile and channel (130 channels: 2 columns of 128) after 256 bytes, backward also a
-    # row of partial sums; bf16 forward tiles hold 128 tokens, the others 64.  Few short sequences have a tile each,
-    # which needs no words
-    for dims, packed, rows, tiles in ((scan_dims(), 0, 10, 6), (scan_dims(seqlen=128), 0, 4, 0),
-                                      (scan_dims(batch=300, seqlen=3), 0, 15, 8), (scan_dims(seqlen=1000), 1, 16, 8),
-                                      (scan_dims(seqlen=0), 0, 1, 0), (scan_dims(batch=0), 0, 1, 0)):
+    # `states` has a row per 64 tokens of a sequence (of the batch, where it is packed or its sequences are short and
+    # many).  Chained tiles (bf16 forward 128 tokens, else 64) need a 64-bit word per tile and channel (130 channels: 2
+    # columns of 128) after 256 bytes; sequences of up to 2 tiles, and of up to 8 where they fill the GPU with a
+    # workgroup each, are worked off without.  Backward also needs a row of partial sums per workgroup.
+    words = lambda n: 256 + r(n * 256 * 8)
+    row = 130 * 4
+    for kw, packed, rows, fwd16, fwd32, bwd in (
+            (dict(), 0, 32, words(16), words(32), words(32) + 32 * row),
+            (dict(), 1, 16, words(8), words(16), words(16) + 16 * row),
+            (dict(seqlen=300), 0, 10, words(6), words(10), words(10) + 10 * row),
+            (dict(seqlen=300), 1, 5, words(3), words(5), words(5) + 5 * row),
+            (dict(seqlen=256), 0, 8, 0, words(8), words(8) + 8 * row),
+            (dict(seqlen=128), 0, 4, 0, 0, 2 * row),
+            (dict(seqlen=128), 1, 2, 0, words(2), words(2) + 2 * row),
+            (dict(seqlen=64), 1, 1, 0, 0, 0),
+            (dict(batch=256, seqlen=500), 0, 2048, 0, 0, 256 * row),               # 512 workgroups: a full round
+            (dict(batch=256, seqlen=1000), 0, 4096, 0, words(4096), words(4096) + 4096 * row),
+            (dict(batch=200, seqlen=1000), 0, 200 * 16, words(200 * 8), words(200 * 16), words(3200) + 3200 * row),
+            (dict(batch=200, seqlen=3), 0, 200, 0, 0, 200 * row),
+            (dict(batch=300, seqlen=3), 0, 15, words(8), words(15), words(15) + 15 * row),
+            (dict(seqlen=0), 0, 1, 0, 0, 0), (dict(batch=0), 0, 1, 0, 0, 0)):
         for io in (m3block.M3_BF16, m3block.M3_F32):
-            dims.io = io
-            ref = ctypes.byref(dims)
-            n = tiles if io == m3block.M3_BF16 else rows          # tiles in chains
+            ref = ctypes.byref(scan_dims(io=io, **kw))
             assert lib.m3_gated_scan_chunks(ref, packed) == rows
-            assert lib.m3_gated_scan_workspace_bytes(ref, packed) == (256 + r(n * 256 * 8) if n > 1 else 0)
-            assert lib.m3_gated_scan_backward_workspace_bytes(ref, packed) == \
-                (256 + r(rows * 256 * 8) + rows * 130 * 4 if rows > 1 else 0)
-    short = scan_dims(batch=200, seqlen=3)
-    assert lib.m3_gated_scan_chunks(ctypes.byref(short), 0) == 200
-    assert lib.m3_gated_scan_workspace_bytes(ctypes.byref(short), 0) == 0
-    assert lib.m3_gated_scan_backward_workspace_bytes(ctypes.byref(short), 0) == 200 * 130 * 4
+            assert lib.m3_gated_scan_workspace_bytes(ref, packed) == (fwd16 if io == m3block.M3_BF16 else fwd32), kw
+            assert lib.m3_gated_scan_backward_workspace_bytes(ref, packed) == bwd, kw
     for call in (FWD, BWD):
         need = getattr(lib, call.fn + "_workspace_bytes")(ctypes.byref(call.dims), 0)
         assert call(cu=0, ws_bytes=need - 1) == m3scan.M3_E_WORKSPACE

@@ -85,6 +85,27 @@ def test_dense(io, b, L, d):
     check(c, [L] * b, run(c, [L] * b, packed=False))
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_a_workgroup_per_sequence(io):
+    """As many sequences as fill the GPU are worked off one by one by their workgroups, without chains: sampled
+    sequences against the formulas, the bias's gradient against that of the packed call, whose tiles are chained (each
+    term off by at most 9 units per token, and the sums by their additions: 48 and one per 64 tiles)."""
+    b, L, d = 512, 330, 130
+    c = draw(b * L, d, b, IO[io], 17)
+    got = run(c, [L] * b, packed=False)
+    for s in (0, 200, 511):
+        one = {k: (v if v is None or k == "bias" else v[s:s + 1] if k in ("h_in", "dh_out") else v[s * L:(s + 1) * L])
+               for k, v in c.items()}
+        ref = scan(one["gate"], one["x"], one["bias"], one["h_in"], [L], one["dy"], one["dh_out"])
+        for k in ("y", "dgate", "dx"):
+            assert_close(got[k][s * L:(s + 1) * L], ref[k], ref["tol"][k], k)
+        for k in ("h_out", "dh_in"):
+            assert_close(got[k][s:s + 1], ref[k], ref["tol"][k], k)
+    other = run(c, [L] * b, packed=True)
+    bound = 2 * got["dgate"].double().abs().sum(0) * (9 * L + 48 + b * L / 4096) * 2.0 ** -24
+    assert ((got["dbias"].double() - other["dbias"].double()).abs() <= bound).all()
+
+
 PACKED = [[1], [0], [0, 0, 5, 0], [128, 128], [127, 1, 129], [1] * 40, [3, 0, 250, 1, 0, 16, 400], [0, 513, 0]]
 
 
