@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 
 import torch
 
@@ -154,6 +155,9 @@ def _pitch(t, name, shape, dtype, index):
         stride = t.stride()
         if len(stride) == 2 and stride[1] == 1 and stride[0] >= shape[1] and shape[0] > 1:
             return stride[0]
+        if len(stride) == 3 and stride[2] == 1 and stride[1] >= shape[2] and shape[1] > 1 \
+                and stride[0] == shape[1] * stride[1]:
+            return stride[1]
     _alike(t, name, shape, dtype, index)
     if t.is_contiguous() or t.numel() == 0:
         return 0
@@ -196,6 +200,15 @@ def _scan_dims(x, cu_seqlens):
     return cu_seqlens.shape[0] - 1, x.shape[0], x.shape[1]
 
 
+@functools.lru_cache(maxsize=1024)
+def _scan_sizes(b, L, D, io, packed, dev):
+    """Rows of `states`, and the workspace bytes of the forward and the backward pass on device `dev`."""
+    lib = load()
+    ref = ctypes.byref(M3ScanDims(b, L, D, 0, 0, 0, 0, 0, io, 0))
+    return (lib.m3_gated_scan_chunks(ref, packed), lib.m3_gated_scan_workspace_bytes(ref, packed),
+            lib.m3_gated_scan_backward_workspace_bytes(ref, packed))
+
+
 def m3_gated_scan(gate, x, bias=None, h_in=None, cu_seqlens=None, y=None, h_out=None, states=None,
                   save_states=False, workspace=None, stream=None):
     """h_t = (1 - z_t) h_{t-1} + z_t x_t with z_t = sigmoid(gate_t + bias), over [b, L, D] or, with
@@ -213,20 +226,19 @@ def m3_gated_scan(gate, x, bias=None, h_in=None, cu_seqlens=None, y=None, h_out=
     if at < 0:
         with _scope(x, stream):
             return m3_gated_scan(gate, x, bias, h_in, cu_seqlens, y, h_out, states, save_states, workspace)
-    ref = ctypes.byref(dims)
+    rows, need, _ = _scan_sizes(b, L, D, dims.io, packed, at)
     if y is None:
         y = x.new_empty(shape)
     if h_out is None:
         h_out = x.new_empty((b, D), dtype=f32)
         h_out_p = h_out.data_ptr()
     if states is not None or save_states:
-        want = (lib.m3_gated_scan_chunks(ref, packed), D)
         if states is None:
-            states = x.new_empty(want, dtype=f32)
+            states = x.new_empty((rows, D), dtype=f32)
         else:
-            _dense(states, "states", want, f32, dev)
-    workspace, ws_bytes = _workspace(workspace, lib.m3_gated_scan_workspace_bytes(ref, packed), x)
-    _check(lib.m3_gated_scan(ref, _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, y.data_ptr(), h_out_p,
+            _dense(states, "states", (rows, D), f32, dev)
+    workspace, ws_bytes = _workspace(workspace, need, x)
+    _check(lib.m3_gated_scan(ctypes.byref(dims), _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, y.data_ptr(), h_out_p,
                              _ptr(states), _ptr(workspace), ws_bytes, _raw_stream(at)))
     return (y, h_out) if states is None else (y, h_out, states)
 
@@ -275,12 +287,14 @@ def m3_gated_scan_backward(gate, x, dy, states, bias=None, h_in=None, dh_out=Non
     dh_out_p = _dense(dh_out, "dh_out", (b, D), f32, dev)
     _dense(g.get("bias"), "grad bias", (D,), f32, dev)
     _dense(g.get("h_in"), "grad h_in", (b, D), f32, dev)
-    ref = ctypes.byref(dims)
-    states_p = _dense(states, "states", (lib.m3_gated_scan_chunks(ref, packed), D), f32, dev)
     at = _here(x, stream)
     if at < 0:
         with _scope(x, stream):
             return m3_gated_scan_backward(gate, x, dy, states, bias, h_in, dh_out, cu_seqlens, grads, workspace)
+    rows, _, need = _scan_sizes(b, L, D, dims.io, packed, at)
+    states_p = _dense(states, "states", (rows, D), f32, dev)
+    if states_p is None:
+        raise ValueError("states are required: m3_gated_scan(..., save_states=True) returns them")
     for k in ("gate", "x"):
         if g.get(k) is None:
             g[k] = x.new_empty(shape)
@@ -288,9 +302,9 @@ def m3_gated_scan_backward(gate, x, dy, states, bias=None, h_in=None, dh_out=Non
         g["bias"] = x.new_empty((D,), dtype=f32)
     if h_in is not None and g.get("h_in") is None:
         g["h_in"] = x.new_empty((b, D), dtype=f32)
-    workspace, ws_bytes = _workspace(workspace, lib.m3_gated_scan_backward_workspace_bytes(ref, packed), x)
+    workspace, ws_bytes = _workspace(workspace, need, x)
     _check(lib.m3_gated_scan_backward(
-        ref, _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, states_p, dy.data_ptr(), dh_out_p,
+        ctypes.byref(dims), _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, states_p, dy.data_ptr(), dh_out_p,
         g["gate"].data_ptr(), g["x"].data_ptr(), _ptr(g.get("bias")), _ptr(g.get("h_in")), _ptr(workspace), ws_bytes,
         _raw_stream(at)))
     return g
