@@ -86,7 +86,7 @@ struct ScanPlan {
     int ncols = 0;
     bool per_seq = false, serial = false;
     int64_t parts = 1;
-    size_t words_off = 256, part_off = 0, bytes = 0;
+    size_t words_off = 256, marks_off = 0, seqs_off = 0, part_off = 0, bytes = 0;
 };
 
 m3_status check_scan_dims(const m3_scan_dims* d) {
@@ -138,7 +138,11 @@ m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan*
     p->serial = p->per_seq ? p->seq_tiles <= kMaxSerialTiles || (p->seq_tiles <= kMaxFullSerialTiles && fills_rounds(wgs))
                            : p->ntiles <= 1;
     p->parts = p->serial ? (p->per_seq ? d->batch : 1) : p->ntiles;
-    if (!p->serial) p->part_off = p->words_off + round256((size_t)p->ntiles * p->ncols * m3::kScanCols * 8);
+    if (!p->serial) {
+        p->marks_off = p->words_off + round256((size_t)p->ntiles * p->ncols * m3::kScanCols * 8);
+        p->seqs_off = p->marks_off + (p->per_seq ? 0 : round256((size_t)p->blocks * 16));
+        p->part_off = p->seqs_off + (p->per_seq ? 0 : round256((size_t)p->T * 4));
+    }
     p->bytes = p->part_off + (backward && p->parts > 1 ? (size_t)p->parts * d->width * 4 : 0);
     return M3_OK;
 }
@@ -158,6 +162,9 @@ void scan_args(const m3_scan_dims* d, const ScanPlan& p, const int32_t* cu, void
     a->parts = p.parts;
     a->ticket = (unsigned*)ws;
     a->words = (uint64_t*)((char*)ws + p.words_off);
+    a->starts = (uint64_t*)((char*)ws + p.marks_off);
+    a->ends = a->starts + p.blocks;
+    a->seqs = (int*)((char*)ws + p.seqs_off);
     a->part = (float*)((char*)ws + p.part_off);
 }
 

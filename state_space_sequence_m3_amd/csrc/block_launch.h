@@ -40,6 +40,10 @@ struct GatedScanArgs {
     int64_t gate_p, x_p, y_p, dgate_p, dx_p;   // pitches in bytes
     uint64_t* words;        // [ntiles, ncols * kScanCols] chain words (not serial)
     unsigned* ticket;
+    // flat, chained: which tokens start and end a sequence (a bit each), and the sequence of each token
+    uint64_t* starts;
+    uint64_t* ends;
+    int* seqs;
     int64_t ntiles;
     uint32_t seq_tiles;     // tiles, and blocks, per sequence (per_seq)
     uint32_t seq_blocks;

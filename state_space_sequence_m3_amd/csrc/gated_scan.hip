@@ -208,7 +208,16 @@ __device__ __forceinline__ uint32_t state_row(const GatedScanArgs& a, const Tile
     return (FLAT ? 0 : t.seq * a.seq_blocks) + t.before * (TILE / kScanBlock);
 }
 
-// FLAT: which tokens of a tile start or end a sequence.  One thread per token looks its sequence up.
+// FLAT: which tokens start or end a sequence.  Every token's sequence is searched once, by the launch that
+// resets the chain; a lone tile's, which has no such launch, by the tile itself, one thread per token.
+struct Place {
+    int seq;
+    bool start, end;
+};
+__device__ __forceinline__ Place place_of(const GatedScanArgs& a, int64_t t) {
+    const int64_t s = seq_of(a, t);
+    return {(int)s, seq_start(a, s) == t, seq_start(a, s + 1) == t + 1};
+}
 template <int TILE>
 struct Marks {
     int seq[TILE];                                     // the sequence of each token
@@ -218,14 +227,12 @@ template <int TILE>
 __device__ __forceinline__ void find_marks(const GatedScanArgs& a, const Tile& tile, Marks<TILE>& m) {
     const int i = threadIdx.x;
     if (i < TILE) {
-        bool start = false, end = false;
+        Place p = {0, false, false};
         if (i < tile.nv) {
-            const int64_t t = tile.t0 + i, s = seq_of(a, t);
-            m.seq[i] = (int)s;
-            start = seq_start(a, s) == t;
-            end = seq_start(a, s + 1) == t + 1;
+            p = place_of(a, tile.t0 + i);
+            m.seq[i] = p.seq;
         }
-        const uint64_t ms = __ballot(start), me = __ballot(end);
+        const uint64_t ms = __ballot(p.start), me = __ballot(p.end);
         if ((i & 63) == 0) {
             m.starts[i >> 6] = ms;
             m.ends[i >> 6] = me;
@@ -238,9 +245,6 @@ template <int N>
 __device__ __forceinline__ uint32_t mark_bits(const uint64_t* m, int i) {
     return uniform32((uint32_t)(m[i / 64] >> (i % 64))) & ((1u << N) - 1);
 }
-template <int TILE>
-__device__ __forceinline__ int64_t mark_seq(const Marks<TILE>& m, int i) { return uniform32((uint32_t)m.seq[i]); }
-
 // ------------------------------------------------------------------------------ chain words
 // Tiles of one sequence are chained through 64-bit words, one per tile and channel, each written
 // whole by one relaxed agent-scope store (so a word is its own flag and needs no fence): low half
@@ -306,10 +310,26 @@ __device__ __forceinline__ void chain_wait(const uint64_t* words, int64_t stride
     carry[0] = carry[1] = __uint_as_float(0x7fc00000u);
 }
 
-__global__ __launch_bounds__(256) void chain_reset_kernel(uint4* words, int64_t n16, unsigned* ticket) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < n16) words[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
-    if (i == 0) *ticket = 0;
+// Before a chained launch: the words unset, the counter at 0, and (flat) the tokens' marks.
+__global__ __launch_bounds__(256) void chain_reset_kernel(const GatedScanArgs a, int64_t n16) {
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += step)
+        ((uint4*)a.words)[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+    if (a.per_seq) return;
+    const int64_t total = a.cu ? seq_start(a, a.b) : a.T;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (a.T + 63) / 64 * 64; i += step) {   // whole waves
+        Place p = {0, false, false};
+        if (i < total) {
+            p = place_of(a, i);
+            a.seqs[i] = p.seq;
+        }
+        const uint64_t ms = __ballot(p.start), me = __ballot(p.end);
+        if ((i & 63) == 0) {
+            a.starts[i >> 6] = ms;
+            a.ends[i >> 6] = me;
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------------- forward
@@ -364,18 +384,18 @@ __device__ __forceinline__ void pass_empty(const GatedScanArgs& a, uint32_t c, c
     }
 }
 
-template <typename T, bool FLAT>
+template <typename T, bool FLAT, bool SERIAL>
 struct FwdShared {
     float2 sA[kWaves][64], sB[kWaves][64], sCarry[64];
     int sHard[kWaves];   // bit 0: the wave's tokens hold a sequence start; bit 1: its first token is one
-    Marks<FLAT ? kWaves * kFwdSteps<T> : 1> marks;
+    Marks<FLAT && SERIAL ? kWaves * kFwdSteps<T> : 1> marks;
     unsigned sTicket;
 };
 
 // One tile.  SERIAL: `state`, the last wave's, is the state before the tile, and then the one after it; else it
 // comes from the chain.
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
-__device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T, FLAT>& sh, uint32_t c, int col, int lane,
+__device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T, FLAT, SERIAL>& sh, uint32_t c, int col, int lane,
                                              int w, float (&state)[2]) {
     constexpr int N = kFwdSteps<T>, TILE = kWaves * N;
     const Tile tile = tile_of<TILE, FLAT, SERIAL>(a, c);
@@ -392,10 +412,15 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
             load_rows(g, rows_at(a.gate, tw * a.gate_p), (int)a.gate_p, nv, cols);
             load_rows(x, rows_at(a.x, tw * a.x_p), (int)a.x_p, nv, cols);
         }
-        if constexpr (FLAT) {
+        if constexpr (FLAT && SERIAL) {
             find_marks(a, tile, sh.marks);
             starts = mark_bits<N>(sh.marks.starts, w * N);
             ends = mark_bits<N>(sh.marks.ends, w * N);
+        } else if constexpr (FLAT) {
+            if (nv > 0) {
+                starts = mark_bits<N>(a.starts + tile.t0 / 64, w * N);
+                ends = mark_bits<N>(a.ends + tile.t0 / 64, w * N);
+            }
         } else {                               // a sequence's first and last token
             if (w == 0 && tile.before == 0) starts = 1;
             if (tile.after == 0 && nv > 0 && w * N + nv == tile.nv) ends = 1u << (nv - 1);
@@ -420,7 +445,8 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
             }
     }
     auto seq_at = [&](int i) -> int64_t {
-        if constexpr (FLAT) return mark_seq(sh.marks, w * N + i);
+        if constexpr (FLAT && SERIAL) return uniform32((uint32_t)sh.marks.seq[w * N + i]);
+        else if constexpr (FLAT) return uniform32((uint32_t)a.seqs[tw + i]);
         else return tile.seq;
     };
     float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};   // the wave's map
@@ -529,7 +555,7 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
 // reset.  For chains so short, or sequences so many, that the tiles need not run at the same time.
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
 __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(const GatedScanArgs a) {
-    __shared__ FwdShared<T, FLAT> sh;
+    __shared__ FwdShared<T, FLAT, SERIAL> sh;
     const int lane = threadIdx.x & 63;
     const int w = uniform32(threadIdx.x >> 6);
     float state[2] = {0.f, 0.f};
@@ -551,18 +577,18 @@ __global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(con
 // With G_t = (1 - z_t) l_t, what flows from token t to h_{t-1}: l_t = dy_t + G_{t+1}, so backwards
 // G_t = keep_t G_{t+1} + keep_t dy_t, an affine map again, and the same chain in the other
 // direction.  A sequence's last token takes dh_out for G_{t+1}.
-template <typename T, bool FLAT>
+template <typename T, bool FLAT, bool SERIAL>
 struct BwdShared {
     float2 sA[kWaves][64], sB[kWaves][64], sRA[kWaves][64], sRB[kWaves][64], sCarry[64];
     int sHard[kWaves];   // bit 0: holds a sequence start; 1: holds an end; 2: its last token is an end
-    Marks<FLAT ? kWaves * kBwdSteps<T> : 1> marks;
+    Marks<FLAT && SERIAL ? kWaves * kBwdSteps<T> : 1> marks;
     unsigned sTicket;
 };
 
 // One tile.  SERIAL: `state`, the first wave's, is what flows in from behind the tile, and then what flows out
 // of it; else it comes from the chain.  `sum`: the wave's share of dbias grows.
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
-__device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<T, FLAT>& sh, uint32_t c, int col,
+__device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<T, FLAT, SERIAL>& sh, uint32_t c, int col,
                                               int lane, int w, float (&state)[2], float (&sum)[2]) {
     constexpr int N = kBwdSteps<T>, TILE = kWaves * N;
     const Tile tile = tile_of<TILE, FLAT, SERIAL>(a, c);
@@ -582,10 +608,15 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
             load_rows(x, rows_at(a.x, tw * a.x_p), (int)a.x_p, nv, cols);
             load_rows(dy, rows_at(a.dy, tw * a.y_p), (int)a.y_p, nv, cols);
         }
-        if constexpr (FLAT) {
+        if constexpr (FLAT && SERIAL) {
             find_marks(a, tile, sh.marks);
             starts = mark_bits<N>(sh.marks.starts, w * N);
             ends = mark_bits<N>(sh.marks.ends, w * N);
+        } else if constexpr (FLAT) {
+            if (nv > 0) {
+                starts = mark_bits<N>(a.starts + tile.t0 / 64, w * N);
+                ends = mark_bits<N>(a.ends + tile.t0 / 64, w * N);
+            }
         } else {                               // a sequence's first and last token
             if (w == 0 && tile.before == 0) starts = 1;
             if (tile.after == 0 && nv > 0 && w * N + nv == tile.nv) ends = 1u << (nv - 1);
@@ -608,7 +639,8 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
             }
     }
     auto seq_at = [&](int i) -> int64_t {
-        if constexpr (FLAT) return mark_seq(sh.marks, w * N + i);
+        if constexpr (FLAT && SERIAL) return uniform32((uint32_t)sh.marks.seq[w * N + i]);
+        else if constexpr (FLAT) return uniform32((uint32_t)a.seqs[tw + i]);
         else return tile.seq;
     };
     {   // the wave's maps, forwards and backwards
@@ -781,8 +813,8 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
 }
 
 // the workgroup's share of dbias: its waves' added in order
-template <typename T, bool VEC, bool FLAT>
-__device__ __forceinline__ void add_dbias(const GatedScanArgs& a, BwdShared<T, FLAT>& sh, uint32_t row, int col, int lane,
+template <typename T, bool VEC, bool FLAT, bool SERIAL>
+__device__ __forceinline__ void add_dbias(const GatedScanArgs& a, BwdShared<T, FLAT, SERIAL>& sh, uint32_t row, int col, int lane,
                                           int w, const float (&sum)[2]) {
     if (a.dbias == nullptr) return;
     __syncthreads();
@@ -801,7 +833,7 @@ __device__ __forceinline__ void add_dbias(const GatedScanArgs& a, BwdShared<T, F
 
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
 __global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_kernel(const GatedScanArgs a) {
-    __shared__ BwdShared<T, FLAT> sh;
+    __shared__ BwdShared<T, FLAT, SERIAL> sh;
     const int lane = threadIdx.x & 63;
     const int w = uniform32(threadIdx.x >> 6);
     float state[2] = {0.f, 0.f}, sum[2] = {0.f, 0.f};
@@ -879,9 +911,9 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* part, int
 }
 
 hipError_t reset_chain(const GatedScanArgs& a, hipStream_t s) {
-    const int64_t n16 = a.ntiles * a.ncols * kScanCols / 2;
-    hipLaunchKernelGGL(chain_reset_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, s, (uint4*)a.words, n16,
-                       a.ticket);
+    const int64_t n16 = a.ntiles * a.ncols * kScanCols / 2, most = a.per_seq || n16 > a.T ? n16 : a.T;
+    const int64_t blocks = (most + 255) / 256;
+    hipLaunchKernelGGL(chain_reset_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, a, n16);
     return hipGetLastError();
 }
 
