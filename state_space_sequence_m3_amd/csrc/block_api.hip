@@ -103,7 +103,9 @@ m3_status check_scan_dims(const m3_scan_dims* d) {
 // Bf16, D 4096, forward (backward): two tiles of few sequences 14.5 -> 12.9 us (4 x 256 tokens; four tiles lose: 23.1 ->
 // 25.1 us); many sequences, which fill the GPU anyway, 88 -> 79 us (161 -> 140) at 64 x 256 tokens, 91 -> 83 us at
 // 16 x 1024, but 162 -> 172 us at 8 x 2048 x 8192 channels, 16 tiles.  Packed batches never gain: their tiles wait
-// for the search of their sequences, which then adds up.
+// for the search of their sequences, which then adds up.  The forward pass of fp32 holds twice the bytes and spills in
+// that form: it gains where there is one tile to a sequence and few of those (4 x 128 tokens 13.6 -> 12.5 us), and
+// loses beyond (147 -> 160 us at 64 x 256 tokens); its backward pass gains as bf16 does (260 -> 241 us at 128 x 128).
 constexpr int64_t kMaxLoneTiles = 512;   // two workgroups on each of 256 compute units
 constexpr int64_t kMaxSerialTiles = 2, kMaxFullSerialTiles = 8;
 // Workgroups that keep the GPU full: no last round of two to a compute unit that is mostly empty.
@@ -115,7 +117,7 @@ bool fills_rounds(int64_t wgs) {
 m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan* p) {
     M3_TRY(check_scan_dims(d));
     constexpr int64_t block = m3::kScanBlock;
-    const int64_t tile = d->io != M3_BF16 ? m3::kScanTileF32 : backward ? m3::kScanBwdTileBf16 : m3::kScanTileBf16;
+    const int64_t tile = backward ? m3::kScanBwdTile : m3::kScanTile;
     p->T = packed ? d->seqlen : d->batch * d->seqlen;
     p->ncols = (int)((d->width + m3::kScanCols - 1) / m3::kScanCols);
     // Short sequences share tiles, unless they are so few that all can have a tile of their own at the same time
@@ -135,8 +137,10 @@ m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan*
         return fail(M3_E_DIMS, "%lld tokens of %lld channels: more than 2^31 blocks of 64 tokens and 128 channels",
                     (long long)p->T, (long long)d->width);
     const int64_t wgs = p->per_seq ? d->batch * p->ncols : p->ncols;
-    p->serial = p->per_seq ? p->seq_tiles <= kMaxSerialTiles || (p->seq_tiles <= kMaxFullSerialTiles && fills_rounds(wgs))
-                           : p->ntiles <= 1;
+    p->serial = !p->per_seq                        ? p->ntiles <= 1
+                : d->io != M3_BF16 && !backward ? p->seq_tiles <= 1 && wgs <= kMaxLoneTiles
+                                                : p->seq_tiles <= kMaxSerialTiles ||
+                                                      (p->seq_tiles <= kMaxFullSerialTiles && fills_rounds(wgs));
     p->parts = p->serial ? (p->per_seq ? d->batch : 1) : p->ntiles;
     if (!p->serial) {
         p->marks_off = p->words_off + round256((size_t)p->ntiles * p->ncols * m3::kScanCols * 8);
@@ -169,7 +173,7 @@ void scan_args(const m3_scan_dims* d, const ScanPlan& p, const int32_t* cu, void
 }
 
 // A tile's rows are addressed with 31-bit offsets from its first one.
-constexpr int64_t kMaxScanPitch = ((int64_t)1 << 31) / m3::kScanTileBf16;   // bytes
+constexpr int64_t kMaxScanPitch = ((int64_t)1 << 31) / m3::kScanTile;   // bytes
 m3_status check_scan_pitch(int64_t pitch, int64_t rows, int64_t width, int64_t es, const char* name, int64_t* bytes) {
     M3_TRY(check_pitch(pitch, rows, width, es, name, bytes));
     if (*bytes >= kMaxScanPitch)

@@ -10,11 +10,11 @@
 namespace m3 {
 
 // ---------------------------------------------------------------------------- gated scan
-// A tile is kScanTile* tokens x kScanCols channels, worked on by one workgroup; `states` has a row per
+// A tile is kScanTile tokens (backward: kScanBwdTile) x kScanCols channels, worked on by one workgroup; `states` has a row per
 // block of kScanBlock tokens, whatever the type.  Dense batches of sequences longer than a block are
 // cut sequence by sequence (`per_seq`), and so are few shorter ones; many shorter ones and packed batches
 // are cut along the flat token axis, so a tile can hold many sequences.
-constexpr int kScanTileBf16 = 128, kScanBwdTileBf16 = 64, kScanTileF32 = 64, kScanBlock = 64;
+constexpr int kScanTile = 128, kScanBwdTile = 64, kScanBlock = 64;
 constexpr int kScanCols = 128;
 
 struct GatedScanArgs {

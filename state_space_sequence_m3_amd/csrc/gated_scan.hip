@@ -12,14 +12,9 @@ namespace m3 {
 namespace {
 
 constexpr int kWaves = 8;   // waves per tile; each holds kSteps consecutive tokens in registers
-template <typename T> constexpr int kFwdSteps = sizeof(T) == 2 ? 16 : 8;
-template <typename T> constexpr int kBwdSteps = sizeof(T) == 2 ? kScanBwdTileBf16 / kWaves : 8;
+constexpr int kFwdSteps = kScanTile / kWaves, kBwdSteps = kScanBwdTile / kWaves;
 constexpr uint32_t kSideBySide = 4;
-template <typename T> constexpr int kFwdOcc = 4;   // waves per SIMD to leave registers for
-template <typename T> constexpr int kBwdOcc = 4;
-static_assert(kWaves * kFwdSteps<bf16> == kScanTileBf16 && kWaves * kFwdSteps<float> == kScanTileF32 &&
-              kWaves * kBwdSteps<float> == kScanTileF32,
-              "tile heights of block_launch.h");
+constexpr int kWavesPerSimd = 4;   // two workgroups on a compute unit: 128 registers
 
 // z = sigmoid(u) and keep = 1 - z, both to a few units in their last place: with e = e^-|u| the larger of
 // the two is 1 / (1 + e) and the smaller one e / (1 + e), never a difference from 1.  The logit comes
@@ -388,7 +383,7 @@ template <typename T, bool FLAT, bool SERIAL>
 struct FwdShared {
     float2 sA[kWaves][64], sB[kWaves][64], sCarry[64];
     int sHard[kWaves];   // bit 0: the wave's tokens hold a sequence start; bit 1: its first token is one
-    Marks<FLAT && SERIAL ? kWaves * kFwdSteps<T> : 1> marks;
+    Marks<FLAT && SERIAL ? kWaves * kFwdSteps : 1> marks;
     unsigned sTicket;
 };
 
@@ -397,7 +392,7 @@ struct FwdShared {
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
 __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T, FLAT, SERIAL>& sh, uint32_t c, int col, int lane,
                                              int w, float (&state)[2]) {
-    constexpr int N = kFwdSteps<T>, TILE = kWaves * N;
+    constexpr int N = kFwdSteps, TILE = kWaves * N;
     const Tile tile = tile_of<TILE, FLAT, SERIAL>(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
     const int64_t tw = tile.t0 + w * N;
@@ -506,7 +501,7 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
             const bool starts_here = (uniform32(sh.sHard[0]) & 2) != 0;
             if (tile.before > 0 && tile.nv > 0 && !starts_here) {
                 const int64_t step = -tile.link;
-                chain_wait<sizeof(T) == 2 ? 4 : 8>(a.words, stride, c + step, step, tile.before, cols.d, carry);
+                chain_wait<4>(a.words, stride, c + step, step, tile.before, cols.d, carry);
             }
             if (!hard) {
 #pragma unroll
@@ -554,7 +549,7 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
 // SERIAL: a workgroup takes one sequence (FLAT: the whole batch) tile by tile: no chain to wait for, none to
 // reset.  For chains so short, or sequences so many, that the tiles need not run at the same time.
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
-__global__ __launch_bounds__(kWaves * 64, kFwdOcc<T>) void gated_scan_kernel(const GatedScanArgs a) {
+__global__ __launch_bounds__(kWaves * 64, kWavesPerSimd) void gated_scan_kernel(const GatedScanArgs a) {
     __shared__ FwdShared<T, FLAT, SERIAL> sh;
     const int lane = threadIdx.x & 63;
     const int w = uniform32(threadIdx.x >> 6);
@@ -581,7 +576,7 @@ template <typename T, bool FLAT, bool SERIAL>
 struct BwdShared {
     float2 sA[kWaves][64], sB[kWaves][64], sRA[kWaves][64], sRB[kWaves][64], sCarry[64];
     int sHard[kWaves];   // bit 0: holds a sequence start; 1: holds an end; 2: its last token is an end
-    Marks<FLAT && SERIAL ? kWaves * kBwdSteps<T> : 1> marks;
+    Marks<FLAT && SERIAL ? kWaves * kBwdSteps : 1> marks;
     unsigned sTicket;
 };
 
@@ -590,7 +585,7 @@ struct BwdShared {
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
 __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<T, FLAT, SERIAL>& sh, uint32_t c, int col,
                                               int lane, int w, float (&state)[2], float (&sum)[2]) {
-    constexpr int N = kBwdSteps<T>, TILE = kWaves * N;
+    constexpr int N = kBwdSteps, TILE = kWaves * N;
     const Tile tile = tile_of<TILE, FLAT, SERIAL>(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
     const int64_t tw = tile.t0 + w * N;
@@ -832,7 +827,7 @@ __device__ __forceinline__ void add_dbias(const GatedScanArgs& a, BwdShared<T, F
 }
 
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
-__global__ __launch_bounds__(kWaves * 64, kBwdOcc<T>) void gated_scan_backward_kernel(const GatedScanArgs a) {
+__global__ __launch_bounds__(kWaves * 64, kWavesPerSimd) void gated_scan_backward_kernel(const GatedScanArgs a) {
     __shared__ BwdShared<T, FLAT, SERIAL> sh;
     const int lane = threadIdx.x & 63;
     const int w = uniform32(threadIdx.x >> 6);

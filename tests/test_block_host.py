@@ -222,26 +222,27 @@ def test_workspaces():
     lib = m3block.load()
     r = lambda n: (n + 255) // 256 * 256
     # `states` has a row per 64 tokens of a sequence (of the batch, where it is packed or its sequences are short and
-    # many).  Chained tiles (bf16 forward 128 tokens, else 64) need a 64-bit word per tile and channel (130 channels: 2
-    # columns of 128) after 256 bytes, and marks where tiles hold several sequences; sequences of up to 2 tiles, and of up to 8 where they fill the GPU with a
-    # workgroup each, are worked off without.  Backward also needs a row of partial sums per workgroup.
+    # many).  Chained tiles (forward 128 tokens, backward 64) need a 64-bit word per tile and channel (130 channels: 2
+    # columns of 128) after 256 bytes, and marks where tiles hold several sequences; sequences of up to 2 tiles, and of
+    # up to 8 where they fill the GPU with a workgroup each, are worked off without (fp32 forward: of one tile, if
+    # few).  Backward also needs a row of partial sums per workgroup.
     words = lambda n: 256 + r(n * 256 * 8)
     row = 130 * 4
     marks = lambda t: r(-(-t // 64) * 16) + r(t * 4)       # where tiles hold several sequences: two bits and 4 bytes a token
     for kw, packed, rows, fwd16, fwd32, bwd in (
-            (dict(), 0, 32, words(16), words(32), words(32) + 32 * row),
-            (dict(), 1, 16, words(8) + marks(1000), words(16) + marks(1000), words(16) + marks(1000) + 16 * row),
-            (dict(seqlen=300), 0, 10, words(6), words(10), words(10) + 10 * row),
-            (dict(seqlen=300), 1, 5, words(3) + marks(300), words(5) + marks(300), words(5) + marks(300) + 5 * row),
-            (dict(seqlen=256), 0, 8, 0, words(8), words(8) + 8 * row),
+            (dict(), 0, 32, words(16), words(16), words(32) + 32 * row),
+            (dict(), 1, 16, words(8) + marks(1000), words(8) + marks(1000), words(16) + marks(1000) + 16 * row),
+            (dict(seqlen=300), 0, 10, words(6), words(6), words(10) + 10 * row),
+            (dict(seqlen=300), 1, 5, words(3) + marks(300), words(3) + marks(300), words(5) + marks(300) + 5 * row),
+            (dict(seqlen=256), 0, 8, 0, words(4), words(8) + 8 * row),
             (dict(seqlen=128), 0, 4, 0, 0, 2 * row),
-            (dict(seqlen=128), 1, 2, 0, words(2) + marks(128), words(2) + marks(128) + 2 * row),
+            (dict(seqlen=128), 1, 2, 0, 0, words(2) + marks(128) + 2 * row),
             (dict(seqlen=64), 1, 1, 0, 0, 0),
-            (dict(batch=256, seqlen=500), 0, 2048, 0, 0, 256 * row),               # 512 workgroups: a full round
-            (dict(batch=256, seqlen=1000), 0, 4096, 0, words(4096), words(4096) + 4096 * row),
-            (dict(batch=200, seqlen=1000), 0, 200 * 16, words(200 * 8), words(200 * 16), words(3200) + 3200 * row),
+            (dict(batch=256, seqlen=500), 0, 2048, 0, words(1024), 256 * row),               # 512 workgroups: a full round
+            (dict(batch=256, seqlen=1000), 0, 4096, 0, words(2048), words(4096) + 4096 * row),
+            (dict(batch=200, seqlen=1000), 0, 200 * 16, words(200 * 8), words(200 * 8), words(3200) + 3200 * row),
             (dict(batch=200, seqlen=3), 0, 200, 0, 0, 200 * row),
-            (dict(batch=300, seqlen=3), 0, 15, words(8) + marks(900), words(15) + marks(900), words(15) + marks(900) + 15 * row),
+            (dict(batch=300, seqlen=3), 0, 15, words(8) + marks(900), words(8) + marks(900), words(15) + marks(900) + 15 * row),
             (dict(seqlen=0), 0, 1, 0, 0, 0), (dict(batch=0), 0, 1, 0, 0, 0)):
         for io in (m3block.M3_BF16, m3block.M3_F32):
             ref = ctypes.byref(scan_dims(io=io, **kw))
