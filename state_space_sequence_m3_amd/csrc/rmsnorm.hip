@@ -9,6 +9,8 @@
 #include "block_launch.h"
 #include "m3_device.h"
 
+#include <algorithm>
+
 namespace m3 {
 namespace {
 
@@ -153,9 +155,15 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v, int R) {
 constexpr int kBlock = 0;
 template <int TPR> constexpr int max_threads() { return TPR == kBlock ? 1024 : 256; }
 // Waves per SIMD that registers are left for, and with it the workgroups that are resident: the grid is
-// that many, each takes every gridDim-th row.
+// that many, each takes every gridDim-th row.  Forward: 4 waves for all 8000 x 5120 bf16 57 -> 65 us (one
+// workgroup of 10 waves per compute unit instead of two), 65536 x 300 33 -> 36 us; 8 waves 16384 x 4096
+// 90 -> 92 us, 65536 x 128 14 -> 17 us (spills).  Backward: 4 waves for all 8000 x 5120 bf16 73 -> 78 us; 6
+// waves 16384 x 4096 104 -> 113 us (spills).
 template <typename T, int C> constexpr int kFwdOcc = C > 1 ? 4 : 6;
 template <typename T, int C> constexpr int kBwdOcc = C > 1 || sizeof(T) == 4 ? 4 : 5;
+// The backward grid of rows on a workgroup leaves out what is over 4 waves per SIMD: with three and more streams of
+// rows to a workgroup, fewer of them run at a better rate (30000 x 1111 bf16 73 -> 68 us, 2048 wide 101 -> 98 us).
+constexpr int kBwdWant = 4;
 
 // Sums or maxima over a row: over the row's lanes, then, for a row on a workgroup, over its waves.
 template <int TPR> __device__ __forceinline__ float row_sum(float v) { return group_sum(v, TPR == kBlock ? 64 : TPR); }
@@ -416,11 +424,14 @@ auto with_plan(const Plan& p, F&& f) {
     if (p.chunks == 1) return f.template operator()<kBlock, 1>();
     return f.template operator()<kBlock, 2>();
 }
-unsigned grid_of(int64_t rows, const Plan& p, int occ, int cus) {
+// Workgroups: as many as fit with `occ` waves per SIMD; for rows on a workgroup, of those as many as come
+// nearest to `want` waves per SIMD.
+unsigned grid_of(int64_t rows, const Plan& p, int occ, int want, int cus) {
     const int per_wg = p.tpr == kBlock ? 1 : p.threads / p.tpr;
-    const int per_cu = occ * 256 / p.threads > 0 ? occ * 256 / p.threads : 1;
-    const int64_t n = (rows + per_wg - 1) / per_wg, most = (int64_t)per_cu * cus;
-    return (unsigned)(n < most ? n : most);
+    int per_cu = occ * 256 / p.threads;
+    if (p.tpr == kBlock) per_cu = std::min(per_cu, (want * 256 + p.threads / 2) / p.threads);
+    const int64_t n = (rows + per_wg - 1) / per_wg, most = (int64_t)std::max(per_cu, 1) * cus;
+    return (unsigned)std::min(n, most);
 }
 template <typename T>
 struct Forward {
@@ -429,7 +440,7 @@ struct Forward {
     hipStream_t s;
     template <int TPR, int C>
     hipError_t operator()() {
-        const dim3 grid(grid_of(a.rows, p, kFwdOcc<T, C>, a.cus)), block(p.threads);
+        const dim3 grid(grid_of(a.rows, p, kFwdOcc<T, C>, kFwdOcc<T, C>, a.cus)), block(p.threads);
         if (a.stream) hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, C, true>), grid, block, 0, s, a);
         else hipLaunchKernelGGL((rmsnorm_kernel<T, TPR, C, false>), grid, block, 0, s, a);
         return hipGetLastError();
@@ -444,7 +455,7 @@ struct Backward {
     int64_t* parts;        // rows of dweight partial sums
     template <int TPR, int C>
     hipError_t operator()() {
-        const dim3 grid(grid_of(a.rows, p, kBwdOcc<T, C>, a.cus)), block(p.threads);
+        const dim3 grid(grid_of(a.rows, p, kBwdOcc<T, C>, kBwdWant, a.cus)), block(p.threads);
         *parts = (int64_t)grid.x;
         if (!launch) return hipSuccess;
         if (a.stream) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, TPR, C, true>), grid, block, 0, s, a);
