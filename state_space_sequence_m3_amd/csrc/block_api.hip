@@ -259,8 +259,9 @@ struct GradPlan {
 // not fit 32 bits), from the first tensor on or from the last; `each` is called with every table and
 // the place of its partial sums.
 template <typename F>
-m3_status for_batches(const m3_grad_tensor* t, int64_t n, bool back, bool stream, F&& each) {
+m3_status for_batches(const m3_grad_tensor* t, int64_t n, bool back, bool stream, int64_t chunk, F&& each) {
     m3::GradBatch b;
+    b.chunk = (int)chunk;
     b.stream = stream ? 1 : 0;
     int64_t k = 0, parts = 0;
     auto at = [&](int64_t i) -> const m3_grad_tensor& { return t[back ? n - 1 - i : i]; };
@@ -273,7 +274,7 @@ m3_status for_batches(const m3_grad_tensor* t, int64_t n, bool back, bool stream
         for (; k < n && b.n < m3::kGradBatch; ++k) {
             const m3_grad_tensor& g = at(k);
             if (g.numel == 0) continue;
-            const int64_t units = (g.numel + m3::kGradChunk - 1) / m3::kGradChunk;
+            const int64_t units = (g.numel + chunk - 1) / chunk;
             if (b.n > 0 && b.first[b.n] + units >= (int64_t)1 << 31) break;
             b.src[b.n] = g.src;
             b.dst[b.n] = g.dst;
@@ -292,7 +293,7 @@ GradPlan plan_grads(const m3_grad_tensor* t, int64_t n) {
         p.elements += t[i].numel;
         p.bytes += t[i].numel * (t[i].io == M3_BF16 ? 2 : 4);
     }
-    for_batches(t, n, false, false, [&](const m3::GradBatch& b, int64_t at) {
+    for_batches(t, n, false, false, m3::kGradChunk, [&](const m3::GradBatch& b, int64_t at) {
         p.batches++;
         p.parts = at + m3::grad_blocks(b);
         return M3_OK;
@@ -329,10 +330,10 @@ m3_status grads(const char* fn, bool write, const m3_grad_tensor* t, int64_t n, 
     M3_TRY(check_device());
     double* part = (double*)ws;
     if (grad_small(p))
-        return for_batches(t, n, false, false, [&](const m3::GradBatch& b, int64_t) {
+        return for_batches(t, n, false, false, m3::kGradSmallChunk, [&](const m3::GradBatch& b, int64_t) {
             return launched(m3::launch_grad_small(b, write, max_norm, stats, stream), fn);
         });
-    M3_TRY(for_batches(t, n, false, false, [&](const m3::GradBatch& b, int64_t at) {
+    M3_TRY(for_batches(t, n, false, false, m3::kGradChunk, [&](const m3::GradBatch& b, int64_t at) {
         return launched(m3::launch_grad_sumsq(b, part + at, stream), fn);
     }));
     const bool own_stats = !write || p.parts == 0 || p.parts > kMaxSharedParts;
@@ -341,7 +342,7 @@ m3_status grads(const char* fn, bool write, const m3_grad_tensor* t, int64_t n, 
         M3_TRY(launched(m3::launch_grad_stats(part, p.parts, max_norm, stats, p.parts ? sum : nullptr, stream), fn));
     if (!write) return M3_OK;
     // backwards: what was read last for the sum is still in the last-level cache
-    return for_batches(t, n, true, p.bytes * 2 > kCacheBytes, [&](const m3::GradBatch& b, int64_t at) {
+    return for_batches(t, n, true, p.bytes * 2 > kCacheBytes, m3::kGradChunk, [&](const m3::GradBatch& b, int64_t at) {
         return launched(m3::launch_grad_scale(b, own_stats ? sum : part, own_stats ? 1 : (int)p.parts, max_norm,
                                               own_stats || at > 0 ? nullptr : stats, stream), fn);
     });

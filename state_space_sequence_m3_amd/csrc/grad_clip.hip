@@ -28,7 +28,7 @@ __device__ __forceinline__ int tensor_of(const GradBatch& b, uint32_t u) {
 __device__ __forceinline__ bool is_bf16(const GradBatch& b, int i) { return (b.is_bf16[i >> 5] >> (i & 31)) & 1; }
 __device__ __forceinline__ int unit_size(const GradBatch& b, int i, int64_t at) {
     const int64_t left = b.numel[i] - at;
-    return (int)(left < kGradChunk ? left : kGradChunk);
+    return (int)(left < b.chunk ? left : b.chunk);
 }
 
 // the sum over all NT threads, in every one of them
@@ -44,12 +44,13 @@ __device__ __forceinline__ double block_sum(double v) {
     return t;
 }
 
+// Thread t of NT: its share of the unit at element `at` of tensor i.
 template <int NT>
-__device__ __forceinline__ void add_squares(const GradBatch& b, int i, int64_t at, double (&acc)[2]) {
+__device__ __forceinline__ void add_squares(const GradBatch& b, int i, int64_t at, int t, double (&acc)[2]) {
     const int n = unit_size(b, i, at);
     if (is_bf16(b, i)) {
         const uint16_t* p = (const uint16_t*)b.src[i] + at;
-        int e = threadIdx.x * 8;
+        int e = t * 8;
 #pragma unroll 4
         for (; e + 8 <= n; e += NT * 8) {
             const Bytes16 v = *(const Bytes16*)(p + e);
@@ -66,7 +67,7 @@ __device__ __forceinline__ void add_squares(const GradBatch& b, int i, int64_t a
         }
     } else {
         const float* p = (const float*)b.src[i] + at;
-        int e = threadIdx.x * 4;
+        int e = t * 4;
 #pragma unroll 4
         for (; e + 4 <= n; e += NT * 4) {
             const Bytes16 v = *(const Bytes16*)(p + e);
@@ -86,7 +87,7 @@ __device__ __forceinline__ void add_squares(const GradBatch& b, int i, int64_t a
 // STREAM: non-temporal stores (a template argument, since the compiler makes one ordinary store of two that
 // differ in nothing else)
 template <int NT, bool STREAM>
-__device__ __forceinline__ void scale_unit(const GradBatch& b, int i, int64_t at, float coef) {
+__device__ __forceinline__ void scale_unit(const GradBatch& b, int i, int64_t at, int t, float coef) {
     if (coef == 1.f && b.src[i] == b.dst[i]) return;
     const int n = unit_size(b, i, at);
     auto put = [&](void* o, const u32x4& v) {
@@ -96,7 +97,7 @@ __device__ __forceinline__ void scale_unit(const GradBatch& b, int i, int64_t at
     if (is_bf16(b, i)) {
         const uint16_t* p = (const uint16_t*)b.src[i] + at;
         uint16_t* o = (uint16_t*)b.dst[i] + at;
-        int e = threadIdx.x * 8;
+        int e = t * 8;
 #pragma unroll 4
         for (; e + 8 <= n; e += NT * 8) {
             const Bytes16 v = *(const Bytes16*)(p + e);
@@ -110,7 +111,7 @@ __device__ __forceinline__ void scale_unit(const GradBatch& b, int i, int64_t at
     } else {
         const float* p = (const float*)b.src[i] + at;
         float* o = (float*)b.dst[i] + at;
-        int e = threadIdx.x * 4;
+        int e = t * 4;
 #pragma unroll 4
         for (; e + 4 <= n; e += NT * 4) {
             const Bytes16 v = *(const Bytes16*)(p + e);
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const GradBatch b,
     const uint32_t units = b.first[b.n];
     for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int i = tensor_of(b, u);
-        add_squares<kThreads>(b, i, (int64_t)(u - b.first[i]) * kGradChunk, acc);
+        add_squares<kThreads>(b, i, (int64_t)(u - b.first[i]) * kGradChunk, threadIdx.x, acc);
     }
     const double t = block_sum<kThreads>(acc[0] + acc[1]);
     if (threadIdx.x == 0) part[blockIdx.x] = t;
@@ -168,21 +169,28 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradBatch b,
     for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int i = tensor_of(b, u);
         // each tensor's units from its end, as the tensors are
-        scale_unit<kThreads, STREAM>(b, i, (int64_t)(b.first[i + 1] - 1 - u) * kGradChunk, nc.y);
+        scale_unit<kThreads, STREAM>(b, i, (int64_t)(b.first[i + 1] - 1 - u) * kGradChunk, threadIdx.x, nc.y);
     }
 }
 
-// Few elements: sum and scaling in one launch by one workgroup, which reads them again from its caches.
+// Few elements: sum and scaling in one launch by one workgroup, a unit to a wave at a time, which reads them
+// again from its caches.
 __global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(const GradBatch b, int write, float max_norm,
                                                                    float* stats) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), units = b.first[b.n];
     double acc[2] = {0.0, 0.0};
-    for (int i = 0; i < b.n; ++i)
-        for (int64_t at = 0; at < b.numel[i]; at += kGradChunk) add_squares<kSmallThreads>(b, i, at, acc);
+    for (uint32_t u = wave; u < units; u += kSmallThreads / 64) {
+        const int i = tensor_of(b, u);
+        add_squares<64>(b, i, (int64_t)(u - b.first[i]) * kGradSmallChunk, lane, acc);
+    }
     const float2 nc = norm_and_coef(block_sum<kSmallThreads>(acc[0] + acc[1]), max_norm);
     write_stats(stats, nc);
     if (!write) return;
-    for (int i = 0; i < b.n; ++i)
-        for (int64_t at = 0; at < b.numel[i]; at += kGradChunk) scale_unit<kSmallThreads, false>(b, i, at, nc.y);
+    for (uint32_t u = wave; u < units; u += kSmallThreads / 64) {
+        const int i = tensor_of(b, u);
+        scale_unit<64, false>(b, i, (int64_t)(u - b.first[i]) * kGradSmallChunk, lane, nc.y);
+    }
 }
 
 }  // namespace
