@@ -11,8 +11,9 @@
  *    Rows that start on 16-byte boundaries (scan: one 4-byte (bf16) or 8-byte (fp32) pair) take
  *    wider loads; nothing else depends on it.
  *  - Pitches.  A pitch is the distance in elements between the first elements of consecutive
- *    rows (tokens); 0 means dense.  Gated scan: rows are at most 2^24 - 1 bytes apart.  Tensors may be slices of one wider buffer, outputs too, as long
- *    as no element is written twice or is both read and written, except where a call allows it.
+ *    rows (tokens); 0 means dense.  Gated scan: rows are at most 2^24 - 1 bytes apart.  Tensors may
+ *    be slices of one wider buffer, outputs too, as long as no element is written twice or is both
+ *    read and written, except where a call allows it.
  *  - Workspaces are scratch: nothing in them has to survive the call or to be cleared before it.
  *    Two calls that may run at the same time (on two streams, or in two graphs that are replayed at
  *    the same time) need a workspace each; calls that run one after the other may share one.
@@ -66,6 +67,8 @@ typedef struct {
  *               read by m3_gated_scan_backward                                 NULL: not wanted
  *   workspace   m3_gated_scan_workspace_bytes(dims, packed) bytes, 16-byte aligned
  *                                                       required when that is not 0
+ * Sizes: fewer than 2^23 blocks of 64 tokens and 128 channels (b ceil(L / 64) ceil(D / 128), packed
+ * ceil(T / 64) ceil(D / 128)); more are refused.  The workspace's size is for the current device.
  * Results do not depend on scheduling: equal inputs give equal bits.
  */
 int64_t m3_gated_scan_chunks(const m3_scan_dims* dims, int packed);
@@ -80,7 +83,7 @@ m3_status m3_gated_scan(const m3_scan_dims* dims, const int32_t* cu_seqlens, con
  *   gate, x, y  [b, D] io with their pitches;  bias [D] f32 or NULL
  *   h           [b, D] f32 state before the token
  *   h_out       [b, D] f32 state after it; may be h (updated in place)
- * y may be x or gate itself (same pitch).
+ * y may be x or gate itself (same pitch).  b * D must be below 2^31.
  */
 m3_status m3_gated_scan_step(const m3_scan_dims* dims, const void* gate, const void* x,
                              const float* bias, const float* h, void* y, float* h_out,
@@ -198,8 +201,8 @@ typedef struct {
  *
  *   tensors    host array (read before the call returns); entries with numel 0 are skipped
  *   stats      [2] f32: norm, coef
- *   workspace  m3_grad_workspace_bytes(tensors, count) bytes, 16-byte aligned; 0 only if there is
- *              nothing to sum
+ *   workspace  m3_grad_workspace_bytes(tensors, count) bytes, 16-byte aligned; 0 where one
+ *              workgroup does it all (and where there is nothing to sum)
  * m3_grad_clip also writes dst = round(coef * src) for every tensor (coef = 1 copies; nothing is
  * written where dst is src and coef is 1).  dst must not overlap another entry's src or dst; a
  * tensor listed twice counts twice in m3_grad_norm and is refused by m3_grad_clip.

@@ -108,11 +108,13 @@ m3_status check_scan_dims(const m3_scan_dims* d) {
 // loses beyond (147 -> 160 us at 64 x 256 tokens); its backward pass gains as bf16 does (260 -> 241 us at 128 x 128).
 constexpr int64_t kMaxLoneTiles = 512;   // two workgroups on each of 256 compute units
 constexpr int64_t kMaxSerialTiles = 2, kMaxFullSerialTiles = 8;
+constexpr int64_t kMaxScanBlocks = (int64_t)1 << 23;
 // Workgroups that keep the GPU full: no last round of two to a compute unit that is mostly empty.
 bool fills_rounds(int64_t wgs) {
     const int64_t slots = 2 * (int64_t)m3::device_cus(), rounds = (wgs + slots - 1) / slots;
     return rounds > 0 && wgs * 100 >= rounds * slots * 85;
 }
+
 // The tiles of the forward or the backward pass, and the blocks that have a row of `states`.
 m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan* p) {
     M3_TRY(check_scan_dims(d));
@@ -133,8 +135,9 @@ m3_status plan_scan(const m3_scan_dims* d, bool packed, bool backward, ScanPlan*
         p->ntiles = std::max<int64_t>(1, (p->T + tile - 1) / tile);
         p->blocks = std::max<int64_t>(1, (p->T + block - 1) / block);
     }
-    if (p->blocks >= kMaxCount || p->blocks * p->ncols >= kMaxCount)
-        return fail(M3_E_DIMS, "%lld tokens of %lld channels: more than 2^31 blocks of 64 tokens and 128 channels",
+    // a launch has fewer than 2^32 threads, and 512 of them to a tile
+    if (p->blocks >= kMaxScanBlocks || p->blocks * p->ncols >= kMaxScanBlocks)
+        return fail(M3_E_DIMS, "%lld tokens of %lld channels: the limit is 2^23 blocks of 64 tokens and 128 channels",
                     (long long)p->T, (long long)d->width);
     const int64_t wgs = p->per_seq ? d->batch * p->ncols : p->ncols;
     p->serial = !p->per_seq                        ? p->ntiles <= 1
@@ -418,7 +421,7 @@ m3_status m3_gated_scan_step(const m3_scan_dims* d, const void* gate, const void
     M3_TRY(check_scan_dims(d));
     if (d->seqlen != 1) return fail(M3_E_DIMS, "m3_gated_scan_step takes one token: seqlen = %lld", (long long)d->seqlen);
     const int64_t es = d->io == M3_BF16 ? 2 : 4, D = d->width, b = d->batch;
-    if (b * D >= (int64_t)1 << 38) return fail(M3_E_DIMS, "size out of range");
+    if (b * D >= kMaxCount) return fail(M3_E_DIMS, "%lld rows of %lld channels: the limit is 2^31 elements", (long long)b, (long long)D);
     int64_t gp, xp, yp;
     M3_TRY(check_scan_pitch(d->gate_pitch, b, D, es, "gate_pitch", &gp));
     M3_TRY(check_scan_pitch(d->x_pitch, b, D, es, "x_pitch", &xp));

@@ -10,10 +10,10 @@
 namespace m3 {
 
 // ---------------------------------------------------------------------------- gated scan
-// A tile is kScanTile tokens (backward: kScanBwdTile) x kScanCols channels, worked on by one workgroup; `states` has a row per
-// block of kScanBlock tokens, whatever the type.  Dense batches of sequences longer than a block are
-// cut sequence by sequence (`per_seq`), and so are few shorter ones; many shorter ones and packed batches
-// are cut along the flat token axis, so a tile can hold many sequences.
+// A tile is kScanTile tokens (backward: kScanBwdTile) x kScanCols channels, worked on by one workgroup;
+// `states` has a row per block of kScanBlock tokens in either pass.  Dense batches of sequences longer than a
+// block are cut sequence by sequence (`per_seq`), and so are few shorter ones; many shorter ones and packed
+// batches are cut along the flat token axis, so a tile can hold many sequences.
 constexpr int kScanTile = 128, kScanBwdTile = 64, kScanBlock = 64;
 constexpr int kScanCols = 128;
 
@@ -104,8 +104,9 @@ int64_t rmsnorm_backward_parts(int64_t rows, int64_t D, bool bf16_io, int cus);
 hipError_t launch_column_sum(const float* part, int64_t n, int64_t D, float* out, hipStream_t s);
 
 constexpr int kGradBatch = 96;           // tensors per launch (their table is a kernel argument)
-// Elements per unit of work, and workgroups (and partial sums) per launch at most: 300 x 500000 fp32 in place 419 us,
-// with 1024 or 4096 workgroups 5% more; units of 8192 cost 40 x 500000 a quarter more, of 32768 20 x 50000 too.
+// Elements per unit of work, and workgroups (and partial sums) per launch at most.  Where nothing is clipped: 60 x
+// 3333333 fp32 148 us, with 1024 or 4096 workgroups 157 and 155; 40 x 500000 31 us, 39 with units of 8192; 20 x
+// 50000 7.3 us, 9.4 with units of 32768.
 constexpr int64_t kGradChunk = 16384;
 constexpr int kGradBlocks = 2048;
 // As many elements in one table are left to a single workgroup, a unit of kGradSmallChunk to a wave: one launch

@@ -205,6 +205,13 @@ def test_pitches_and_sizes():
     assert FWD(dims=scan_dims(batch=1, seqlen=1 << 30, x_pitch=big)) == m3scan.M3_E_DIMS
     assert FWD(dims=scan_dims(y_pitch=1 << 23)) == m3scan.M3_E_DIMS and "2^24" in m3scan.last_error()
     assert m3block.load().m3_gated_scan_workspace_bytes(ctypes.byref(scan_dims(batch=big, seqlen=big)), 0) == 0
+    # a launch's threads: 2^23 blocks of 64 tokens and 128 channels are one too many
+    many = {n: scan_dims(batch=1 << 22, seqlen=n, width=1) for n in (64, 65)}      # one and two blocks to a sequence
+    rows = {n: m3block.load().m3_gated_scan_chunks(ctypes.byref(d), 0) for n, d in many.items()}
+    assert rows == {64: 1 << 22, 65: 0}
+    for call in (FWD, BWD):
+        assert call(dims=many[65], cu=0) == m3scan.M3_E_DIMS and "2^23" in m3scan.last_error()
+    assert STEP(dims=scan_dims(batch=1 << 16, width=1 << 15, seqlen=1)) == m3scan.M3_E_DIMS and "2^31" in m3scan.last_error()
     assert STEP(dims=scan_dims(seqlen=2)) == m3scan.M3_E_DIMS
     assert NORM(dims=norm_dims(width=16385)) == m3scan.M3_E_UNSUPPORTED
     assert NORM(dims=norm_dims(group=48)) == m3scan.M3_E_UNSUPPORTED
