@@ -366,17 +366,40 @@ __device__ __forceinline__ void to_seq(float* p, int64_t seq, int64_t D, const C
     for (int v = 0; v < 2; ++v)
         if (cols.ok[v]) p[seq * D + cols.d[v]] = o[v];
 }
-// empty sequences pass `from` (0 without one) through to `to`
+// Empty sequences pass `from` (0 without one) through to `to`.  512 sequences to a tile at a time, every 8th of
+// them to a wave, one to a lane to find the empty ones, which are then copied four at a time.
 template <typename T, bool VEC>
-__device__ __forceinline__ void pass_empty(const GatedScanArgs& a, uint32_t c, const Cols<T, VEC>& cols, const float* from,
-                                           float* to) {
+__device__ __forceinline__ void pass_empty(const GatedScanArgs& a, uint32_t c, const Cols<T, VEC>& cols, int lane, int w,
+                                           const float* from, float* to) {
     if (a.cu == nullptr && a.L != 0) return;
-    for (int64_t s = c; s < a.b; s += a.ntiles) {
-        if (seq_start(a, s + 1) > seq_start(a, s)) continue;
-        float v[2];
-        from_seq(from, s, a.D, cols, v);
-        to_seq(to, s, a.D, cols, v);
+    for (int64_t s0 = (int64_t)c * (64 * kWaves); s0 < a.b; s0 += a.ntiles * (64 * kWaves)) {
+        const int64_t mine = s0 + lane * kWaves + w;
+        uint64_t empty = __ballot(mine < a.b && !(seq_start(a, mine + 1) > seq_start(a, mine)));
+        while (empty != 0) {
+            int64_t s[4];
+            float v[4][2];
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[k] = s0 + (empty ? __builtin_ctzll(empty) : 0) * kWaves + w;
+                n += empty != 0 ? 1 : 0;
+                empty &= empty - 1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) from_seq(k < n ? from : nullptr, s[k], a.D, cols, v[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < n) to_seq(to, s[k], a.D, cols, v[k]);
+        }
     }
+}
+// The sequences of a wave's N tokens, one to a lane (FLAT), so that they are read once and together.
+template <int N, bool FLAT, bool SERIAL>
+__device__ __forceinline__ int seqs_of(const GatedScanArgs& a, const int* marks, int64_t tw, int lane, int w, int nv) {
+    const int i = min(lane & (N - 1), nv - 1);
+    if constexpr (!FLAT) return 0;
+    else if constexpr (SERIAL) return marks[w * N + i];
+    else return a.seqs[tw + i];
 }
 
 template <typename T, bool FLAT, bool SERIAL>
@@ -439,24 +462,36 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
                 add[i][0] = add[i][1] = 0.f;
             }
     }
+    const int ids = (starts | ends) != 0 ? seqs_of<N, FLAT, SERIAL>(a, sh.marks.seq, tw, lane, w, nv) : 0;
     auto seq_at = [&](int i) -> int64_t {
-        if constexpr (FLAT && SERIAL) return uniform32((uint32_t)sh.marks.seq[w * N + i]);
-        else if constexpr (FLAT) return uniform32((uint32_t)a.seqs[tw + i]);
+        if constexpr (FLAT) return __builtin_amdgcn_readlane(ids, i);
         else return tile.seq;
     };
+    auto first = [&](int i) { return (FLAT || i == 0) && ((starts >> i) & 1) != 0; };
+    if (starts != 0 && a.h_in) {               // the states that sequences start from are in their first tokens' `add`
+        constexpr int K = FLAT ? 8 : 1;        // as many are read together
+#pragma unroll
+        for (int i = 0; i < (FLAT ? N : 1); i += K) {
+            float h0[K][2];
+#pragma unroll
+            for (int k = 0; k < K; ++k) from_seq(a.h_in, seq_at(i + k), a.D, cols, h0[k]);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (first(i + k)) {
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) add[i + k][v] = fmaf(keep[i + k][v], h0[k][v], add[i + k][v]);
+                }
+        }
+    }
     float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f};   // the wave's map
     auto step = [&](int i, float (&h)[2]) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) h[v] = fmaf(keep[i][v], h[v], add[i][v]);
+        for (int v = 0; v < 2; ++v) h[v] = first(i) ? add[i][v] : fmaf(keep[i][v], h[v], add[i][v]);
     };
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if ((FLAT || i == 0) && ((starts >> i) & 1)) {
-            A[0] = A[1] = 0.f;
-            from_seq(a.h_in, seq_at(i), a.D, cols, B);
-        }
-        A[0] *= keep[i][0];
-        A[1] *= keep[i][1];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) A[v] = first(i) ? 0.f : A[v] * keep[i][v];
         step(i, B);
     }
     sh.sA[w][lane] = make_float2(A[0], A[1]);
@@ -527,7 +562,8 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
     if (nv == N && (starts | ends) == 0) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            step(i, h);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) h[v] = fmaf(keep[i][v], h[v], add[i][v]);
             store_pair<T, VEC>(yr, cols.off[0], cols.off[1], row, h[0], h[1]);
             row += (int)a.y_p;
         }
@@ -535,7 +571,6 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (i < nv) {
-                if ((starts >> i) & 1) from_seq(a.h_in, seq_at(i), a.D, cols, h);
                 step(i, h);
                 store_pair<T, VEC>(yr, cols.off[0], cols.off[1], row, h[0], h[1]);
                 row += (int)a.y_p;
@@ -543,7 +578,7 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
             }
         }
     }
-    if (FLAT && w == 0) pass_empty(a, c, cols, a.h_in, a.h_out);
+    if (FLAT) pass_empty(a, c, cols, lane, w, a.h_in, a.h_out);
 }
 
 // SERIAL: a workgroup takes one sequence (FLAT: the whole batch) tile by tile: no chain to wait for, none to
@@ -633,10 +668,26 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
                 dy[i].zero();
             }
     }
+    const int ids = (starts | ends) != 0 ? seqs_of<N, FLAT, SERIAL>(a, sh.marks.seq, tw, lane, w, nv) : 0;
     auto seq_at = [&](int i) -> int64_t {
-        if constexpr (FLAT && SERIAL) return uniform32((uint32_t)sh.marks.seq[w * N + i]);
-        else if constexpr (FLAT) return uniform32((uint32_t)a.seqs[tw + i]);
+        if constexpr (FLAT) return __builtin_amdgcn_readlane(ids, i);
         else return tile.seq;
+    };
+    auto first = [&](int i) { return (FLAT || i == 0) && ((starts >> i) & 1) != 0; };
+    auto last = [&](int i) { return ((ends >> i) & 1) != 0; };
+    // the rows of p that belong to the tokens' sequences, read together
+    auto at_marks = [&](const float* p, float (&o)[N][2]) {
+        if constexpr (FLAT) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) from_seq(p, seq_at(i), a.D, cols, o[i]);
+        } else {
+            from_seq(p, tile.seq, a.D, cols, o[0]);
+#pragma unroll
+            for (int i = 1; i < N; ++i) {
+                o[i][0] = o[0][0];
+                o[i][1] = o[0][1];
+            }
+        }
     };
     {   // the wave's maps, forwards and backwards
         float A[2] = {1.f, 1.f}, B[2] = {0.f, 0.f}, RA[2] = {1.f, 1.f}, RB[2] = {0.f, 0.f};
@@ -649,18 +700,15 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
                     B[v] = fmaf(keep[i][v], B[v], z[i][v] * x[i].get(v));
                 }
         } else {
+            float h0[N][2];
+            at_marks(a.h_in, h0);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if ((FLAT || i == 0) && ((starts >> i) & 1)) {
-                    A[0] = A[1] = 0.f;
-                    from_seq(a.h_in, seq_at(i), a.D, cols, B);
-                }
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    A[v] *= keep[i][v];
-                    B[v] = fmaf(keep[i][v], B[v], z[i][v] * x[i].get(v));
+                    A[v] = first(i) ? 0.f : A[v] * keep[i][v];
+                    B[v] = fmaf(keep[i][v], first(i) ? h0[i][v] : B[v], z[i][v] * x[i].get(v));
                 }
-            }
         }
         forget(x);
         if (ends == 0) {
@@ -672,18 +720,15 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
                     RB[v] = keep[i][v] * (RB[v] + dy[i].get(v));
                 }
         } else {
+            float l0[N][2];
+            at_marks(a.dh_out, l0);
 #pragma unroll
-            for (int i = N - 1; i >= 0; --i) {
-                if ((ends >> i) & 1) {
-                    RA[0] = RA[1] = 0.f;
-                    from_seq(a.dh_out, seq_at(i), a.D, cols, RB);
-                }
+            for (int i = N - 1; i >= 0; --i)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    RA[v] *= keep[i][v];
-                    RB[v] = keep[i][v] * (RB[v] + dy[i].get(v));
+                    RA[v] = last(i) ? 0.f : RA[v] * keep[i][v];
+                    RB[v] = keep[i][v] * ((last(i) ? l0[i][v] : RB[v]) + dy[i].get(v));
                 }
-            }
         }
         sh.sA[w][lane] = make_float2(A[0], A[1]);
         sh.sB[w][lane] = make_float2(B[0], B[1]);
@@ -756,14 +801,25 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
     }
     // forwards: what dgate is of l_t
     float fac[N][2];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if ((FLAT || i == 0) && ((starts >> i) & 1)) from_seq(a.h_in, seq_at(i), a.D, cols, h);
+    auto factor = [&](int i) {
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
             const float xv = x[i].get(v);
             fac[i][v] = z[i][v] * keep[i][v] * (xv - h[v]);
             h[v] = fmaf(keep[i][v], h[v], z[i][v] * xv);
+        }
+    };
+    if (starts == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) factor(i);
+    } else {
+        float h0[N][2];
+        at_marks(a.h_in, h0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) h[v] = first(i) ? h0[i][v] : h[v];
+            factor(i);
         }
     }
     __syncthreads();
@@ -795,16 +851,19 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
 #pragma unroll
         for (int i = N - 1; i >= 0; --i) token(i);
     } else {
+        float l0[N][2];
+        if (ends != 0) at_marks(a.dh_out, l0);
 #pragma unroll
         for (int i = N - 1; i >= 0; --i) {
             if (i < nv) {
-                if ((ends >> i) & 1) from_seq(a.dh_out, seq_at(i), a.D, cols, G);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) G[v] = last(i) ? l0[i][v] : G[v];
                 token(i);
-                if ((FLAT || i == 0) && ((starts >> i) & 1) && a.dh_in) to_seq(a.dh_in, seq_at(i), a.D, cols, G);
+                if (first(i) && a.dh_in) to_seq(a.dh_in, seq_at(i), a.D, cols, G);
             }
         }
     }
-    if (FLAT && w == 0 && a.dh_in) pass_empty(a, c, cols, a.dh_out, a.dh_in);
+    if (FLAT && a.dh_in) pass_empty(a, c, cols, lane, w, a.dh_out, a.dh_in);
 }
 
 // the workgroup's share of dbias: its waves' added in order
