@@ -118,6 +118,17 @@ def test_packed(io, lens):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("most,carry", [(0, True), (1, True), (2, False), (3, True)])
+def test_many_short_sequences(io, most, carry):
+    """1300 sequences of up to `most` tokens, empty ones among them: more than the waves of a tile look through at
+    once, and starts and ends at any place of a wave's tokens."""
+    g = torch.Generator().manual_seed(most)
+    lens = torch.randint(0, most + 1, (1300,), generator=g).tolist()
+    c = draw(sum(lens), 70, len(lens), IO[io], seed=40 + most, carry=carry)
+    check(c, lens, run(c, lens, packed=True, tail=3))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("layout", ["sliced", "odd"])
 @pytest.mark.parametrize("d", [128, 131])
 def test_layouts(io, layout, d):
