@@ -215,7 +215,8 @@ m3_status check_grads(const m3_grad_tensor* t, int64_t n, bool write) {
         if (t[i].numel < 0 || t[i].numel >= ((int64_t)1 << 40))
             return fail(M3_E_DIMS, "tensor %lld: numel out of range", (long long)i);
         if (t[i].numel == 0) continue;
-        if (!t[i].src || (write && !t[i].dst)) return fail(M3_E_NULL, "tensor %lld: %s is NULL", (long long)i, t[i].src ? "dst" : "src");
+        if (!t[i].src || (write && !t[i].dst))
+            return fail(M3_E_NULL, "tensor %lld: %s is NULL", (long long)i, t[i].src ? "dst" : "src");
         const size_t es = t[i].io == M3_BF16 ? 2 : 4;
         if (!aligned(t[i].src, es) || (write && !aligned(t[i].dst, es)))
             return fail(M3_E_ALIGN, "tensor %lld is not aligned to its elements", (long long)i);
@@ -246,7 +247,8 @@ m3_status check_grad_overlap(const m3_grad_tensor* t, int64_t n, const Extent* m
     uintptr_t any_hi = 0, out_hi = 0;
     for (const Extent& x : e) {
         if (x.lo < out_hi || (x.out && x.lo < any_hi)) {
-            if (x.i >= 0) return fail(M3_E_ALIAS, "tensor %lld overlaps another tensor, stats or the workspace", (long long)x.i);
+            if (x.i >= 0)
+                return fail(M3_E_ALIAS, "tensor %lld overlaps another tensor, stats or the workspace", (long long)x.i);
             return fail(M3_E_ALIAS, "stats or the workspace overlap a tensor");
         }
         any_hi = std::max(any_hi, x.hi);
@@ -326,7 +328,8 @@ m3_status grads(const char* fn, bool write, const m3_grad_tensor* t, int64_t n, 
     } else {
         for (int64_t i = 0; i < n; ++i)
             for (const Extent& x : more)
-                if (m3::overlap((const void*)x.lo, x.hi - x.lo, t[i].src, (size_t)t[i].numel * (t[i].io == M3_BF16 ? 2 : 4)))
+                if (m3::overlap((const void*)x.lo, x.hi - x.lo, t[i].src,
+                                (size_t)t[i].numel * (t[i].io == M3_BF16 ? 2 : 4)))
                     return fail(M3_E_ALIAS, "stats or the workspace overlap tensor %lld", (long long)i);
         if (m3::overlap(stats, 8, ws, grad_bytes(p))) return fail(M3_E_ALIAS, "stats overlaps the workspace");
     }
@@ -421,7 +424,8 @@ m3_status m3_gated_scan_step(const m3_scan_dims* d, const void* gate, const void
     M3_TRY(check_scan_dims(d));
     if (d->seqlen != 1) return fail(M3_E_DIMS, "m3_gated_scan_step takes one token: seqlen = %lld", (long long)d->seqlen);
     const int64_t es = d->io == M3_BF16 ? 2 : 4, D = d->width, b = d->batch;
-    if (b * D >= kMaxCount) return fail(M3_E_DIMS, "%lld rows of %lld channels: the limit is 2^31 elements", (long long)b, (long long)D);
+    if (b * D >= kMaxCount)
+        return fail(M3_E_DIMS, "%lld rows of %lld channels: the limit is 2^31 elements", (long long)b, (long long)D);
     int64_t gp, xp, yp;
     M3_TRY(check_scan_pitch(d->gate_pitch, b, D, es, "gate_pitch", &gp));
     M3_TRY(check_scan_pitch(d->x_pitch, b, D, es, "x_pitch", &xp));
@@ -524,7 +528,8 @@ m3_status m3_rmsnorm(const m3_norm_dims* d, const void* x, const void* residual,
     a.ngroups = (int)ng;
     a.eps = d->eps;
     a.cus = m3::device_cus();
-    a.stream = n * D * (es * (1 + (residual != nullptr) + (r_out != nullptr) + (y != nullptr)) + (q != nullptr)) > kCacheBytes;
+    const int64_t moved = es * (1 + (residual != nullptr) + (r_out != nullptr) + (y != nullptr)) + (q != nullptr);
+    a.stream = n * D * moved > kCacheBytes;
     return launched(m3::launch_rmsnorm(a, es == 2, stream), "m3_rmsnorm");
 }
 

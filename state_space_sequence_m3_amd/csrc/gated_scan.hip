@@ -5,16 +5,31 @@
 // end from a zero state, and maps compose: (A2, B2) after (A1, B1) is (A2 A1, A2 B1 + B2).  A
 // sequence's first token forgets what came before: its map is h -> B (A = 0), with B taking the
 // carried h_in in.
+//
+// Bound: memory.  A forward pass reads gate and x and writes y, a backward pass reads gate, x and dy and writes
+// dgate and dx; the arithmetic (an exponential, a reciprocal and some six more per element) hides behind that.  So
+// every element travels once: a workgroup takes a tile of 128 tokens (backward 64) x 128 channels, each of its 8
+// waves 16 (8) consecutive tokens, two channels to a lane, all in registers from the load to the store; the waves'
+// maps are composed through shared memory, the tiles' through a chain of words in the workspace, and the tokens are
+// then run once more from registers.  b8 L2048 D4096 bf16: 403 MB in 89 us, 4.5 TB/s, backward 671 MB in 157 us, 4.3
+// TB/s (a copy of that size: 5.3 to 5.5 TB/s); fp32 151 us, 5.3 TB/s, and 254 us, 5.3 TB/s.  What is left: 4 us for
+// the launch that resets the chain, 5 us for taking tiles in order, and waits for the chain: one sequence of
+// 16384 tokens takes 93 us, and 76, a copy's time, without the three.
+// Shapes, b8 L2048 D4096 fp32 unless said: 4 waves to a tile of 64 tokens 160 us, 16 waves to one of 256 170 us;
+// fp32 in tiles of 64 tokens 111 us instead of 100 (13 packed sequences); a backward tile of 128 tokens spills
+// (bf16 420 us); workgroups that stay and fetch the next tile ahead 110 us (bf16), backward 433 us; gates computed
+// again for the second run instead of held 107 us (bf16).
 #include "block_launch.h"
 #include "m3_device.h"
 
 namespace m3 {
 namespace {
 
-constexpr int kWaves = 8;   // waves per tile; each holds kSteps consecutive tokens in registers
+constexpr int kWaves = 8;          // waves per tile; each holds as many consecutive tokens in registers
 constexpr int kFwdSteps = kScanTile / kWaves, kBwdSteps = kScanBwdTile / kWaves;
-constexpr uint32_t kSideBySide = 4;
-constexpr int kWavesPerSimd = 4;   // two workgroups on a compute unit: 128 registers
+constexpr uint32_t kSideBySide = 4;   // sequences whose tiles are taken in turns: 94.3 us, 2 of them 95.8, 8 of them 94.2
+constexpr int kWavesPerSimd = 4;   // two workgroups on a compute unit: 128 registers.  3 waves: 126 us for 94, 5: 98
+constexpr int kWindow = 4;         // chain words looked at together: 94 us, 6 of them 98, 8 of them 102
 
 // z = sigmoid(u) and keep = 1 - z, both to a few units in their last place: with e = e^-|u| the larger of
 // the two is 1 / (1 + e) and the smaller one e / (1 + e), never a difference from 1.  The logit comes
@@ -267,8 +282,7 @@ constexpr int kMaxPolls = 1 << 22;    // some seconds: a wait that long means a 
 // does not depend on which word was found final.  Ends: workgroups take tiles from a counter in
 // chain order, so every tile waited for here is held by a workgroup that runs (or is done) and
 // itself waits for earlier ones only; the first tile of a chain waits for none.  A wait that
-// outlasts kMaxPolls gives NaN.
-template <int kWindow>   // words looked at together
+// outlasts kMaxPolls gives NaN.  kWindow words are looked at together.
 __device__ __forceinline__ void chain_wait(const uint64_t* words, int64_t stride, int64_t first, int64_t step,
                                            uint32_t links, const int (&d)[2], float (&carry)[2]) {
     for (int poll = 0; poll < kMaxPolls; ++poll) {
@@ -356,7 +370,8 @@ __device__ __forceinline__ int clamp_rows(int left, int n) { return left < 0 ? 0
 
 // the values of sequence seq in a [b, D] tensor, 0 without one
 template <typename T, bool VEC>
-__device__ __forceinline__ void from_seq(const float* p, int64_t seq, int64_t D, const Cols<T, VEC>& cols, float (&o)[2]) {
+__device__ __forceinline__ void from_seq(const float* p, int64_t seq, int64_t D, const Cols<T, VEC>& cols,
+                                         float (&o)[2]) {
 #pragma unroll
     for (int v = 0; v < 2; ++v) o[v] = p && cols.ok[v] ? p[seq * D + cols.d[v]] : 0.f;
 }
@@ -413,8 +428,8 @@ struct FwdShared {
 // One tile.  SERIAL: `state`, the last wave's, is the state before the tile, and then the one after it; else it
 // comes from the chain.
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
-__device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T, FLAT, SERIAL>& sh, uint32_t c, int col, int lane,
-                                             int w, float (&state)[2]) {
+__device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T, FLAT, SERIAL>& sh, uint32_t c, int col,
+                                             int lane, int w, float (&state)[2]) {
     constexpr int N = kFwdSteps, TILE = kWaves * N;
     const Tile tile = tile_of<TILE, FLAT, SERIAL>(a, c);
     const Cols<T, VEC> cols(col, lane, a.D);
@@ -536,7 +551,7 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
             const bool starts_here = (uniform32(sh.sHard[0]) & 2) != 0;
             if (tile.before > 0 && tile.nv > 0 && !starts_here) {
                 const int64_t step = -tile.link;
-                chain_wait<4>(a.words, stride, c + step, step, tile.before, cols.d, carry);
+                chain_wait(a.words, stride, c + step, step, tile.before, cols.d, carry);
             }
             if (!hard) {
 #pragma unroll
@@ -780,7 +795,7 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
             for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], hard ? final_word(Bp[v]) : map_word(Ap[v], Bp[v]));
             if (tile.after > 0 && !ends_here) {
                 const int64_t step = tile.link;
-                chain_wait<4>(a.words, stride, c + step, step, tile.after, cols.d, carry);
+                chain_wait(a.words, stride, c + step, step, tile.after, cols.d, carry);
             }
             if (!hard) {
 #pragma unroll
@@ -868,8 +883,8 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
 
 // the workgroup's share of dbias: its waves' added in order
 template <typename T, bool VEC, bool FLAT, bool SERIAL>
-__device__ __forceinline__ void add_dbias(const GatedScanArgs& a, BwdShared<T, FLAT, SERIAL>& sh, uint32_t row, int col, int lane,
-                                          int w, const float (&sum)[2]) {
+__device__ __forceinline__ void add_dbias(const GatedScanArgs& a, BwdShared<T, FLAT, SERIAL>& sh, uint32_t row, int col,
+                                          int lane, int w, const float (&sum)[2]) {
     if (a.dbias == nullptr) return;
     __syncthreads();
     sh.sA[w][lane] = make_float2(sum[0], sum[1]);

@@ -6,6 +6,9 @@
 // outputs and the 8-bit scale.  Where 8 does not divide the width, the row's last chunk is moved back to
 // end with the row: it reads and writes whole, and its first `skip` elements, which belong to the chunk
 // before it as well, are left out of sums and scales (both chunks write the same values there).
+//
+// Bound: memory, each tensor travelling once.  16384 x 4096 bf16, x and residual in, r, y and q out: 604 MB in 118 us,
+// 5.1 TB/s; backward with dr_out 537 MB in 104 us, 5.2 TB/s (a copy: 5.3 to 5.5).  Sums and statistics are in fp32.
 #include "block_launch.h"
 #include "m3_device.h"
 
@@ -404,7 +407,11 @@ __global__ __launch_bounds__(max_threads<TPR>(), (kBwdOcc<T, C>)) void rmsnorm_b
     }
 }
 
-// How rows of D elements are laid out: lanes per row (kBlock: a workgroup), chunks, threads per workgroup.
+// How rows of D elements are laid out: lanes per row (kBlock: a workgroup), chunks, threads per workgroup.  A row
+// is on as few lanes as hold it in 8 (or 16) elements each, so that loads are 16 bytes and few lanes idle: 65536 x
+// 64 on a wave each took 39 us backward, on 16 lanes 17; 30000 x 1111 on a workgroup of 4 waves 104 us, on the 3 it
+// needs 61.  65536 x 768 on a wave with two chunks 71 us, on a workgroup of two waves 72 (fp32 129, 134); 8000 x
+// 8192 fp32 with one chunk 163 us, with two 180.
 struct Plan {
     int tpr, chunks, threads;
 };

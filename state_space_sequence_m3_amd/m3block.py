@@ -238,8 +238,8 @@ def m3_gated_scan(gate, x, bias=None, h_in=None, cu_seqlens=None, y=None, h_out=
         else:
             _dense(states, "states", (rows, D), f32, dev)
     workspace, ws_bytes = _workspace(workspace, need, x)
-    _check(lib.m3_gated_scan(ctypes.byref(dims), _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, y.data_ptr(), h_out_p,
-                             _ptr(states), _ptr(workspace), ws_bytes, _raw_stream(at)))
+    _check(lib.m3_gated_scan(ctypes.byref(dims), _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p,
+                             y.data_ptr(), h_out_p, _ptr(states), _ptr(workspace), ws_bytes, _raw_stream(at)))
     return (y, h_out) if states is None else (y, h_out, states)
 
 
@@ -253,7 +253,8 @@ def m3_gated_scan_step(gate, x, h, bias=None, y=None, h_out=None, stream=None):
     b, D = shape
     dense = x.is_contiguous()
     xp = 0 if dense else _pitch(x, "x", shape, io, dev)
-    dims = M3ScanDims(b, 1, D, _pitch(gate, "gate", shape, io, dev), xp, 0 if y is None else _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
+    dims = M3ScanDims(b, 1, D, _pitch(gate, "gate", shape, io, dev), xp,
+                      0 if y is None else _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
     bias_p = None if bias is None else _dense(bias, "bias", (D,), f32, dev)
     h_p = h_out_p = _dense(h, "h", shape, f32, dev)
     if h_out is not None:
@@ -304,9 +305,9 @@ def m3_gated_scan_backward(gate, x, dy, states, bias=None, h_in=None, dh_out=Non
         g["h_in"] = x.new_empty((b, D), dtype=f32)
     workspace, ws_bytes = _workspace(workspace, need, x)
     _check(lib.m3_gated_scan_backward(
-        ctypes.byref(dims), _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, states_p, dy.data_ptr(), dh_out_p,
-        g["gate"].data_ptr(), g["x"].data_ptr(), _ptr(g.get("bias")), _ptr(g.get("h_in")), _ptr(workspace), ws_bytes,
-        _raw_stream(at)))
+        ctypes.byref(dims), _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, states_p, dy.data_ptr(),
+        dh_out_p, g["gate"].data_ptr(), g["x"].data_ptr(), _ptr(g.get("bias")), _ptr(g.get("h_in")), _ptr(workspace),
+        ws_bytes, _raw_stream(at)))
     return g
 
 
