@@ -27,9 +27,11 @@ namespace {
 
 constexpr int kWaves = 8;          // waves per tile; each holds as many consecutive tokens in registers
 constexpr int kFwdSteps = kScanTile / kWaves, kBwdSteps = kScanBwdTile / kWaves;
-constexpr uint32_t kSideBySide = 4;   // sequences whose tiles are taken in turns: 94.3 us, 2 of them 95.8, 8 of them 94.2
+// Sequences whose tiles are taken in turns: b8 L2048 D4096 bf16 82 us, backward 144; 1: 88, 154, 2: 86, 148; 8: 82,
+// 143, but 16 x 1024 fp32 backward 254 -> 272.
+constexpr uint32_t kSideBySide = 4;
 constexpr int kWavesPerSimd = 4;   // two workgroups on a compute unit: 128 registers.  3 waves: 126 us for 94, 5: 98
-constexpr int kWindow = 4;         // chain words looked at together: 94 us, 6 of them 98, 8 of them 102
+constexpr uint32_t kFar = 56;      // chain words looked at, at most: 1 KB of shared memory each
 
 // z = sigmoid(u) and keep = 1 - z, both to a few units in their last place: with e = e^-|u| the larger of
 // the two is 1 / (1 + e) and the smaller one e / (1 + e), never a difference from 1.  The logit comes
@@ -279,41 +281,53 @@ constexpr int kMaxPolls = 1 << 22;    // some seconds: a wait that long means a 
 // The state that enters a tile whose neighbour in the chain is `first`, the one after that
 // first + step, and so on for `links` tiles.  It starts from the nearest final word and applies
 // the maps after it in order.  A tile's own final word is made by the same steps, so the value
-// does not depend on which word was found final.  Ends: workgroups take tiles from a counter in
-// chain order, so every tile waited for here is held by a workgroup that runs (or is done) and
-// itself waits for earlier ones only; the first tile of a chain waits for none.  A wait that
-// outlasts kMaxPolls gives NaN.  kWindow words are looked at together.
+// does not depend on which word was found final.  Words are read one by one, the next only while all
+// so far are maps: reads beyond the final word cost more than they save where many channels keep it near
+// (b8 L2048 D4096 bf16: one at a time 83 us, backward 143; four 88, 151), and where few channels
+// leave many tiles of one chain running at once it is far (b1 L65536 D256 bf16: up to 4 words 147 us,
+// backward 282; up to 16: 75, 131; up to 56: 57, 92).  Ends: workgroups take tiles from a counter in chain order, so
+// every tile waited for here is held by a workgroup that runs (or is done) and itself waits for
+// earlier ones only; the first tile of a chain waits for none.  A wait that outlasts kMaxPolls gives NaN.
+template <uint32_t N>
+struct FarWords {
+    uint64_t w[N][2][64];
+};
 __device__ __forceinline__ void chain_wait(const uint64_t* words, int64_t stride, int64_t first, int64_t step,
-                                           uint32_t links, const int (&d)[2], float (&carry)[2]) {
+                                           uint32_t links, const int (&d)[2], int lane, FarWords<kFar>& far,
+                                           float (&carry)[2]) {
+    auto apply = [](uint64_t w, float h) {
+        const float B = __uint_as_float((uint32_t)(w >> 32));
+        return (uint32_t)w == kFinal ? B : fmaf(__uint_as_float((uint32_t)w), h, B);
+    };
+    const uint32_t most = links < kFar ? links : kFar;
+#pragma unroll 1
     for (int poll = 0; poll < kMaxPolls; ++poll) {
-        uint64_t w[kWindow][2];
+        bool found[2] = {false, false}, maps[2] = {true, true};   // a final word; only maps so far
+#pragma unroll 1
+        for (uint32_t n = 0; n < most; ++n) {
+            const char* row = (const char*)(words + (first + (int64_t)n * step) * stride);
+            uint64_t w[2];
 #pragma unroll
-        for (int k = 0; k < kWindow; ++k) {
-            if ((uint32_t)k < links) {
-                const char* row = (const char*)(words + (first + k * step) * stride);
-                w[k][0] = get_word((const uint64_t*)(row + (uint32_t)d[0] * 8u));
-                w[k][1] = get_word((const uint64_t*)(row + (uint32_t)d[1] * 8u));
-            } else {
-                w[k][0] = w[k][1] = ~0ull;
+            for (int v = 0; v < 2; ++v) w[v] = get_word((const uint64_t*)(row + (uint32_t)d[v] * 8u));
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                found[v] = found[v] || (maps[v] && (uint32_t)w[v] == kFinal);
+                maps[v] = maps[v] && (uint32_t)w[v] != kFinal && (uint32_t)w[v] != kUnset;
             }
-        }
-        bool done = true;
+            if (__all(found[0] && found[1])) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            bool valid = false;
-            float h = 0.f;
-#pragma unroll
-            for (int k = kWindow - 1; k >= 0; --k) {
-                const uint32_t A = (uint32_t)w[k][v];
-                const float B = __uint_as_float((uint32_t)(w[k][v] >> 32));
-                const float next = A == kFinal ? B : fmaf(__uint_as_float(A), h, B);
-                valid = A == kFinal || (valid && A != kUnset);
-                h = next;
+                for (int v = 0; v < 2; ++v) {
+                    float h = apply(w[v], 0.f);
+#pragma unroll 4
+                    for (int k = (int)n - 1; k >= 0; --k) h = apply(far.w[k][v][lane], h);
+                    carry[v] = h;
+                }
+                return;
             }
-            carry[v] = h;
-            done = done && valid;
+            if (!__all((found[0] || maps[0]) && (found[1] || maps[1]))) break;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) far.w[n][v][lane] = w[v];
         }
-        if (__all(done)) return;
         __builtin_amdgcn_s_sleep(1);
     }
     carry[0] = carry[1] = __uint_as_float(0x7fc00000u);
@@ -422,6 +436,7 @@ struct FwdShared {
     float2 sA[kWaves][64], sB[kWaves][64], sCarry[64];
     int sHard[kWaves];   // bit 0: the wave's tokens hold a sequence start; bit 1: its first token is one
     Marks<FLAT && SERIAL ? kWaves * kFwdSteps : 1> marks;
+    FarWords<SERIAL ? 1 : kFar> far;
     unsigned sTicket;
 };
 
@@ -551,7 +566,7 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
             const bool starts_here = (uniform32(sh.sHard[0]) & 2) != 0;
             if (tile.before > 0 && tile.nv > 0 && !starts_here) {
                 const int64_t step = -tile.link;
-                chain_wait(a.words, stride, c + step, step, tile.before, cols.d, carry);
+                chain_wait(a.words, stride, c + step, step, tile.before, cols.d, lane, sh.far, carry);
             }
             if (!hard) {
 #pragma unroll
@@ -627,6 +642,7 @@ struct BwdShared {
     float2 sA[kWaves][64], sB[kWaves][64], sRA[kWaves][64], sRB[kWaves][64], sCarry[64];
     int sHard[kWaves];   // bit 0: holds a sequence start; 1: holds an end; 2: its last token is an end
     Marks<FLAT && SERIAL ? kWaves * kBwdSteps : 1> marks;
+    FarWords<SERIAL ? 1 : kFar> far;
     unsigned sTicket;
 };
 
@@ -795,7 +811,7 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
             for (int v = 0; v < 2; ++v) put_word(mine + cols.d[v], hard ? final_word(Bp[v]) : map_word(Ap[v], Bp[v]));
             if (tile.after > 0 && !ends_here) {
                 const int64_t step = tile.link;
-                chain_wait(a.words, stride, c + step, step, tile.after, cols.d, carry);
+                chain_wait(a.words, stride, c + step, step, tile.after, cols.d, lane, sh.far, carry);
             }
             if (!hard) {
 #pragma unroll

@@ -85,6 +85,18 @@ def test_dense(io, b, L, d):
     check(c, [L] * b, run(c, [L] * b, packed=False))
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_long_narrow_sequence(packed):
+    """15000 tokens of 3 channels: all of the chain's tiles, over a hundred, run at the same time, so a tile's way back
+    to a state can be as long as it may be.  Same bits every time."""
+    c = draw(15000, 3, 1, torch.float32, 8)
+    got = run(c, [15000], packed)
+    check(c, [15000], got)
+    for _ in range(3):
+        again = run(c, [15000], packed)
+        assert all(torch.equal(got[k], again[k]) for k in got)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_a_workgroup_per_sequence(io):
     """As many sequences as fill the GPU are worked off one by one by their workgroups, without chains: sampled
