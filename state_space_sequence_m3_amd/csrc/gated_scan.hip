@@ -11,10 +11,10 @@
 // every element travels once: a workgroup takes a tile of 128 tokens (backward 64) x 128 channels, each of its 8
 // waves 16 (8) consecutive tokens, two channels to a lane, all in registers from the load to the store; the waves'
 // maps are composed through shared memory, the tiles' through a chain of words in the workspace, and the tokens are
-// then run once more from registers.  b8 L2048 D4096 bf16: 403 MB in 89 us, 4.5 TB/s, backward 671 MB in 157 us, 4.3
-// TB/s (a copy of that size: 5.3 to 5.5 TB/s); fp32 151 us, 5.3 TB/s, and 254 us, 5.3 TB/s.  What is left: 4 us for
+// then run once more from registers.  b8 L2048 D4096 bf16: 403 MB in 84 us, 4.8 TB/s, backward 671 MB in 153 us, 4.4
+// TB/s (a copy of that size: 5.3 to 5.5 TB/s); fp32 149 us, 5.4 TB/s, and 252 us, 5.3 TB/s.  What is left: 4 us for
 // the launch that resets the chain, 5 us for taking tiles in order, and waits for the chain: one sequence of
-// 16384 tokens takes 93 us, and 76, a copy's time, without the three.
+// 16384 tokens takes 91 us, and 76, a copy's time, without the three.
 // Shapes, b8 L2048 D4096 fp32 unless said: 4 waves to a tile of 64 tokens 160 us, 16 waves to one of 256 170 us;
 // fp32 in tiles of 64 tokens 111 us instead of 100 (13 packed sequences); a backward tile of 128 tokens spills
 // (bf16 420 us); workgroups that stay and fetch the next tile ahead 110 us (bf16), backward 433 us; gates computed
