@@ -162,6 +162,8 @@ __device__ __forceinline__ int64_t seq_start(const GatedScanArgs& a, int64_t s) 
     const int64_t v = a.cu[s];
     return v < 0 ? 0 : (v > a.T ? a.T : v);
 }
+// Tokens that belong to sequences: those behind the last one, or without any, are left as they are.
+__device__ __forceinline__ int64_t tokens_of(const GatedScanArgs& a) { return a.b > 0 ? seq_start(a, a.b) : 0; }
 // The sequence that holds token t: the last one that starts at or before t (empty sequences at
 // the same place come before it).
 __device__ __forceinline__ int64_t seq_of(const GatedScanArgs& a, int64_t t) {
@@ -207,7 +209,7 @@ __device__ __forceinline__ Tile tile_of(const GatedScanArgs& a, uint32_t c) {
         t.seq = 0;
         t.link = 1;
         t.t0 = (int64_t)c * TILE;
-        left = (a.cu ? seq_start(a, a.b) : a.T) - t.t0;
+        left = tokens_of(a) - t.t0;
         t.before = c;
         t.after = (uint32_t)a.ntiles - 1 - c;
     }
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(256) void chain_reset_kernel(const GatedScanArgs a,
         ((uint4*)a.words)[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
     if (a.per_seq) return;
-    const int64_t total = a.cu ? seq_start(a, a.b) : a.T;
+    const int64_t total = tokens_of(a);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (a.T + 63) / 64 * 64; i += step) {   // whole waves
         Place p = {0, false, false};
         if (i < total) {

@@ -222,6 +222,21 @@ def test_offsets_that_break_the_rules_stay_in_bounds():
         assert (wide[:100] == 7.0).all() and (wide[100 + t:] == 7.0).all()
 
 
+@pytest.mark.parametrize("t", [10, 300])
+def test_tokens_without_a_sequence(t):
+    """A packed batch of no sequences, with an end that breaks the rules: nothing is written but dbias, a sum of
+    nothing."""
+    x = torch.randn(t, 70, device=DEV)
+    cu = torch.tensor([5], dtype=torch.int32, device=DEV)
+    bias, none = torch.zeros(70, device=DEV), torch.zeros(0, 70, device=DEV)
+    y, h, st = m3block.m3_gated_scan(x, x, bias, none, cu, y=torch.full_like(x, 7.0), save_states=True)
+    g = m3block.m3_gated_scan_backward(x, x, x, st, bias, none, none, cu,
+                                       grads={k: torch.full_like(x, 7.0) for k in ("gate", "x")})
+    torch.cuda.synchronize()
+    assert h.shape == g["h_in"].shape == (0, 70)
+    assert all((v == 7.0).all() for v in (y, g["gate"], g["x"])) and (g["bias"] == 0).all()
+
+
 def test_rows_four_gigabytes_apart():
     """Row offsets past 32 bits: 2100 tokens in a buffer of 2^20 elements per row (4.4 GB)."""
     t, d, pitch = 2100, 64, 1 << 20
@@ -329,6 +344,32 @@ def test_on_a_side_stream():
     s.synchronize()
     ref = scan(c["gate"], c["x"], c["bias"], c["h_in"], [600])
     assert_close(y[0], ref["y"], ref["tol"]["y"], "y")
+
+
+def test_two_calls_at_once():
+    """Chained calls on two streams, each with what it allocates, give what they give alone."""
+    calls = []
+    for seed, lens in ((1, [5000, 0, 1, 3000]), (2, [9000])):
+        c = draw(sum(lens), 200, len(lens), torch.bfloat16, seed)
+        a = {k: dev(v) for k, v in c.items()}
+        calls.append((a, torch.tensor(offsets(lens), dtype=torch.int32, device=DEV)))
+
+    def one(a, cu):
+        y, h, st = m3block.m3_gated_scan(a["gate"], a["x"], a["bias"], a["h_in"], cu, save_states=True)
+        g = m3block.m3_gated_scan_backward(a["gate"], a["x"], a["dy"], st, a["bias"], a["h_in"], a["dh_out"], cu)
+        return [y, h, st] + [g[k] for k in sorted(g)]
+
+    alone = [one(*c) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(one(*c))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(alone[i % 2], g))
 
 
 def test_captured_and_replayed():

@@ -120,6 +120,22 @@ def test_the_same_tensor_twice():
         m3block.m3_grad_clip([t, t], 1.0)
 
 
+def test_more_elements_than_32_bits_count():
+    """2^31 + 70001 bf16 elements of one tensor, all 0 but at its ends and around 2^31: norm sqrt(4 + 9 + 16 + 25 + 36),
+    scaled to 1 (the sum is exact, the factor rounded to fp32, products to bf16: half a step and one unit)."""
+    n = 2 ** 31 + 70001
+    at = torch.tensor([0, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 65536, n - 1], device=DEV)
+    v = torch.tensor([2.0, 3.0, 4.0, 5.0, 6.0], device=DEV)
+    g = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    g[at] = v.bfloat16()
+    stats = m3block.m3_grad_norm([g], 1.0)
+    assert abs(float(stats[0]) - 90 ** 0.5) <= 90 ** 0.5 * 2.0 ** -23
+    m3block.m3_grad_clip([g], 1.0)
+    want = v.double() / (90 ** 0.5 + 1e-6)
+    assert ((g[at].double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -22)).all()
+    assert int(g.count_nonzero()) == 5
+
+
 def test_equal_inputs_give_equal_bits():
     grads = [t.to(DEV) for t in draw([70001, 12, 900000], 8)]
     first = m3block.m3_grad_norm(grads)
