@@ -200,11 +200,28 @@ def _scan_dims(x, cu_seqlens):
     return cu_seqlens.shape[0] - 1, x.shape[0], x.shape[1]
 
 
+# Calls repeat their sizes, so the structures that carry them are kept (the library only reads them).
+@functools.lru_cache(maxsize=1024)
+def _scan_ref(*fields):
+    return ctypes.byref(M3ScanDims(*fields))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_ref(*fields):
+    return ctypes.byref(M3NormDims(*fields))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(rows, D, io, dev):
+    """Workspace bytes of the norm's backward pass on device `dev`."""
+    return load().m3_rmsnorm_backward_workspace_bytes(_norm_ref(rows, D, 0, 0, 0, 0, 0, 0, io, 0, 0.0))
+
+
 @functools.lru_cache(maxsize=1024)
 def _scan_sizes(b, L, D, io, packed, dev):
     """Rows of `states`, and the workspace bytes of the forward and the backward pass on device `dev`."""
     lib = load()
-    ref = ctypes.byref(M3ScanDims(b, L, D, 0, 0, 0, 0, 0, io, 0))
+    ref = _scan_ref(b, L, D, 0, 0, 0, 0, 0, io, 0)
     return (lib.m3_gated_scan_chunks(ref, packed), lib.m3_gated_scan_workspace_bytes(ref, packed),
             lib.m3_gated_scan_backward_workspace_bytes(ref, packed))
 
@@ -218,15 +235,16 @@ def m3_gated_scan(gate, x, bias=None, h_in=None, cu_seqlens=None, y=None, h_out=
     b, L, D = _scan_dims(x, cu_seqlens)
     io, shape, dev, f32 = x.dtype, x.shape, x.get_device(), torch.float32
     packed = cu_seqlens is not None
-    dims = M3ScanDims(b, L, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
-                      _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
+    code = _io_code(x, "x")
+    ref = _scan_ref(b, L, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
+                    _pitch(y, "y", shape, io, dev), 0, 0, code, 0)
     bias_p, h_in_p = _dense(bias, "bias", (D,), f32, dev), _dense(h_in, "h_in", (b, D), f32, dev)
     h_out_p = _dense(h_out, "h_out", (b, D), f32, dev)
     at = _here(x, stream)
     if at < 0:
         with _scope(x, stream):
             return m3_gated_scan(gate, x, bias, h_in, cu_seqlens, y, h_out, states, save_states, workspace)
-    rows, need, _ = _scan_sizes(b, L, D, dims.io, packed, at)
+    rows, need, _ = _scan_sizes(b, L, D, code, packed, at)
     if y is None:
         y = x.new_empty(shape)
     if h_out is None:
@@ -238,7 +256,7 @@ def m3_gated_scan(gate, x, bias=None, h_in=None, cu_seqlens=None, y=None, h_out=
         else:
             _dense(states, "states", (rows, D), f32, dev)
     workspace, ws_bytes = _workspace(workspace, need, x)
-    _check(lib.m3_gated_scan(ctypes.byref(dims), _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p,
+    _check(lib.m3_gated_scan(ref, _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p,
                              y.data_ptr(), h_out_p, _ptr(states), _ptr(workspace), ws_bytes, _raw_stream(at)))
     return (y, h_out) if states is None else (y, h_out, states)
 
@@ -253,8 +271,8 @@ def m3_gated_scan_step(gate, x, h, bias=None, y=None, h_out=None, stream=None):
     b, D = shape
     dense = x.is_contiguous()
     xp = 0 if dense else _pitch(x, "x", shape, io, dev)
-    dims = M3ScanDims(b, 1, D, _pitch(gate, "gate", shape, io, dev), xp,
-                      0 if y is None else _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
+    ref = _scan_ref(b, 1, D, _pitch(gate, "gate", shape, io, dev), xp,
+                    0 if y is None else _pitch(y, "y", shape, io, dev), 0, 0, _io_code(x, "x"), 0)
     bias_p = None if bias is None else _dense(bias, "bias", (D,), f32, dev)
     h_p = h_out_p = _dense(h, "h", shape, f32, dev)
     if h_out is not None:
@@ -264,7 +282,7 @@ def m3_gated_scan_step(gate, x, h, bias=None, y=None, h_out=None, stream=None):
             return m3_gated_scan_step(gate, x, h, bias, y, h_out)
     if y is None:
         y = _new(x) if dense else x.new_empty(shape)
-    status = lib.m3_gated_scan_step(ctypes.byref(dims), gate.data_ptr(), x.data_ptr(), bias_p, h_p, y.data_ptr(),
+    status = lib.m3_gated_scan_step(ref, gate.data_ptr(), x.data_ptr(), bias_p, h_p, y.data_ptr(),
                                     h_out_p, _raw_stream(dev))
     if status:
         _check(status)
@@ -281,9 +299,10 @@ def m3_gated_scan_backward(gate, x, dy, states, bias=None, h_in=None, dh_out=Non
     io, shape, dev, f32 = x.dtype, x.shape, x.get_device(), torch.float32
     packed = cu_seqlens is not None
     g = dict(grads) if grads else {}
-    dims = M3ScanDims(b, L, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
-                      _pitch(dy, "dy", shape, io, dev), _pitch(g.get("gate"), "grad gate", shape, io, dev),
-                      _pitch(g.get("x"), "grad x", shape, io, dev), _io_code(x, "x"), 0)
+    code = _io_code(x, "x")
+    ref = _scan_ref(b, L, D, _pitch(gate, "gate", shape, io, dev), _pitch(x, "x", shape, io, dev),
+                    _pitch(dy, "dy", shape, io, dev), _pitch(g.get("gate"), "grad gate", shape, io, dev),
+                    _pitch(g.get("x"), "grad x", shape, io, dev), code, 0)
     bias_p, h_in_p = _dense(bias, "bias", (D,), f32, dev), _dense(h_in, "h_in", (b, D), f32, dev)
     dh_out_p = _dense(dh_out, "dh_out", (b, D), f32, dev)
     _dense(g.get("bias"), "grad bias", (D,), f32, dev)
@@ -292,7 +311,7 @@ def m3_gated_scan_backward(gate, x, dy, states, bias=None, h_in=None, dh_out=Non
     if at < 0:
         with _scope(x, stream):
             return m3_gated_scan_backward(gate, x, dy, states, bias, h_in, dh_out, cu_seqlens, grads, workspace)
-    rows, _, need = _scan_sizes(b, L, D, dims.io, packed, at)
+    rows, _, need = _scan_sizes(b, L, D, code, packed, at)
     states_p = _dense(states, "states", (rows, D), f32, dev)
     if states_p is None:
         raise ValueError("states are required: m3_gated_scan(..., save_states=True) returns them")
@@ -305,7 +324,7 @@ def m3_gated_scan_backward(gate, x, dy, states, bias=None, h_in=None, dh_out=Non
         g["h_in"] = x.new_empty((b, D), dtype=f32)
     workspace, ws_bytes = _workspace(workspace, need, x)
     _check(lib.m3_gated_scan_backward(
-        ctypes.byref(dims), _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, states_p, dy.data_ptr(),
+        ref, _ptr(cu_seqlens), gate.data_ptr(), x.data_ptr(), bias_p, h_in_p, states_p, dy.data_ptr(),
         dh_out_p, g["gate"].data_ptr(), g["x"].data_ptr(), _ptr(g.get("bias")), _ptr(g.get("h_in")), _ptr(workspace),
         ws_bytes, _raw_stream(at)))
     return g
@@ -327,7 +346,7 @@ def m3_rmsnorm(x, residual=None, weight=None, eps=1e-5, want_y=True, quant=False
     pp = 0 if residual is None else _pitch(residual, "residual", shape, io, dev)
     rp = 0 if r_out is None else _pitch(r_out, "r_out", shape, io, dev)
     yp = 0 if y is None else _pitch(y, "y", shape, io, dev)
-    dims = M3NormDims(x.numel() // D if D else 0, D, xp, pp, rp, yp, 0, group, _io_code(x, "x"), 0, eps)
+    ref = _norm_ref(x.numel() // D if D else 0, D, xp, pp, rp, yp, 0, group, _io_code(x, "x"), 0, eps)
     weight_p = None if weight is None else _dense(weight, "weight", (D,), f32, dev)
     if stream is not None or dev < 0 or dev != _current_device():
         with _scope(x, stream):
@@ -346,7 +365,7 @@ def m3_rmsnorm(x, residual=None, weight=None, eps=1e-5, want_y=True, quant=False
             scale = x.new_empty(sshape, dtype=f32)
         else:
             _dense(scale, "scale", sshape, f32, dev)
-    status = lib.m3_rmsnorm(ctypes.byref(dims), x.data_ptr(), _ptr(residual), weight_p, _ptr(r_out), _ptr(y), _ptr(q),
+    status = lib.m3_rmsnorm(ref, x.data_ptr(), _ptr(residual), weight_p, _ptr(r_out), _ptr(y), _ptr(q),
                             _ptr(scale), _raw_stream(dev))
     if status:
         _check(status)
@@ -363,9 +382,9 @@ def m3_rmsnorm_backward(r, dy, weight=None, dr_out=None, eps=1e-5, dx=None, dwei
     if not shape:
         raise ValueError("r must have at least one dimension")
     D = shape[-1]
-    dims = M3NormDims(r.numel() // D if D else 0, D, 0, _pitch(dr_out, "dr_out", shape, io, dev),
-                      _pitch(r, "r", shape, io, dev), _pitch(dy, "dy", shape, io, dev),
-                      _pitch(dx, "dx", shape, io, dev), 0, _io_code(r, "r"), 0, eps)
+    ref = _norm_ref(r.numel() // D if D else 0, D, 0, _pitch(dr_out, "dr_out", shape, io, dev),
+                    _pitch(r, "r", shape, io, dev), _pitch(dy, "dy", shape, io, dev),
+                    _pitch(dx, "dx", shape, io, dev), 0, _io_code(r, "r"), 0, eps)
     weight_p = _dense(weight, "weight", (D,), f32, dev)
     _dense(dweight, "dweight", (D,), f32, dev)
     at = _here(r, stream)
@@ -376,8 +395,7 @@ def m3_rmsnorm_backward(r, dy, weight=None, dr_out=None, eps=1e-5, dx=None, dwei
         dx = r.new_empty(shape)
     if dweight is None and weight is not None:
         dweight = r.new_empty((D,), dtype=f32)
-    ref = ctypes.byref(dims)
-    need = lib.m3_rmsnorm_backward_workspace_bytes(ref) if dweight is not None else 0
+    need = _norm_workspace(r.numel() // D if D else 0, D, _io_code(r, "r"), at) if dweight is not None else 0
     workspace, ws_bytes = _workspace(workspace, need, r)
     _check(lib.m3_rmsnorm_backward(ref, r.data_ptr(), weight_p, dy.data_ptr(), _ptr(dr_out), dx.data_ptr(), _ptr(dweight),
                                    _ptr(workspace), ws_bytes, _raw_stream(at)))
