@@ -278,7 +278,7 @@ __device__ __forceinline__ uint64_t get_word(const uint64_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-constexpr int kMaxPolls = 1 << 22;    // some seconds: a wait that long means a workspace in use twice
+constexpr int kMaxReads = 1 << 22;    // some seconds: a wait that long means a workspace in use twice
 
 // The state that enters a tile whose neighbour in the chain is `first`, the one after that
 // first + step, and so on for `links` tiles.  It starts from the nearest final word and applies
@@ -289,7 +289,7 @@ constexpr int kMaxPolls = 1 << 22;    // some seconds: a wait that long means a 
 // leave many tiles of one chain running at once it is far (b1 L65536 D256 bf16: up to 4 words 147 us,
 // backward 282; up to 16: 75, 131; up to 56: 57, 92).  Ends: workgroups take tiles from a counter in chain order, so
 // every tile waited for here is held by a workgroup that runs (or is done) and itself waits for
-// earlier ones only; the first tile of a chain waits for none.  A wait that outlasts kMaxPolls gives NaN.
+// earlier ones only; the first tile of a chain waits for none.  A wait of kMaxReads words gives NaN.
 template <uint32_t N>
 struct FarWords {
     uint64_t w[N][2][64];
@@ -303,10 +303,10 @@ __device__ __forceinline__ void chain_wait(const uint64_t* words, int64_t stride
     };
     const uint32_t most = links < kFar ? links : kFar;
 #pragma unroll 1
-    for (int poll = 0; poll < kMaxPolls; ++poll) {
+    for (int reads = 0; reads < kMaxReads; ++reads) {
         bool found[2] = {false, false}, maps[2] = {true, true};   // a final word; only maps so far
 #pragma unroll 1
-        for (uint32_t n = 0; n < most; ++n) {
+        for (uint32_t n = 0; n < most; ++n, ++reads) {
             const char* row = (const char*)(words + (first + (int64_t)n * step) * stride);
             uint64_t w[2];
 #pragma unroll
