@@ -943,7 +943,9 @@ __global__ __launch_bounds__(kWaves * 64, kWavesPerSimd) void gated_scan_backwar
 }
 
 // ------------------------------------------------------------------------------- one token
-// One lane per run of W channels: W = 4 (16 bytes of state per access) where rows allow it, else 1.
+// One lane per run of W channels: W = 4 (16 bytes of state per access) where rows allow it, else 1.  Bound: memory, the
+// state's 8 bytes per channel first of all: b4096 D4096 bf16 235 MB in 49 us, 4.8 TB/s, b16384 5.3 TB/s; b8 3.0 us,
+// a launch.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs a, int64_t per_row) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -972,7 +974,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs a, 
 }
 
 // out[d] = sum over rows of part[row, d]: 16 columns per workgroup, every 64th row per thread, the
-// 64 partial sums added in order, so the sum's order is fixed.
+// 64 partial sums added in order, so the sum's order is fixed.  256 rows of 4096: 4.8 us, a launch and one latency.
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float* part, int64_t n, int64_t D, float* out) {
     __shared__ float s[64][17];
     const int cx = threadIdx.x & 15, g = threadIdx.x >> 4;
