@@ -271,11 +271,18 @@ __global__ __launch_bounds__(max_threads<TPR>(), (kFwdOcc<T, C>)) void rmsnorm_k
                 const float m = __uint_as_float(a.group == 0 ? all : group_umax(top[c], a.group >> 3));
                 const float scale = m == 0.f ? 1.f : m / 448.f;
                 float qv[8];
-                if (scale > 1e-37f) {
+                // q is the fp32 quotient, rounded.  The product with 1 / scale alone lands on the other side of a border
+                // between two 8-bit values for 10% of the quotients next to one; with its remainder added it is the
+                // quotient.  Where 1 / scale or the remainder could leave fp32's range (a NaN scale is there, too): divided.
+                // 16384 x 4096 bf16, x in and q out: the product alone 54 us, this 57, dividing always 75.
+                if (scale > 1e-30f && scale < 1e30f) {
                     const float inv = 1.f / scale;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) qv[k] = r[c][k] * inv;
-                } else {   // 1 / scale could overflow (a NaN scale comes here, too)
+                    for (int k = 0; k < 8; ++k) {
+                        const float q0 = r[c][k] * inv;
+                        qv[k] = fmaf(fmaf(-q0, scale, r[c][k]), inv, q0);
+                    }
+                } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) qv[k] = r[c][k] / scale;
                 }

@@ -206,3 +206,34 @@ def test_rows_past_four_gigabytes():
     dx_ref, dw_ref, t_dx, t_dw = rmsnorm_backward(res, dy, w, dr, EPS)
     assert_close(dx, dx_ref, t_dx, "dx")
     assert_close(dw, dw_ref, t_dw, "dweight")
+
+
+def e4m3_values():
+    """The values of codes 0 to 126: 0 to 448."""
+    return torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+
+
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("d", [64, 512, 1024, 2048, 16384])
+def test_quotients_next_to_borders(d, group):
+    """Rows of ones and eps 0 make n the weight itself (a power of two of squares sums to its number, whose mean is 1),
+    so scale and q follow from fp32 divisions alone: q = round(n / scale) for quotients on the borders between two
+    8-bit values and up to two units beside them, all equal."""
+    g = torch.Generator().manual_seed(d + group)
+    w = group or d
+    top = (1 + torch.rand(d // w, 1, generator=g)) * 2.0 ** torch.randint(-20, 20, (d // w, 1), generator=g)
+    scale = top / 448
+    values = e4m3_values()
+    borders = (values[1:] + values[:-1])[torch.randint(0, 126, (d // w, w), generator=g)] / 2
+    n = (borders * scale).view(torch.int32) + torch.randint(-2, 3, (d // w, w), generator=g, dtype=torch.int32)
+    n = n.view(torch.float32)
+    n[:, w // 2] = top[:, 0]
+    want = (n / scale).to(torch.float8_e4m3fn)
+    n *= 1 - 2 * torch.randint(0, 2, n.shape, generator=g)
+    y, _, q, s = m3block.m3_rmsnorm(torch.ones(5, d, device=DEV), weight=n.reshape(-1).to(DEV), quant=True, group=group,
+                                    eps=0.0)
+    torch.cuda.synchronize()
+    for row in range(5):
+        assert torch.equal(y[row].cpu(), n.reshape(-1))
+        assert torch.equal(s[row].cpu(), scale[:, 0])
+        assert torch.equal(q[row].cpu().float().abs(), want.float().reshape(-1))
