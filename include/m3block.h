@@ -164,6 +164,8 @@ m3_status m3_rmsnorm(const m3_norm_dims* dims, const void* x, const void* residu
  *   s = 1 / sqrt(mean(r^2) + eps),  u = weight dy
  *   dx = s u - r s^3 mean(u r) + dr_out,  dweight = sum over rows of dy r s
  *
+ * in fp32, without the cube: for rows whose squares and products u r sum up within fp32's range.
+ *
  *   r          [rows, D] io, m3_rmsnorm's r_out (or x where there was no residual), pitch r_pitch
  *   dy         [rows, D] io, pitch y_pitch
  *   dr_out     [rows, D] io, pitch res_pitch: the gradient of r_out from the residual stream

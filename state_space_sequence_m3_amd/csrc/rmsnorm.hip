@@ -373,7 +373,8 @@ __global__ __launch_bounds__(max_threads<TPR>(), (kBwdOcc<T, C>)) void rmsnorm_b
             }
         }
         const float rs = 1.f / sqrtf(ss * inv_d + a.eps);
-        const float along = rs * rs * rs * (su * inv_d);
+        // r rs and not rs^3: the cube leaves fp32's range for rows of root mean squares beyond 1e13 or below 1e-13
+        const float along = su * inv_d * rs;
         char* op = (char*)a.dx + row * a.dx_p;
         if (live) {
 #pragma unroll
@@ -381,10 +382,10 @@ __global__ __launch_bounds__(max_threads<TPR>(), (kBwdOcc<T, C>)) void rmsnorm_b
                 float o[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float r = rr[c].get(k), dy = ry[c].get(k);
-                    o[k] = rs * (dy * wt[c][k]) - r * along;
+                    const float n = rr[c].get(k) * rs, dy = ry[c].get(k);
+                    o[k] = rs * (dy * wt[c][k] - n * along);
                     if (a.dr_out) o[k] += rd[c].get(k);
-                    dw[c][k] = fmaf(dy, r * rs, dw[c][k]);
+                    dw[c][k] = fmaf(dy, n, dw[c][k]);
                 }
                 store8<STREAM>(op, ch[c], D, o, T{});
             }

@@ -237,3 +237,20 @@ def test_quotients_next_to_borders(d, group):
         assert torch.equal(y[row].cpu(), n.reshape(-1))
         assert torch.equal(s[row].cpu(), scale[:, 0])
         assert torch.equal(q[row].cpu().float().abs(), want.float().reshape(-1))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size,eps", [(1e12, EPS), (1e14, EPS), (1e16, EPS), (1e17, EPS), (1e-12, 0.0), (1e-14, 0.0), (1e-16, 0.0),
+                                      (1e-3, 0.0)])
+@pytest.mark.parametrize("d", [96, 700, 1100])
+def test_backward_of_large_and_small_rows(io, size, eps, d):
+    """Rows whose squares fp32 still holds (1100 of 1e34, and 1e-32) have gradients as good as any others."""
+    n = 7
+    _, r, w, dy, _ = draw(n, d, IO[io], d)
+    r = (r.float() / 3 * size).to(IO[io])
+    dr = (torch.randn(n, d, generator=torch.Generator().manual_seed(3)) / size).to(IO[io])
+    dx_ref, dw_ref, t_dx, t_dw = rmsnorm_backward(r, dy, w, dr, eps)
+    dx, dw = m3block.m3_rmsnorm_backward(r.to(DEV), dy.to(DEV), w.to(DEV), dr.to(DEV), eps)
+    torch.cuda.synchronize()
+    assert_close(dx, dx_ref, t_dx, "dx")
+    assert_close(dw, dw_ref, t_dw, "dweight")
