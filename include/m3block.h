@@ -138,7 +138,8 @@ typedef struct {
  *   r = x + residual,  n = r / sqrt(mean(r^2) + eps) * weight      (per row, in fp32)
  *   r_out = round(r), y = round(n)
  *   scale = max |n| / 448 over the row or over each group of `group` consecutive elements (the
- *           last one may be shorter), 1 where that maximum is 0;  q = round(n / scale) in e4m3
+ *           last one may be shorter), rounded up below 1e-37, 1 where that maximum is 0;
+ *   q = round(n / scale) in e4m3
  *
  * (the RMS norm is the one m3_bcnorm_rope applies to B and C: papernotes.org summary of Mamba-3,
  * key design 4; here over whole rows of the residual stream.)

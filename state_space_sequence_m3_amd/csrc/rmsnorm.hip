@@ -269,7 +269,9 @@ __global__ __launch_bounds__(max_threads<TPR>(), (kFwdOcc<T, C>)) void rmsnorm_k
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const float m = __uint_as_float(a.group == 0 ? all : group_umax(top[c], a.group >> 3));
-                const float scale = m == 0.f ? 1.f : m / 448.f;
+                float scale = m == 0.f ? 1.f : m / 448.f;
+                // a scale with few digits left (or none) is rounded up, since n over one rounded down exceeds 448
+                if (scale < 1e-37f && scale * 448.f < m) scale = __uint_as_float(__float_as_uint(scale) + 1);
                 float qv[8];
                 // q is the fp32 quotient, rounded.  The product with 1 / scale alone lands on the other side of a border
                 // between two 8-bit values for 10% of the quotients next to one; with its remainder added it is the

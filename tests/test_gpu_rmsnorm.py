@@ -254,3 +254,23 @@ def test_backward_of_large_and_small_rows(io, size, eps, d):
     torch.cuda.synchronize()
     assert_close(dx, dx_ref, t_dx, "dx")
     assert_close(dw, dw_ref, t_dw, "dweight")
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_scales_that_vanish(group):
+    """Rows of ones and eps 0: n is the weight, here of 1 to 2^23 of fp32's smallest steps.  The scale is the least
+    number of steps whose 448-fold holds the maximum (a division of whole numbers), and q = round(n / scale)."""
+    for most in (1, 2, 200, 447, 448, 449, 668, 671, 900, 6000, 6500, 65000, 3000001, 2 ** 23):
+        g = torch.Generator().manual_seed(most)
+        steps = torch.randint(0, most + 1, (64,), generator=g)
+        steps[5], steps[40] = most, most
+        n = steps.to(torch.int32).view(torch.float32)
+        assert int(n.view(torch.int32).max()) == most
+        y, _, q, s = m3block.m3_rmsnorm(torch.ones(3, 64, device=DEV), weight=n.to(DEV), quant=True, group=group, eps=0.0)
+        torch.cuda.synchronize()
+        unit = -(-most // 448)
+        want = (steps.double() / unit).float().to(torch.float8_e4m3fn)
+        for row in range(3):
+            assert torch.equal(y[row].cpu().view(torch.int32), steps.to(torch.int32)), most
+            assert (s[row].cpu().view(torch.int32) == unit).all(), most
+            assert torch.equal(q[row].cpu().float(), want.float()), most
