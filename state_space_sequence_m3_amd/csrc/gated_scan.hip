@@ -33,29 +33,19 @@ constexpr uint32_t kSideBySide = 4;
 constexpr int kWavesPerSimd = 4;   // two workgroups on a compute unit: 128 registers.  3 waves: 126 us for 94, 5: 98
 constexpr uint32_t kFar = 56;      // chain words looked at, at most: 1 KB of shared memory each
 
-// z = sigmoid(u) and keep = 1 - z, both to a few units in their last place: with e = e^-|u| the larger of
-// the two is 1 / (1 + e) and the smaller one e / (1 + e), never a difference from 1.  The logit comes
-// in parts, gate + bias, since with bf16 gates u log2(e) is one fused multiply-add (the gate's own
-// rounding is larger than that one's); fp32 carries the rounding of u log2(e) along.
+// z = sigmoid(u) and keep = 1 - z, u = gate + bias, both to a few units in their last place: with e = e^-|u| the larger
+// of the two is 1 / (1 + e) and the smaller one e / (1 + e), never a difference from 1.  The rounding of u log2(e) is
+// carried along.  For bf16 gates, too: their logits are added in fp32 like any other, since the sum is close to exact
+// where gate and bias cancel (one fused product with log2(e) on top of a rounded bias log2(e) was up to 100 units off
+// there, 140 elsewhere).
 constexpr float kLog2eLo = 1.925963033500e-8f;   // log2(e) - kLog2e
-template <typename T>
-__device__ __forceinline__ float gate_exp(float g, float bias, bool& up) {
-    if constexpr (sizeof(T) == 2) {
-        const float t = fmaf(g, kLog2e, bias * kLog2e);
-        up = t >= 0.f;
-        return fast_exp2(-fabsf(t));
-    } else {
-        const float u = g + bias, m = -fabsf(u), t = m * kLog2e;
-        const float e = fast_exp2(t), lo = fmaf(m, kLog2e, -t) + m * kLog2eLo;
-        up = u >= 0.f;
-        return t < -126.f ? e : fmaf(e, lo * 0.6931471805599453f, e);
-    }
-}
-template <typename T>
 __device__ __forceinline__ void gate_of(float g, float bias, float& z, float& keep) {
-    bool up;
-    const float e = gate_exp<T>(g, bias, up);
+    const float u = g + bias, m = -fabsf(u), t = m * kLog2e;
+    const float rest = fmaf(m, kLog2e, -t) + m * kLog2eLo;
+    float e = fast_exp2(t);
+    e = t < -126.f ? e : fmaf(e, rest * 0.6931471805599453f, e);
     const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+    const bool up = u >= 0.f;
     z = up ? big : small;
     keep = up ? small : big;
 }
@@ -481,7 +471,7 @@ __device__ __forceinline__ void forward_tile(const GatedScanArgs& a, FwdShared<T
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     float z;
-                    gate_of<T>(g[i].get(v), bias[v], z, keep[i][v]);
+                    gate_of(g[i].get(v), bias[v], z, keep[i][v]);
                     add[i][v] = z * x[i].get(v);
                 }
         }
@@ -688,7 +678,7 @@ __device__ __forceinline__ void backward_tile(const GatedScanArgs& a, BwdShared<
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int v = 0; v < 2; ++v) gate_of<T>(g[i].get(v), bias[v], z[i][v], keep[i][v]);
+                for (int v = 0; v < 2; ++v) gate_of(g[i].get(v), bias[v], z[i][v], keep[i][v]);
         }
     }
     if (nv < N) {                              // tokens that are not there: keep = 1, nothing added
@@ -965,7 +955,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs a, 
 #pragma unroll
     for (int v = 0; v < W; ++v) {
         float z, keep;
-        gate_of<T>(to_f32(g.v[v]), a.bias ? a.bias[d + v] : 0.f, z, keep);
+        gate_of(to_f32(g.v[v]), a.bias ? a.bias[d + v] : 0.f, z, keep);
         o.v[v] = fmaf(keep, h.v[v], z * to_f32(x.v[v]));
         y.v[v] = from_f32<T>(o.v[v]);
     }

@@ -417,3 +417,39 @@ def test_one_workspace_for_calls_in_a_row():
         assert_close(y[0], ref["y"], ref["tol"]["y"], "y")
         assert_close(g["gate"][0], ref["dgate"], ref["tol"]["dgate"], "dgate")
         assert_close(g["bias"], ref["dbias"], ref["tol"]["dbias"], "dbias")
+
+
+def gates(gate, bias):
+    """z and keep as the single-token form computes them, and the 64-bit logits, whose fp32 sums have to be exact."""
+    d = gate.shape[1]
+    u = gate.double() + bias.double()
+    assert torch.equal(u, (gate.float() + bias).double())
+    gate, bias = gate.to(DEV), bias.to(DEV)
+    ones, zeros = torch.ones(gate.shape, device=DEV), torch.zeros(gate.shape, device=DEV)
+    z, keep = torch.empty_like(ones), torch.empty_like(ones)
+    m3block.m3_gated_scan_step(gate, ones.to(gate.dtype), zeros, bias, h_out=z)        # 0 keep + 1 z
+    m3block.m3_gated_scan_step(gate, zeros.to(gate.dtype), ones, bias, h_out=keep)     # 1 keep + 0 z
+    torch.cuda.synchronize()
+    return z.cpu().double(), keep.cpu().double(), u
+
+
+def draw_gates(io, cancel):
+    """Logits of up to 70 on a grid of 2^-7 that bf16 and fp32 both hold: gate a whole number from -256 to 256, bias
+    with a fraction, where they cancel of the other sign."""
+    g = torch.Generator().manual_seed(9)
+    bias = torch.randint(-2 ** 14, 2 ** 14, (512,), generator=g) / 128.0
+    gate = torch.randint(-70, 71, (2000, 512), generator=g).float()
+    gate = (gate - bias.round() if cancel else gate).clamp(-256, 256)
+    if not cancel:
+        bias = bias / 64
+    return gate.to(IO[io]), bias
+
+
+@pytest.mark.parametrize("cancel", [False, True])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_both_gates_keep_their_digits(io, cancel):
+    """In units of 2^-24: e^-|u| is off by 2 for the exponential (one step of its last place) and 1 for the product that
+    carries the rest, its sum with 1 by 1, the reciprocal by 2 (one step), the product by 1: both gates by at most 7."""
+    z, keep, u = gates(*draw_gates(io, cancel))
+    for got, ref in ((z, torch.sigmoid(u)), (keep, torch.sigmoid(-u))):
+        assert ((got - ref).abs() <= 7.1 * 2.0 ** -24 * ref).all()
