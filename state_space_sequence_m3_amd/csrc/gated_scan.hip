@@ -38,13 +38,19 @@ constexpr uint32_t kFar = 56;      // chain words looked at, at most: 1 KB of sh
 // carried along.  For bf16 gates, too: their logits are added in fp32 like any other, since the sum is close to exact
 // where gate and bias cancel (one fused product with log2(e) on top of a rounded bias log2(e) was up to 100 units off
 // there, 140 elsewhere).
+// The reciprocal takes a Newton step: the hardware's errs to one side, by up to a step, which adds up over
+// a recurrence of many tokens (fp32 gradient of a bias over 11000 tokens 7e-7 off, with the step 3e-7, as the formula in
+// torch's fp32; bf16 forward 84.7 -> 86.5 us at b8 L2048 D4096, fp32 and backward the same).
 constexpr float kLog2eLo = 1.925963033500e-8f;   // log2(e) - kLog2e
 __device__ __forceinline__ void gate_of(float g, float bias, float& z, float& keep) {
     const float u = g + bias, m = -fabsf(u), t = m * kLog2e;
     const float rest = fmaf(m, kLog2e, -t) + m * kLog2eLo;
     float e = fast_exp2(t);
     e = t < -126.f ? e : fmaf(e, rest * 0.6931471805599453f, e);
-    const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+    const float d = 1.f + e;
+    float big = __builtin_amdgcn_rcpf(d);
+    big = fmaf(big, fmaf(-d, big, 1.f), big);
+    const float small = e * big;
     const bool up = u >= 0.f;
     z = up ? big : small;
     keep = up ? small : big;

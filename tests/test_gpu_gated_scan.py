@@ -453,3 +453,21 @@ def test_both_gates_keep_their_digits(io, cancel):
     z, keep, u = gates(*draw_gates(io, cancel))
     for got, ref in ((z, torch.sigmoid(u)), (keep, torch.sigmoid(-u))):
         assert ((got - ref).abs() <= 7.1 * 2.0 ** -24 * ref).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_the_larger_gate_is_rounded_once(io):
+    """big = 1 / (1 + e) in units of 2^-24, its own half step being 1/2: the sum's rounding moves it by big^2, e's error of
+    3 by 3 e big^2; a reciprocal that is not the nearest would add to that, always to one side, token after token.  1e-3 covers products of errors,
+    which are 2^-22 of one."""
+    g = torch.Generator().manual_seed(10)
+    if io == "f32":
+        gate, bias = (torch.rand(4000, 512, generator=g) - 0.5) * 40, torch.zeros(512)
+    else:                    # many values of one type's few: gates of whole numbers, biases with fractions of 2^-16
+        gate = torch.randint(-10, 11, (4000, 512), generator=g).to(torch.bfloat16)
+        bias = torch.randint(-2 ** 20, 2 ** 20, (512,), generator=g) / 2.0 ** 16
+    z, keep, u = gates(gate, bias)
+    e = torch.exp(-u.abs())
+    big = 1 / (1 + e)
+    got = torch.where(u >= 0, z, keep)
+    assert ((got - big).abs() <= (0.5 + big * big * (1 + 3 * e) + 1e-3) * 2.0 ** -24).all()
