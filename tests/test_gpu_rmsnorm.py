@@ -274,3 +274,62 @@ def test_scales_that_vanish(group):
             assert torch.equal(y[row].cpu().view(torch.int32), steps.to(torch.int32)), most
             assert (s[row].cpu().view(torch.int32) == unit).all(), most
             assert torch.equal(q[row].cpu().float(), want.float()), most
+
+
+def same_bits(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n,d", [(50003, 96), (15001, 300), (9001, 1000), (3001, 1111), (1601, 4096), (700, 9001)])
+def test_several_rows_to_a_workgroup(io, n, d):
+    """Two rows or more to every workgroup and a ragged last round, in each layout of rows: every row against the
+    formulas, the same in place, and the weight's gradient over all rows."""
+    x, res, w, dy, dr = draw(n, d, IO[io], n + d)
+    r_ref, n_ref = rmsnorm(x, res, w, EPS)
+    xs, rs, wd = x.to(DEV), res.to(DEV), w.to(DEV)
+    y, r, q, s = m3block.m3_rmsnorm(xs, rs, wd, EPS, quant=True)
+    y2, r2, q2, s2 = m3block.m3_rmsnorm(xs, rs, wd, EPS, quant=True, group=32, r_out=rs, y=xs)
+    torch.cuda.synchronize()
+    assert_close(r, r_ref, r_ref.abs() * U32, "r")
+    assert_close(y, n_ref, n_ref.abs() * NORM_UNITS * U32, "y")
+    check_q(q, s, n_ref, 0)
+    check_q(q2, s2, n_ref, 32)
+    assert same_bits(y, y2) and same_bits(r, r2)
+    dx_ref, dw_ref, t_dx, t_dw = rmsnorm_backward(res, dy, w, dr, EPS)
+    rs, dys, drs = res.to(DEV), dy.to(DEV), dr.to(DEV)
+    dx, dw = m3block.m3_rmsnorm_backward(rs, dys, wd, drs, EPS)
+    e = dys.clone()
+    over_dy, dw2 = m3block.m3_rmsnorm_backward(rs, e, wd, drs, EPS, dx=e)
+    over_dr, dw3 = m3block.m3_rmsnorm_backward(rs, dys, wd, drs, EPS, dx=drs)
+    torch.cuda.synchronize()
+    assert_close(dx, dx_ref, t_dx, "dx")
+    assert_close(dw, dw_ref, t_dw, "dweight")
+    assert same_bits(dx, over_dy) and same_bits(dx, over_dr) and same_bits(dw, dw2) and same_bits(dw, dw3)
+
+
+@pytest.mark.parametrize("io,n,d", [("f32", 4099, 4096), ("bf16", 8209, 4096), ("f32", 15203, 1111), ("bf16", 33203, 1013),
+                                    ("f32", 250501, 67)])
+def test_outputs_past_the_caches(io, n, d):
+    """More than 256 MB moved, where outputs are stored non-temporally: 300 rows, first and last ones among them,
+    against the formulas, and the weight's gradient over all rows."""
+    es = 4 if io == "f32" else 2
+    assert 4 * es * n * d > 1 << 28
+    g = torch.Generator(device=DEV).manual_seed(n)
+    x, res, dy, dr = (torch.randn(n, d, generator=g, device=DEV).mul_(k).to(IO[io]) for k in (1, 3, 1, 1))
+    w = 1 + 0.2 * torch.randn(d, generator=g, device=DEV)
+    pick = torch.cat([torch.arange(100, device=DEV), torch.randint(0, n, (100,), generator=g, device=DEV),
+                      torch.arange(n - 100, n, device=DEV)])
+    r_ref, n_ref = rmsnorm(x[pick].cpu(), res[pick].cpu(), w.cpu(), EPS)
+    y, r, q, s = m3block.m3_rmsnorm(x, res, w, EPS, quant=True)
+    torch.cuda.synchronize()
+    assert_close(r[pick], r_ref, r_ref.abs() * U32, "r")
+    assert_close(y[pick], n_ref, n_ref.abs() * NORM_UNITS * U32, "y")
+    check_q(q.view(torch.uint8)[pick].view(torch.float8_e4m3fn), s[pick], n_ref, 0)
+    del x, y, r, q
+    dx, dw = m3block.m3_rmsnorm_backward(res, dy, w, dr, EPS)
+    dx_ref, _, t_dx, _ = rmsnorm_backward(res[pick].cpu(), dy[pick].cpu(), w.cpu(), dr[pick].cpu(), EPS)
+    _, dw_ref, _, t_dw = rmsnorm_backward(res, dy, w, None, EPS)
+    torch.cuda.synchronize()
+    assert_close(dx[pick], dx_ref, t_dx, "dx")
+    assert_close(dw, dw_ref.cpu(), t_dw.cpu(), "dweight")
