@@ -2,6 +2,8 @@
 types, empty and unaligned ones, in place and not, coefficients of 1 and below, infinities and NaN."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 import torch
 
@@ -143,3 +145,27 @@ def test_equal_inputs_give_equal_bits():
         again = m3block.m3_grad_norm(grads)
         torch.cuda.synchronize()
         assert torch.equal(first, again)
+
+
+def test_more_partial_sums_than_are_added_twice():
+    """300 tensors of 15 units of 16384 elements make 4500 partial sums in four launches: over 4096 a launch of their
+    own adds them, and all scaling passes take its sum."""
+    grads = [torch.randn(230000 + 13 * i, device=DEV) for i in range(300)]
+    table = (m3block.M3GradTensor * len(grads))()
+    for t, g in zip(table, grads):
+        t.src, t.dst, t.numel, t.io = g.data_ptr(), g.data_ptr(), g.numel(), m3block.M3_F32
+    parts = m3block.load().m3_grad_workspace_bytes(ctypes.cast(table, ctypes.c_void_p), len(grads)) // 8 - 1
+    assert parts > 4096
+    norm = sum(t.double().square().sum() for t in grads).sqrt()
+    coef = 2.0 / (norm + 1e-6)
+    out, stats = m3block.m3_grad_clip(grads, 2.0, out=[torch.full_like(t, 3.0) for t in grads])
+    alone = m3block.m3_grad_norm(grads, 2.0)
+    want = [t.double() * coef for t in grads]
+    m3block.m3_grad_clip(grads, 2.0)                        # in place
+    torch.cuda.synchronize()
+    assert torch.equal(stats, alone)
+    assert abs(float(stats[0]) - float(norm)) <= 2 * U32 * float(norm)
+    assert abs(float(stats[1]) - float(coef)) <= 2 * U32 * float(coef)
+    for w, o, g in zip(want, out, grads):
+        assert ((o.double() - w).abs() <= 4 * U32 * w.abs()).all()
+        assert torch.equal(o, g)
