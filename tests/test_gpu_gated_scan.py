@@ -471,3 +471,31 @@ def test_the_larger_gate_is_rounded_once(io):
     big = 1 / (1 + e)
     got = torch.where(u >= 0, z, keep)
     assert ((got - big).abs() <= (0.5 + big * big * (1 + 3 * e) + 1e-3) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("b,L,d", [(700, 7, 70), (300, 3, 257), (520, 64, 66), (513, 1, 5)])
+def test_many_short_dense_sequences(io, b, L, d):
+    """Dense sequences of up to 64 tokens, too many for a workgroup each, share tiles.  The reference runs them side by
+    side as channels of one sequence; the bias's gradient adds up over them (its additions: block_ref)."""
+    assert b * -(-d // 128) > 512
+    c = draw(b * L, d, b, IO[io], seed=b + L + d)
+    got = run(c, [L] * b, packed=False)
+    side = lambda v: v.view(b, L, d).transpose(0, 1).reshape(L, b * d)
+    flat = lambda v: None if v is None else v.reshape(1, b * d)
+    ref = scan(side(c["gate"]), side(c["x"]), c["bias"].repeat(b), flat(c["h_in"]), [L], side(c["dy"]), flat(c["dh_out"]))
+    for k in ("y", "dgate", "dx"):
+        assert_close(side(got[k]), ref[k], ref["tol"][k], k)
+    for k in ("h_out", "dh_in"):
+        assert_close(flat(got[k]), ref[k], ref["tol"][k], k)
+    over = lambda v: v.view(b, d).sum(0)
+    assert_close(got["dbias"], over(ref["dbias"]), over(ref["tol"]["dbias"]) + over(ref["dgate"].abs().sum(0)) *
+                 (48 + b * L / 4096) * 2.0 ** -24, "dbias")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("b,L,d", [(5, 700, 66), (7, 1100, 130)])
+def test_chains_side_by_side(io, b, L, d):
+    """Tiles of four sequences are taken in turns, then those of the rest: of one, and of three."""
+    c = draw(b * L, d, b, IO[io], seed=b + L + d)
+    check(c, [L] * b, run(c, [L] * b, packed=False))
