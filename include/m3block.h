@@ -150,9 +150,11 @@ typedef struct {
  *   y            [rows, D] io; may be x or residual itself (same pitch)   NULL: not wanted
  *   q, scale     [rows, D] e4m3 (OCP, 8 bits, largest value 448), [rows, ceil(D / group)] f32;
  *                both or neither
- * At least one of y and q is required.  A NaN in a row makes the row's y, q and scales NaN (with
- * groups: the scale of each group that holds one); the sum of squares is in fp32, so rows with
- * magnitudes over about 1e19 overflow it and give y = 0, as the formula in fp32 does.
+ * At least one of y and q is required.  A NaN in a row makes the row's y, q and scales NaN; an infinity
+ * makes its own element NaN, and the scale over it, and the row's other elements 0.  The sum of
+ * squares is in fp32, as the formula in fp32 has it: rows with magnitudes over about 1e19 overflow it
+ * and give y = 0; with eps 0, rows below about 1e-19 lose digits of it, and a row whose squares are
+ * all 0 is divided by 0.
  */
 m3_status m3_rmsnorm(const m3_norm_dims* dims, const void* x, const void* residual,
                      const float* weight, void* r_out, void* y, void* q, float* scale,

@@ -99,14 +99,17 @@ m3_status check_scan_dims(const m3_scan_dims* d) {
     return M3_OK;
 }
 
-// When a workgroup works its sequence off tile by tile instead of chaining tiles that run at the same time.
+// When a workgroup works its sequence off tile by tile instead of chaining tiles that run at the same time (times of
+// the builds that both forms were compared in).
 // Bf16, D 4096, forward (backward): two tiles of few sequences 14.5 -> 12.9 us (4 x 256 tokens; four tiles lose: 23.1 ->
 // 25.1 us); many sequences, which fill the GPU anyway, 88 -> 79 us (161 -> 140) at 64 x 256 tokens, 91 -> 83 us at
 // 16 x 1024, but 162 -> 172 us at 8 x 2048 x 8192 channels, 16 tiles.  Packed batches never gain: their tiles wait
 // for the search of their sequences, which then adds up.  The forward pass of fp32 holds twice the bytes and spills in
 // that form: it gains where there is one tile to a sequence and few of those (4 x 128 tokens 13.6 -> 12.5 us), and
 // loses beyond (147 -> 160 us at 64 x 256 tokens); its backward pass gains as bf16 does (260 -> 241 us at 128 x 128).
-constexpr int64_t kMaxLoneTiles = 512;   // two workgroups on each of 256 compute units
+// Two workgroups on each of 256 compute units, not asked of the device: which batches are cut sequence by sequence decides
+// the rows of `states`, which belong to sizes alone.
+constexpr int64_t kMaxLoneTiles = 512;
 constexpr int64_t kMaxSerialTiles = 2, kMaxFullSerialTiles = 8;
 constexpr int64_t kMaxScanBlocks = (int64_t)1 << 23;
 // Workgroups that keep the GPU full: no last round of two to a compute unit that is mostly empty.

@@ -111,7 +111,8 @@ constexpr int64_t kGradChunk = 16384;
 constexpr int kGradBlocks = 2048;
 // As many elements in one table are left to a single workgroup, a unit of kGradSmallChunk to a wave: one launch
 // and no partial sums, so that the call costs the host a third less (8 x 5125 elements 22 -> 17 us); on the GPU
-// alone it takes 4.6 us instead of 5.9 for 8 x 1000 elements, 9.3 instead of 8.4 for 8 x 5125.
+// alone it takes 4.6 us instead of 5.9 for 8 x 1000 elements, 9.3 instead of 8.4 for 8 x 5125 (which a replayed graph
+// pays without the host's gain).
 constexpr int64_t kGradSmall = 65536;
 constexpr int64_t kGradSmallChunk = 2048;   // 1024: 10.6 us for 8 x 5125 elements, 4096: 9.7
 

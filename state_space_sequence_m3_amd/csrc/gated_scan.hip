@@ -4,17 +4,19 @@
 // A run of steps is the affine map h -> A h + B with A the product of (1 - z_t) and B the run's
 // end from a zero state, and maps compose: (A2, B2) after (A1, B1) is (A2 A1, A2 B1 + B2).  A
 // sequence's first token forgets what came before: its map is h -> B (A = 0), with B taking the
-// carried h_in in.
+// carried h_in in.  Tiles of a sequence run at the same time and are joined by a single-pass scan with decoupled
+// look-back (Merrill and Garland, 2016).
 //
 // Bound: memory.  A forward pass reads gate and x and writes y, a backward pass reads gate, x and dy and writes
-// dgate and dx; the arithmetic (an exponential, a reciprocal and some six more per element) hides behind that.  So
+// dgate and dx; the arithmetic (an exponential, a reciprocal and some fifteen more per element) hides behind that.  So
 // every element travels once: a workgroup takes a tile of 128 tokens (backward 64) x 128 channels, each of its 8
 // waves 16 (8) consecutive tokens, two channels to a lane, all in registers from the load to the store; the waves'
 // maps are composed through shared memory, the tiles' through a chain of words in the workspace, and the tokens are
-// then run once more from registers.  b8 L2048 D4096 bf16: 403 MB in 84 us, 4.8 TB/s, backward 671 MB in 153 us, 4.4
-// TB/s (a copy of that size: 5.3 to 5.5 TB/s); fp32 149 us, 5.4 TB/s, and 252 us, 5.3 TB/s.  What is left: 4 us for
-// the launch that resets the chain, 5 us for taking tiles in order, and waits for the chain: one sequence of
-// 16384 tokens takes 91 us, and 76, a copy's time, without the three.
+// then run once more from registers.  b8 L2048 D4096 bf16, calls with all their launches: 403 MB in 86 us, 4.7 TB/s,
+// backward 671 MB in 155 us, 4.3 TB/s (a copy of that size: 5.3 to 5.5 TB/s); fp32 141 us, 5.7 TB/s, and 251 us, 5.3
+// TB/s.  What is left: 5 us for the launch that resets the chain, 5 us for taking tiles in order, and waits for the
+// chain: one sequence of 16384 tokens takes 93 us, where a copy of its bytes takes 76.
+// Here and at the constants below, times of alternatives are from the build that each was compared in.
 // Shapes, b8 L2048 D4096 fp32 unless said: 4 waves to a tile of 64 tokens 160 us, 16 waves to one of 256 170 us;
 // fp32 in tiles of 64 tokens 111 us instead of 100 (13 packed sequences); a backward tile of 128 tokens spills
 // (bf16 420 us); workgroups that stay and fetch the next tile ahead 110 us (bf16), backward 433 us; gates computed
@@ -39,8 +41,9 @@ constexpr uint32_t kFar = 56;      // chain words looked at, at most: 1 KB of sh
 // where gate and bias cancel (one fused product with log2(e) on top of a rounded bias log2(e) was up to 100 units off
 // there, 140 elsewhere).
 // The reciprocal takes a Newton step: the hardware's errs to one side, by up to a step, which adds up over
-// a recurrence of many tokens (fp32 gradient of a bias over 11000 tokens 7e-7 off, with the step 3e-7, as the formula in
-// torch's fp32; bf16 forward 84.7 -> 86.5 us at b8 L2048 D4096, fp32 and backward the same).
+// a recurrence of many tokens (fp32 gradient of a bias over 12000 tokens 7e-7 off, with the step 3e-7, as the formula in
+// torch's fp32; bf16 forward 84.7 -> 86 us at b8 L2048 D4096, 76 -> 81 at 16 x 1024 tokens with the carried
+// rounding's share, fp32 and backward the same).
 constexpr float kLog2eLo = 1.925963033500e-8f;   // log2(e) - kLog2e
 __device__ __forceinline__ void gate_of(float g, float bias, float& z, float& keep) {
     const float u = g + bias, m = -fabsf(u), t = m * kLog2e;

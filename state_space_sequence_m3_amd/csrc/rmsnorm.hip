@@ -7,8 +7,8 @@
 // end with the row: it reads and writes whole, and its first `skip` elements, which belong to the chunk
 // before it as well, are left out of sums and scales (both chunks write the same values there).
 //
-// Bound: memory, each tensor travelling once.  16384 x 4096 bf16, x and residual in, r, y and q out: 604 MB in 118 us,
-// 5.1 TB/s; backward with dr_out 537 MB in 104 us, 5.2 TB/s (a copy: 5.3 to 5.5).  Sums and statistics are in fp32.
+// Bound: memory, each tensor travelling once.  16384 x 4096 bf16, x and residual in, r, y and q out: 604 MB in 119 us,
+// 5.1 TB/s; backward with dr_out 537 MB in 103 us, 5.2 TB/s (a copy: 5.3 to 5.5).  Sums and statistics are in fp32.
 #include "block_launch.h"
 #include "m3_device.h"
 
