@@ -499,3 +499,19 @@ def test_chains_side_by_side(io, b, L, d):
     """Tiles of four sequences are taken in turns, then those of the rest: of one, and of three."""
     c = draw(b * L, d, b, IO[io], seed=b + L + d)
     check(c, [L] * b, run(c, [L] * b, packed=False))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gates_at_the_ends(io):
+    """Infinite and far logits give gates of 0 and 1 exactly, also with a bias that ends there; NaN stays NaN."""
+    inf, nan = float("inf"), float("nan")
+    gate = torch.tensor([[inf, -inf, 200.0, -200.0, nan, 0.0, inf, 1.0, -1.0, 3e38]]).to(IO[io]).repeat(3, 1).to(DEV)
+    bias = torch.tensor([0.0, 0.0, 0.0, 0.0, 0.0, nan, -inf, inf, -inf, 3e38], device=DEV)
+    want = torch.tensor([1.0, 0.0, 1.0, 0.0, nan, nan, nan, 1.0, 0.0, 1.0])
+    ones, z = torch.ones(3, 10, device=DEV), torch.empty(3, 10, device=DEV)
+    m3block.m3_gated_scan_step(gate, ones.to(IO[io]), 0 * ones, bias, h_out=z)
+    _, last = m3block.m3_gated_scan(gate[None], ones.to(IO[io])[None], bias, torch.zeros(1, 10, device=DEV))
+    torch.cuda.synchronize()
+    for row in z.cpu():
+        assert torch.equal(row.isnan(), want.isnan()) and torch.equal(row.nan_to_num(), want.nan_to_num())
+    assert torch.equal(last[0].cpu().nan_to_num(), want.nan_to_num()) and torch.equal(last[0].cpu().isnan(), want.isnan())
