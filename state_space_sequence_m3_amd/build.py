@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build", "m3scan")
 LIB = os.path.join(PKG, "libm3scan.so")
 SOURCES = ["api.hip", "bcnorm_rope.hip", "prefill.hip", "decode.hip", "backward.hip",
-           "block_api.hip", "gated_scan.hip", "rmsnorm.hip", "grad_clip.hip"]
+           "block_api.hip", "gated_scan.hip", "rmsnorm.hip", "grad_clip.hip",
+           "attn_api.hip", "attention.hip", "attention_backward.hip", "cache_append.hip", "attention_step.hip"]
 ARCH = "gfx950"
 
 

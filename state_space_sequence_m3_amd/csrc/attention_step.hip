@@ -1,0 +1,374 @@
+// attention_step.hip -- one token's attention per sequence over a paged cache (m3_attention_step).
+//
+// Memory-bound: each key and value is read once for the query heads that share it.  A sequence's keys are cut into pieces
+// of a length that follows from all lengths together, so that pieces fill the GPU whatever the lengths are; a
+// piece is a workgroup's, whose 4 waves take its tiles in turn, each with a running maximum and sum of its own, and
+// the pieces of a sequence are joined by a second launch.
+//
+// Up to 16 query heads of a key head are the columns of 16x16 products.  Scores are computed transposed (keys down), with
+// the keys in an order that makes a lane's probabilities those of 8 (fp32: 4) consecutive keys: the right operand of the
+// product with the values, whose left operand is the values' rows as they are loaded, 16 lanes to a row, with (bf16) an
+// 8 x 8 transpose inside each lane.  Nothing goes through LDS but the join of the waves.
+#include "m3_mma.h"
+#include "m3_pages.h"
+
+namespace m3 {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Pieces of a batch: all are `keys` long but the last of a sequence.
+struct Cut {
+    int64_t keys;
+    __device__ __forceinline__ int64_t pieces(int64_t len) const { return pieces_of(len, keys); }
+};
+__device__ __forceinline__ int64_t length_of(const StepArgs& a, int64_t s) {
+    const int64_t n = a.lens[s], most = a.pages.table_w * (int64_t)a.pages.size;
+    return n < 0 ? 0 : n > most ? most : n;
+}
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+    return v;
+}
+__device__ __forceinline__ Cut cut_batch(const StepArgs& a) {
+    int64_t all = 0;
+    for (int64_t s = threadIdx.x & 63; s < a.b; s += 64) all += length_of(a, s);
+    all = wave_sum(all);
+    return {piece_keys(all, a.items)};
+}
+// The sequence that piece `item` belongs to (-1: there are fewer pieces), the pieces before it, and its length.
+__device__ __forceinline__ int64_t find_piece(const StepArgs& a, const Cut& cut, int64_t item, int64_t& before, int64_t& len) {
+    const int lane = threadIdx.x & 63;
+    before = 0;
+    for (int64_t s0 = 0; s0 < a.b; s0 += 64) {
+        const int64_t l = s0 + lane < a.b ? length_of(a, s0 + lane) : 0;
+        const int64_t mine = s0 + lane < a.b ? cut.pieces(l) : 0;
+        int64_t upto = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t u = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += u;
+        }
+        const uint64_t past = __ballot(before + upto > item);
+        if (past) {
+            const int i = __ffsll((unsigned long long)past) - 1;
+            before += __shfl(upto - mine, i, 64);
+            len = __shfl(l, i, 64);
+            return s0 + i;
+        }
+        before += __shfl(upto, 63, 64);
+    }
+    return -1;
+}
+// The pieces before sequence s.
+__device__ __forceinline__ int64_t pieces_before(const StepArgs& a, const Cut& cut, int64_t s) {
+    int64_t n = 0;
+    for (int64_t i = threadIdx.x & 63; i < s; i += 64) n += cut.pieces(length_of(a, i));
+    return wave_sum(n);
+}
+
+// DC: elements of a head that are worked on, 64 or 128.  TILED: a page holds whole tiles.
+template <typename T, int DC, bool TILED>
+struct Piece {
+    static constexpr bool BF = sizeof(T) == 2;
+    static constexpr int ES = sizeof(T);
+    static constexpr int TILE = BF ? 32 : 16;        // keys
+    static constexpr int BLK = TILE / 16;            // score blocks of 16 keys
+    static constexpr int KS = DC * ES / 64;          // steps of 4 chunks along a row
+    static constexpr int VE = DC / 16;               // a lane's elements of a value row
+    static constexpr int VK = TILE / 4;              // a lane's value rows
+    static constexpr int VW = VE * ES / 4;           // words of them
+
+    uint4 k[BLK][KS];
+    uint32_t v[VK][VW];
+    uint32_t there;                                  // bits of the lane's score keys that exist
+
+    // the key of score row r in block n
+    static __device__ __forceinline__ int key_of(int r, int n) { return BF ? 8 * (r >> 2) + 4 * n + (r & 3) : r; }
+
+    __device__ __forceinline__ void load(const StepArgs& a, const int32_t* table, int kv_head, int64_t k0, int64_t kend,
+                                         int lane) {
+        const int r16 = lane & 15, g = lane >> 4, row_bytes = a.dim * ES;
+        const Pages& p = a.pages;
+        const int left = (int)(kend - k0 < TILE ? kend - k0 : TILE);
+        const int vcol = r16 * VE * ES;
+        if constexpr (TILED) {
+            int place;
+            const int id = __builtin_amdgcn_readfirstlane(page_of(p, table, (int32_t)k0, place));
+            place = __builtin_amdgcn_readfirstlane(place);
+            const int rows = id >= 0 ? left : 0;
+            const int64_t at = id >= 0 ? id : 0;
+            const rsrc_t kr = make_rsrc(p.k + at * p.k_page + kv_head * p.k_head + place * (int64_t)p.k_token,
+                                        rows > 0 ? (uint32_t)(rows - 1) * p.k_token + row_bytes : 0u);
+            const rsrc_t vr = make_rsrc(p.v + at * p.v_page + kv_head * p.v_head + place * (int64_t)p.v_token,
+                                        rows > 0 ? (uint32_t)(rows - 1) * p.v_token + row_bytes : 0u);
+#pragma unroll
+            for (int n = 0; n < BLK; ++n)
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const int col = (4 * s + g) * 16;
+                    k[n][s] = buffer_load16(kr, col < row_bytes ? (uint32_t)key_of(r16, n) * p.k_token + col : 0x80000000u);
+                }
+#pragma unroll
+            for (int i = 0; i < VK; ++i) {
+                const uint32_t off = vcol < row_bytes ? (uint32_t)(VK * g + i) * p.v_token + vcol : 0x80000000u;
+                load_value(i, vr, off);
+            }
+            there = 0;
+#pragma unroll
+            for (int i = 0; i < 4 * BLK; ++i) there |= (VK * g + i < rows ? 1u : 0u) << i;
+        } else {
+            // lane i looks key i up for all
+            int place = 0, id = -1;
+            if ((lane & 31) < left) id = page_of(p, table, (int32_t)(k0 + (lane & 31)), place);
+#pragma unroll
+            for (int n = 0; n < BLK; ++n) {
+                const int key = key_of(r16, n), kid = __shfl(id, key, 64), kplace = __shfl(place, key, 64);
+                const char* row = p.k + kid * p.k_page + kv_head * p.k_head + kplace * (int64_t)p.k_token;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const int col = (4 * s + g) * 16;
+                    k[n][s] = make_uint4(0, 0, 0, 0);
+                    if (kid >= 0 && col < row_bytes) k[n][s] = *(const uint4*)(row + col);
+                }
+            }
+            there = 0;
+#pragma unroll
+            for (int i = 0; i < VK; ++i) {
+                const int key = VK * g + i, kid = __shfl(id, key, 64), kplace = __shfl(place, key, 64);
+                const char* row = p.v + kid * p.v_page + kv_head * p.v_head + kplace * (int64_t)p.v_token + vcol;
+                const bool ok = kid >= 0 && vcol < row_bytes;
+#pragma unroll
+                for (int w = 0; w < VW; w += (VW < 4 ? VW : 4)) {
+                    if constexpr (VW == 2) {
+                        const uint2 u = ok ? *(const uint2*)row : make_uint2(0, 0);
+                        v[i][0] = u.x, v[i][1] = u.y;
+                    } else {
+                        const uint4 u = ok && vcol + 4 * w < row_bytes ? *(const uint4*)(row + 4 * w) : make_uint4(0, 0, 0, 0);
+                        v[i][w] = u.x, v[i][w + 1] = u.y, v[i][w + 2] = u.z, v[i][w + 3] = u.w;
+                    }
+                }
+                there |= (kid >= 0 ? 1u : 0u) << i;
+            }
+        }
+    }
+    __device__ __forceinline__ void load_value(int i, rsrc_t r, uint32_t off) {
+        if constexpr (VW == 2) {
+            const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+            v[i][0] = u[0], v[i][1] = u[1];
+        } else {
+#pragma unroll
+            for (int w = 0; w < VW; w += 4) {
+                const uint4 u = buffer_load16(r, off + 4 * w);
+                v[i][w] = u.x, v[i][w + 1] = u.y, v[i][w + 2] = u.z, v[i][w + 3] = u.w;
+            }
+        }
+    }
+
+    // scores of the tile; key VK g + i in register i
+    __device__ __forceinline__ void scores(const uint4 (&q)[KS], float (&s)[4 * BLK]) const {
+#pragma unroll
+        for (int n = 0; n < BLK; ++n) {
+            floatx4 d = {};
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                if constexpr (BF) {
+                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[n][j]),
+                                                                __builtin_bit_cast(bf16x8, q[j]), d, 0, 0, 0);
+                } else {
+                    d = Mma<float>::mma(__builtin_bit_cast(floatx4, k[n][j]), __builtin_bit_cast(floatx4, q[j]), d);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[4 * n + i] = (there >> (4 * n + i)) & 1 ? d[i] : -INFINITY;
+        }
+    }
+    // acc[j][m]: element (4 g + m) VE + j of the lane's query head
+    __device__ __forceinline__ void values(const float (&p)[4 * BLK], floatx4 (&acc)[VE]) const {
+        if constexpr (BF) {
+            uint4 b;
+            b.x = pack_bf16x2(p[0], p[1]);
+            b.y = pack_bf16x2(p[2], p[3]);
+            b.z = pack_bf16x2(p[4], p[5]);
+            b.w = pack_bf16x2(p[6], p[7]);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+                const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+                uint4 t;
+                t.x = __builtin_amdgcn_perm(v[1][j >> 1], v[0][j >> 1], sel);
+                t.y = __builtin_amdgcn_perm(v[3][j >> 1], v[2][j >> 1], sel);
+                t.z = __builtin_amdgcn_perm(v[5][j >> 1], v[4][j >> 1], sel);
+                t.w = __builtin_amdgcn_perm(v[7][j >> 1], v[6][j >> 1], sel);
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, t), __builtin_bit_cast(bf16x8, b),
+                                                                 acc[j], 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[m][j]), p[m], acc[j], 0, 0, 0);
+        }
+    }
+};
+
+// Partial results: a piece's heads one after another, {maximum (log2 units), sum, D unscaled elements} each.
+__device__ __forceinline__ int64_t part_row(const StepArgs& a, int64_t item, int head) {
+    return (item * a.heads + head) * (2 + a.dim);
+}
+
+template <typename T, int DC, bool TILED>
+__global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
+    using P = Piece<T, DC, TILED>;
+    constexpr int VE = P::VE;
+    __shared__ float tops[4][16], sums[4][16];
+    __shared__ float outs[4][16][DC + 4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int hb = blockIdx.x % a.head_blocks, kv_head = blockIdx.x / a.head_blocks % a.kv_heads;
+    const int64_t item = blockIdx.x / a.head_blocks / a.kv_heads;
+    const int group = a.heads / a.kv_heads;
+    const Cut cut = cut_batch(a);
+    int64_t before, len = 0;
+    const int64_t s = find_piece(a, cut, item, before, len);
+    if (s < 0) return;
+    const int64_t k0 = (item - before) * cut.keys, kend = k0 + cut.keys < len ? k0 + cut.keys : len;
+    const int32_t* table = a.pages.table + s * a.pages.table_w;
+    const int in_group = hb * 16 + col, head = kv_head * group + in_group;
+
+    uint4 q[P::KS];
+#pragma unroll
+    for (int j = 0; j < P::KS; ++j) {
+        const int at = (4 * j + g) * 16;
+        q[j] = make_uint4(0, 0, 0, 0);
+        if (in_group < group && at < a.dim * P::ES) q[j] = *(const uint4*)(a.q.p + s * a.q.batch + head * a.q.head + at);
+    }
+    const float c = a.scale * kLog2e;
+    floatx4 acc[VE] = {};
+    float top = -1e37f, sum = 0.f;
+
+    P now, next;
+    int64_t k = k0 + wave * P::TILE;
+    if (k < kend) now.load(a, table, kv_head, k, kend, lane);
+    for (; k < kend; k += 4 * P::TILE) {
+        const bool more = k + 4 * P::TILE < kend;
+        if (more) next.load(a, table, kv_head, k + 4 * P::TILE, kend, lane);
+        float p[4 * P::BLK];
+        now.scores(q, p);
+        float m = p[0];
+#pragma unroll
+        for (int i = 1; i < 4 * P::BLK; ++i) m = fmaxf(m, p[i]);
+        m = fmaxf(m, __shfl_xor(m, 16, 64));
+        m = fmaxf(m, __shfl_xor(m, 32, 64)) * c;
+        if (__ballot(m > top)) {
+            const float to = fmaxf(top, m), f = fast_exp2(top - to);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) acc[j] *= f;
+            sum *= f;
+            top = to;
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * P::BLK; ++i) {
+            p[i] = fast_exp2(fmaf(p[i], c, -top));
+            sum += p[i];
+        }
+        now.values(p, acc);
+        now = next;
+    }
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+
+    // the four waves' results
+    if (g == 0) {
+        tops[wave][col] = top;
+        sums[wave][col] = sum;
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) outs[wave][col][(4 * g + m) * VE + j] = acc[j][m];
+    __syncthreads();
+    const bool whole = cut.pieces(len) == 1;
+    const int heads_here = group - hb * 16 < 16 ? group - hb * 16 : 16;
+    for (int e = threadIdx.x; e < heads_here * a.dim; e += 256) {
+        const int h = e / a.dim, d = e % a.dim, at = kv_head * group + hb * 16 + h;
+        const float t = fmaxf(fmaxf(tops[0][h], tops[1][h]), fmaxf(tops[2][h], tops[3][h]));
+        float n = 0.f, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = fast_exp2(tops[w][h] - t);
+            n = fmaf(f, sums[w][h], n);
+            o = fmaf(f, outs[w][h][d], o);
+        }
+        if (whole) {
+            // nothing to attend to: zeros
+            *(T*)(a.o.p + s * a.o.batch + at * a.o.head + d * P::ES) = from_f32<T>(t > -1e37f || n != 0.f ? o / n : 0.f);
+            if (a.lse && d == 0) a.lse[s * a.heads + at] = (t + __builtin_amdgcn_logf(n)) * kLn2;
+        } else {
+            float* part = a.part + part_row(a, item, at);
+            part[2 + d] = o;
+            if (d == 0) part[0] = t, part[1] = n;
+        }
+    }
+}
+
+// Joins the pieces of one head of one sequence.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_step_join(const StepArgs a) {
+    __shared__ float outs[2][128];
+    __shared__ float tops[4], sums[4];
+    const int64_t s = blockIdx.x / a.heads;
+    const int head = (int)(blockIdx.x % a.heads);
+    const Cut cut = cut_batch(a);
+    const int64_t n = cut.pieces(length_of(a, s));
+    if (n <= 1) return;
+    const int64_t first = pieces_before(a, cut, s);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    float top = -1e37f;
+    for (int64_t i = tid; i < n; i += 256) top = fmaxf(top, a.part[part_row(a, first + i, head)]);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    // two halves of the workgroup take every other piece, an element to a thread
+    const int d = tid & 127, from = tid >> 7;
+    float o = 0.f, sum = 0.f;
+    for (int64_t i = from; i < n; i += 2) {
+        const float* part = a.part + part_row(a, first + i, head);
+        const float f = fast_exp2(part[0] - top);
+        sum = fmaf(f, part[1], sum);
+        if (d < a.dim) o = fmaf(f, part[2 + d], o);
+    }
+    outs[from][d] = o;
+    if (d == 0) sums[from] = sum;
+    __syncthreads();
+    if (tid < a.dim) {
+        sum = sums[0] + sums[1];
+        *(T*)(a.o.p + s * a.o.batch + head * a.o.head + tid * (int)sizeof(T)) =
+            from_f32<T>(top > -1e37f || sum != 0.f ? (outs[0][tid] + outs[1][tid]) / sum : 0.f);
+        if (a.lse && tid == 0) a.lse[s * a.heads + head] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    }
+}
+
+template <typename T, int DC>
+hipError_t launch_dim(const StepArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)((a.items + a.b) * a.kv_heads * a.head_blocks));
+    if (a.pages.size % Piece<T, DC, true>::TILE == 0) attn_step<T, DC, true><<<grid, 256, 0, s>>>(a);
+    else attn_step<T, DC, false><<<grid, 256, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.joined) return e;
+    attn_step_join<T><<<dim3((uint32_t)(a.b * a.heads)), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention_step(const StepArgs& a, bool bf16_io, hipStream_t s) {
+    if (bf16_io) return a.dim <= 64 ? launch_dim<bf16, 64>(a, s) : launch_dim<bf16, 128>(a, s);
+    return a.dim <= 64 ? launch_dim<float, 64>(a, s) : launch_dim<float, 128>(a, s);
+}
+
+}  // namespace m3

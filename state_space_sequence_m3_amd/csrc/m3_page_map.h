@@ -1,0 +1,37 @@
+// m3_page_map.h -- index maps of the attention operators, shared by the kernels and host-side tests (no HIP types).
+#pragma once
+
+#include <stdint.h>
+
+#include "m3_mapping.h"
+
+namespace m3 {
+
+// Position `pos` of a sequence whose row of the page table is `row`: its page, and its place there; -1 where the
+// position is negative, past the table, or on a number that is no page.  shift: log2 of the page's
+// size, or -1.
+M3_HD int32_t page_place(const int32_t* row, int64_t width, int32_t pages, int32_t size, int shift, int32_t pos,
+                         int32_t* place) {
+    *place = 0;
+    if (pos < 0) return -1;
+    const int32_t n = shift >= 0 ? pos >> shift : pos / size;
+    *place = pos - n * size;
+    if (n >= width) return -1;
+    const int32_t id = row[n];
+    return id >= 0 && id < pages ? id : -1;
+}
+
+// Blocks of R rows of a packed batch: sequence s, which starts at token `start`, has the numbers from start / R + s on.
+// The next sequence's first number leaves it at least as many as it has blocks, and all are below T / R + b.
+M3_HD int64_t first_block(int64_t start, int64_t s, int64_t R) { return start / R + s; }
+
+// Pieces of at most `keys` keys that a sequence of `len` is cut into: one at least.
+M3_HD int64_t pieces_of(int64_t len, int64_t keys) { return len <= keys ? 1 : (len + keys - 1) / keys; }
+// The length of pieces that makes at most items + b of them out of b sequences of `all` keys together.
+constexpr int64_t kMinPiece = 256;
+M3_HD int64_t piece_keys(int64_t all, int64_t items) {
+    const int64_t even = (all + items - 1) / items;
+    return even < kMinPiece ? kMinPiece : (even + 127) / 128 * 128;
+}
+
+}  // namespace m3
