@@ -23,18 +23,15 @@ struct Rows {
     floatx16 o[X::DB] = {};
     float top = -1e37f, sum = 0.f;   // log2 units; this half's part of the sum
 
-    // 32 keys at tile row r0; `diagonal`: they are the rows' own tokens
-    __device__ __forceinline__ void add(const char* K, const char* V, int r0, float c, bool diagonal, int lane) {
-        const int half = lane >> 5, row = lane & 31;
-        floatx16 s = X::rows_by(K, r0, q, lane);
-        if (diagonal) {
+    // the scores against 32 keys become probabilities
+    template <int N>
+    __device__ __forceinline__ void soften(floatx16 (&s)[N], float c) {
+        float m = s[0][0];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = acc_row(i, half) > row ? -INFINITY : s[i];
-        }
-        float m = fmaxf(s[0], s[1]);
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 2; i < 16; ++i) m = fmaxf(m, s[i]);
-        m = fmaxf(m, other_half(m)) * c;
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, s[n][i]);
+        m = halves_max(m) * c;
         if (__ballot(m > top + kSlack)) {
             const float to = fmaxf(top, m), f = fast_exp2(top - to);
 #pragma unroll
@@ -43,18 +40,33 @@ struct Rows {
             top = to;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = fast_exp2(fmaf(s[i], c, -top));
-        float part = 0.f;
+        for (int n = 0; n < N; ++n) {
+            float part = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part += s[i];
-        sum += part;
+            for (int i = 0; i < 16; ++i) {
+                s[n][i] = fast_exp2(fmaf(s[n][i], c, -top));
+                part += s[n][i];
+            }
+            sum += part;
+        }
+    }
+
+    // 32 keys at tile row r0 that are the rows' own tokens (`diagonal`), or earlier ones
+    __device__ __forceinline__ void add(const char* K, const char* V, int r0, float c, bool diagonal, int lane) {
+        const int half = lane >> 5, row = lane & 31;
+        floatx16 s[1] = {X::rows_by(K, r0, q, lane)};
+        if (diagonal) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[0][i] = acc_row(i, half) > row ? -INFINITY : s[0][i];
+        }
+        soften(s, c);
         if (diagonal && any_odd(V, r0, lane)) {
             // key by key, each for the rows that see it
 #pragma unroll 1
             for (int j = 0; j < 32; ++j) {
-                float p = s[0];
+                float p = s[0][0];
 #pragma unroll
-                for (int i = 1; i < 16; ++i) p = i == 4 * (j >> 3) + (j & 3) ? s[i] : p;
+                for (int i = 1; i < 16; ++i) p = i == 4 * (j >> 3) + (j & 3) ? s[0][i] : p;
                 p = __shfl(p, row + 32 * ((j >> 2) & 1), 64);
                 if (j <= row) {
 #pragma unroll
@@ -65,7 +77,7 @@ struct Rows {
                 }
             }
         } else {
-            X::columns_by(V, r0, s, o, lane);
+            X::columns_by(V, r0, s[0], o, lane);
         }
     }
 
@@ -91,65 +103,74 @@ struct Rows {
 template <typename T, int DC>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd(const AttnArgs a) {
     using X = HeadTile<T, DC>;
-    __shared__ alignas(16) char lds[2][2 * X::BYTES];
+    __shared__ alignas(16) char k0[X::BYTES];
+    __shared__ alignas(16) char k1[X::BYTES];
+    __shared__ alignas(16) char v0[X::BYTES];
+    __shared__ alignas(16) char v1[X::BYTES];
     RowBlock w;
     if (!locate_rows<true>(a, a.heads, blockIdx.x, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kv_head = w.head / (a.heads / a.kv_heads), row_bytes = a.dim * X::ES;
-    const RowSource ks = head_rows(a.k, w, kv_head, row_bytes), vs = head_rows(a.v, w, kv_head, row_bytes);
+    const TileLoad<X> load_k(head_rows(a.k, w, kv_head, row_bytes), tid);
+    const TileLoad<X> load_v(head_rows(a.v, w, kv_head, row_bytes), tid);
     const int64_t q0 = w.r0 + 32 * wave;
     const bool active = q0 < w.len;
-
-    Rows<T, DC> rows;
-    load_rows<X>(rows.q, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
-    const float c = a.scale * kLog2e;
 
     // tiles that all rows see, and those that hold the rows' own tokens
     const int before = (int)(w.r0 / X::ROWS);
     const int64_t kend = w.len < w.r0 + kAttnRows ? w.len : w.r0 + kAttnRows;
     const int ntiles = (int)((kend + X::ROWS - 1) / X::ROWS);
-    Staged<X> kt, vt;
-    kt.load(ks, 0, w.len, tid);
-    vt.load(vs, 0, w.len, tid);
-    kt.store(lds[0], tid);
-    vt.store(lds[0] + X::BYTES, tid);
+    load_k(k0, 0, w.len, wave);
+    load_v(v0, 0, w.len, wave);
+    if (ntiles > 1) load_k(k1, X::ROWS, w.len, wave);
+
+    Rows<T, DC> rows;
+    load_rows<X>(rows.q, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
+    const float c = a.scale * kLog2e;
+
+    // Tile t's keys are in k0 (t even) or k1, its values in v0 or v1.  Scores of tile t + 1 are computed while tile
+    // t's become probabilities, keys are loaded two tiles ahead and values one.
+    floatx16 s[X::SUB], ahead[X::SUB];
     __syncthreads();
-    int t = 0;
-    for (; t < before; ++t) {
-        const char* K = lds[t & 1];
-        char* next = lds[(t + 1) & 1];
-        kt.load(ks, (int64_t)(t + 1) * X::ROWS, w.len, tid);
-        vt.load(vs, (int64_t)(t + 1) * X::ROWS, w.len, tid);
+    if (before > 0) {
 #pragma unroll
-        for (int r0 = 0; r0 < X::ROWS; r0 += 32) rows.add(K, K + X::BYTES, r0, c, false, lane);
-        kt.store(next, tid);
-        vt.store(next + X::BYTES, tid);
-        __syncthreads();
+        for (int n = 0; n < X::SUB; ++n) s[n] = X::rows_by(k0, 32 * n, rows.q, lane);
     }
-    for (; t < ntiles; ++t) {
-        const char* K = lds[t & 1];
-        char* next = lds[(t + 1) & 1];
+    auto turn = [&](int t, const char* K, char* old_k, const char* V, char* old_v) {
+        __syncthreads();
+        if (t + 2 < ntiles) load_k(old_k, (int64_t)(t + 2) * X::ROWS, w.len, wave);
+        load_v(old_v, (int64_t)(t + 1) * X::ROWS, w.len, wave);
+#pragma unroll
+        for (int n = 0; n < X::SUB; ++n) ahead[n] = X::rows_by(K, 32 * n, rows.q, lane);
+        rows.soften(s, c);
+#pragma unroll
+        for (int n = 0; n < X::SUB; ++n) X::columns_by(V, 32 * n, s[n], rows.o, lane);
+#pragma unroll
+        for (int n = 0; n < X::SUB; ++n) s[n] = ahead[n];
+    };
+    // before is even: 128 rows are an even number of tiles
+    for (int t = 0; t < before; t += 2) {
+        turn(t, k1, k0, v0, v1);
+        turn(t + 1, k0, k1, v1, v0);
+    }
+    for (int t = before; t < ntiles; ++t) {
+        const bool odd = t & 1;
+        __syncthreads();
         if (t + 1 < ntiles) {
-            kt.load(ks, (int64_t)(t + 1) * X::ROWS, w.len, tid);
-            vt.load(vs, (int64_t)(t + 1) * X::ROWS, w.len, tid);
+            if (t > before) load_k(odd ? k0 : k1, (int64_t)(t + 1) * X::ROWS, w.len, wave);
+            load_v(odd ? v0 : v1, (int64_t)(t + 1) * X::ROWS, w.len, wave);
         }
 #pragma unroll 1
         for (int r0 = 0; r0 < X::ROWS; r0 += 32) {
-            const int64_t k0 = (int64_t)t * X::ROWS + r0;
-            if (active && k0 <= q0) rows.add(K, K + X::BYTES, r0, c, k0 == q0, lane);
+            const int64_t at = (int64_t)t * X::ROWS + r0;
+            if (active && at <= q0) rows.add(odd ? k1 : k0, odd ? v1 : v0, r0, c, at == q0, lane);
         }
-        if (t + 1 < ntiles) {
-            kt.store(next, tid);
-            vt.store(next + X::BYTES, tid);
-        }
-        __syncthreads();
     }
     if (!active) return;
-    const float sum = rows.sum + other_half(rows.sum);
+    const float sum = halves_sum(rows.sum);
     store_columns<T, X::DB>(rows.o, 1.f / sum, head_rows(a.o, w, w.head, row_bytes), q0, w.len, lane);
-    if (a.lse && lane < 32 && q0 + lane < w.len) {
+    if (a.lse && lane < 32 && q0 + lane < w.len)
         a.lse[token_row(a, w, w.head) + q0 + lane] = (rows.top + __builtin_amdgcn_logf(sum)) * kLn2;
-    }
 }
 
 template <typename T>

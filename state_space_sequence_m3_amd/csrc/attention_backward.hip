@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq(const Att
         load_rows<X>(df, head_rows(a.dout, w, w.head, row_bytes), q0, w.len, lane);
 #pragma unroll
         for (int g = 0; g < X::SG; ++g) delta += X::dot(qf[g], df[g]);
-        delta += other_half(delta);
+        delta = halves_sum(delta);
     }
     load_rows<X>(qf, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
     const int64_t at = token_row(a, w, w.head) + q0 + row;

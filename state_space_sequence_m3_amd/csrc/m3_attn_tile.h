@@ -23,8 +23,15 @@ typedef short shortx8 __attribute__((ext_vector_type(8)));
 
 // row of result register i in lane half h
 __device__ __forceinline__ constexpr int acc_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
-// the other half's value for the same column
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+// over both halves of a column (v_permlane32_swap of a value with itself gives both halves')
+__device__ __forceinline__ float halves_sum(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+__device__ __forceinline__ float halves_max(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
 
 // DC: elements of a head that are worked on (the head's own number rounded up to 32); T: io type
 template <typename T, int DC>
@@ -33,6 +40,7 @@ struct HeadTile {
     static constexpr int PITCH = (DC <= 64 ? 64 : 128) * ES;   // bytes between rows
     static constexpr int CPR = PITCH / 16;                     // chunks per row
     static constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;      // rows of a tile
+    static constexpr int SUB = ROWS / 32;
     static constexpr int BYTES = ROWS * PITCH;
     static constexpr int SG = DC * ES / 32;                    // steps along a row
     static constexpr int DB = DC / 32;                         // result tiles across a row
@@ -42,7 +50,7 @@ struct HeadTile {
     // 8 consecutive rows hold a chunk in 8 places (row reads), and the rows that transposed reads take together
     // lie in different quarters of the banks.
     static __device__ __forceinline__ int swz(int row) {
-        if constexpr (ES == 4) return (((row >> 2) & 1) << 3) | ((row & 3) << 1) | ((row >> 3) & 1);
+        if constexpr (ES == 4) return (((row >> 2) & 1) << 3) | ((row & 3) << 1);
         else if constexpr (CPR == 16) return ((row & 3) << 2) | ((row >> 2) & 3);
         else return (((row >> 1) & 1) << 2) | ((row >> 2) & 1) | (((row >> 3) & 1) << 1);
     }
@@ -194,6 +202,30 @@ __device__ __forceinline__ RowSource head_rows(const HeadRows& t, const RowBlock
 __device__ __forceinline__ int64_t token_row(const AttnArgs& a, const RowBlock& w, int head) {
     return a.cu ? head * a.L + w.start : (w.seq * a.heads + head) * a.L;
 }
+
+// A tile from global memory straight into LDS, by 256 threads.  Lanes fill consecutive chunks of LDS, so each
+// asks for the chunk that swz puts there; what the descriptor does not cover arrives as zero.  Buffers that are
+// filled while others are read have to be arrays of their own: the compiler then knows that reads need not wait for
+// the fill, and waits for it at the next barrier.
+typedef __attribute__((address_space(3))) void lds_void;
+template <typename X>
+struct TileLoad {
+    static constexpr int STEP = 256 / X::CPR;   // rows that one load of all threads covers
+    RowSource src;
+    uint32_t off;
+    __device__ __forceinline__ TileLoad(const RowSource& s, int tid) : src(s) {
+        static_assert(STEP % 8 == 0, "swz has a period of 8 or 16 rows");
+        const int row = tid / X::CPR, chunk = (tid % X::CPR) ^ X::swz(row);
+        off = chunk * 16 < s.row_bytes ? (uint32_t)row * s.token + chunk * 16 : kOutside;
+    }
+    __device__ __forceinline__ void operator()(char* tile, int64_t r0, int64_t len, int wave) const {
+        const rsrc_t r = src.rows(r0, len, X::ROWS);
+#pragma unroll
+        for (int i = 0; i < X::NLD; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(tile + (i * 4 + wave) * 1024), 16,
+                                                     (int)(off + (uint32_t)(i * STEP) * src.token), 0, 0, 0);
+    }
+};
 
 // A tile on its way from global memory to LDS, through registers of 256 threads.
 template <typename X>
