@@ -33,13 +33,13 @@ __device__ __forceinline__ float halves_max(float v) {
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
-// DC: elements of a head that are worked on (the head's own number rounded up to 32); T: io type
-template <typename T, int DC>
+// DC: elements of a head that are worked on (the head's own number rounded up to 32); T: io type; R: rows of a tile
+template <typename T, int DC, int R = (sizeof(T) == 2 ? 64 : 32)>
 struct HeadTile {
     static constexpr int ES = sizeof(T);
     static constexpr int PITCH = (DC <= 64 ? 64 : 128) * ES;   // bytes between rows
     static constexpr int CPR = PITCH / 16;                     // chunks per row
-    static constexpr int ROWS = sizeof(T) == 2 ? 64 : 32;      // rows of a tile
+    static constexpr int ROWS = R;
     static constexpr int SUB = ROWS / 32;
     static constexpr int BYTES = ROWS * PITCH;
     static constexpr int SG = DC * ES / 32;                    // steps along a row
@@ -94,6 +94,16 @@ struct HeadTile {
         floatx16 s = {};
 #pragma unroll
         for (int g = 0; g < SG; ++g) s = mma(row_chunk(tile, r0 + (lane & 31), 2 * g + (lane >> 5)), b[g], s);
+        return s;
+    }
+
+    // the same with the other rows in LDS too, from row b0 of tile `b` on
+    static __device__ __forceinline__ floatx16 rows_by_rows(const char* tile, int r0, const char* b, int b0, int lane) {
+        floatx16 s = {};
+#pragma unroll
+        for (int g = 0; g < SG; ++g)
+            s = mma(row_chunk(tile, r0 + (lane & 31), 2 * g + (lane >> 5)),
+                    row_chunk(b, b0 + (lane & 31), 2 * g + (lane >> 5)), s);
         return s;
     }
 
@@ -206,7 +216,7 @@ __device__ __forceinline__ int64_t token_row(const AttnArgs& a, const RowBlock& 
 // A tile from global memory straight into LDS, by 256 threads.  Lanes fill consecutive chunks of LDS, so each
 // asks for the chunk that swz puts there; what the descriptor does not cover arrives as zero.  Buffers that are
 // filled while others are read have to be arrays of their own: the compiler then knows that reads need not wait for
-// the fill, and waits for it at the next barrier.
+// the fill.  A wave knows of its own loads only: tiles_ready lets each wait for its own and then for the others.
 typedef __attribute__((address_space(3))) void lds_void;
 template <typename X>
 struct TileLoad {
@@ -227,26 +237,11 @@ struct TileLoad {
     }
 };
 
-// A tile on its way from global memory to LDS, through registers of 256 threads.
-template <typename X>
-struct Staged {
-    uint4 v[X::NLD];
-    __device__ __forceinline__ void load(const RowSource& s, int64_t r0, int64_t len, int tid) {
-        const rsrc_t r = s.rows(r0, len, X::ROWS);
-#pragma unroll
-        for (int i = 0; i < X::NLD; ++i) {
-            const int c = i * 256 + tid, row = c / X::CPR, chunk = c % X::CPR;
-            v[i] = buffer_load16(r, chunk * 16 < s.row_bytes ? (uint32_t)row * s.token + chunk * 16 : kOutside);
-        }
-    }
-    __device__ __forceinline__ void store(char* tile, int tid) const {
-#pragma unroll
-        for (int i = 0; i < X::NLD; ++i) {
-            const int c = i * 256 + tid;
-            *(uint4*)(tile + X::at(c / X::CPR, c % X::CPR)) = v[i];
-        }
-    }
-};
+// All tiles asked for before are whole, and all reads of tiles before are done.
+__device__ __forceinline__ void tiles_ready() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): loads into LDS count there
+    __syncthreads();
+}
 
 // The chunks 2 g + h of row (lane % 32), for use as a right operand.
 template <typename X>
