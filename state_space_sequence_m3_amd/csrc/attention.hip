@@ -53,8 +53,11 @@ struct Rows {
 
     // 32 keys at tile row r0 that are the rows' own tokens (`diagonal`), or earlier ones
     __device__ __forceinline__ void add(const char* K, const char* V, int r0, float c, bool diagonal, int lane) {
-        const int half = lane >> 5, row = lane & 31;
         floatx16 s[1] = {X::rows_by(K, r0, q, lane)};
+        add_scores(s, V, r0, c, diagonal, lane);
+    }
+    __device__ __forceinline__ void add_scores(floatx16 (&s)[1], const char* V, int r0, float c, bool diagonal, int lane) {
+        const int half = lane >> 5, row = lane & 31;
         if (diagonal) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[0][i] = acc_row(i, half) > row ? -INFINITY : s[0][i];
@@ -79,6 +82,13 @@ struct Rows {
         } else {
             X::columns_by(V, r0, s[0], o, lane);
         }
+    }
+
+    __device__ __forceinline__ void finish(const AttnArgs& a, const RowBlock& w, int64_t q0, int row_bytes, int lane) {
+        const float all = halves_sum(sum);
+        store_columns<T, X::DB>(o, 1.f / all, head_rows(a.o, w, w.head, row_bytes), q0, w.len, lane);
+        if (a.lse && lane < 32 && q0 + lane < w.len)
+            a.lse[token_row(a, w, w.head) + q0 + lane] = (top + __builtin_amdgcn_logf(all)) * kLn2;
     }
 
     // A probability of 0 times an infinity or NaN in a later token's value would be NaN: the values of the one block
@@ -108,7 +118,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd(const At
     __shared__ alignas(16) char v0[X::BYTES];
     __shared__ alignas(16) char v1[X::BYTES];
     RowBlock w;
-    if (!locate_rows<true>(a, a.heads, blockIdx.x, w)) return;
+    if (!locate_rows<kAttnRows, true>(a, a.heads, blockIdx.x, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kv_head = w.head / (a.heads / a.kv_heads), row_bytes = a.dim * X::ES;
     const TileLoad<X> load_k(head_rows(a.k, w, kv_head, row_bytes), tid);
@@ -169,20 +179,78 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd(const At
             if (active && at <= q0) rows.add(odd ? k1 : k0, odd ? v1 : v0, r0, c, at == q0, lane);
         }
     }
-    if (!active) return;
-    const float sum = halves_sum(rows.sum);
-    store_columns<T, X::DB>(rows.o, 1.f / sum, head_rows(a.o, w, w.head, row_bytes), q0, w.len, lane);
-    if (a.lse && lane < 32 && q0 + lane < w.len)
-        a.lse[token_row(a, w, w.head) + q0 + lane] = (rows.top + __builtin_amdgcn_logf(sum)) * kLn2;
+    if (active) rows.finish(a, w, q0, row_bytes, lane);
 }
 
+// For few rows: a workgroup takes 32 query rows, and its waves the four parts of 32 keys of each tile of 128, with a
+// softmax of their own each, which are joined at the end.  Keys are loaded while probabilities meet values, values
+// while queries meet keys.
+template <typename T, int DC>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd_few(const AttnArgs a) {
+    using X = HeadTile<T, DC, 128>;
+    using R = Rows<T, DC>;
+    __shared__ alignas(16) char ks[X::BYTES];
+    __shared__ alignas(16) char vs[X::BYTES];
+    RowBlock w;
+    if (!locate_rows<kAttnFew, true>(a, a.heads, blockIdx.x, w)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kv_head = w.head / (a.heads / a.kv_heads), row_bytes = a.dim * X::ES;
+    const TileLoad<X> load_k(head_rows(a.k, w, kv_head, row_bytes), tid);
+    const TileLoad<X> load_v(head_rows(a.v, w, kv_head, row_bytes), tid);
+    const int64_t q0 = w.r0, kend = w.len < q0 + kAttnFew ? w.len : q0 + kAttnFew;
+    R rows;
+    load_rows<typename R::X>(rows.q, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
+    load_k(ks, 0, kend, wave);
+    load_v(vs, 0, kend, wave);
+    const float c = a.scale * kLog2e;
+    for (int64_t t = 0; t < kend; t += 128) {
+        const int64_t k0 = t + 32 * wave;
+        const bool mine = k0 < kend, more = t + 128 < kend;
+        tiles_ready_but<X::NLD>();
+        floatx16 s[1];
+        if (mine) s[0] = R::X::rows_by(ks, 32 * wave, rows.q, lane);
+        tiles_ready();
+        if (more) load_k(ks, t + 128, kend, wave);
+        if (mine) rows.add_scores(s, vs, 32 * wave, c, k0 == q0, lane);
+        __syncthreads();
+        if (more) load_v(vs, t + 128, kend, wave);
+    }
+    static_assert(2 * 64 * 16 * X::DB * 4 <= X::BYTES, "two waves' values fit a tile");
+    __shared__ float ends[2][2][64];
+    float* const end = &ends[wave >> 1][0][lane];
+    join_waves<16 * X::DB>((float*)ks, wave, lane,
+        [&](float* at) __attribute__((always_inline)) {
+            float* e = wave == 2 ? &ends[0][0][lane] : end;
+            e[0] = rows.top, e[64] = rows.sum;
+#pragma unroll
+            for (int db = 0; db < X::DB; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) at[(db * 16 + i) * 64] = rows.o[db][i];
+        },
+        [&](float* at) __attribute__((always_inline)) {
+            const float to = fmaxf(rows.top, end[0]), f = fast_exp2(rows.top - to), g = fast_exp2(end[0] - to);
+            rows.top = to;
+            rows.sum = rows.sum * f + end[64] * g;
+#pragma unroll
+            for (int db = 0; db < X::DB; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) rows.o[db][i] = rows.o[db][i] * f + at[(db * 16 + i) * 64] * g;
+        });
+    if (wave == 0) rows.finish(a, w, q0, row_bytes, lane);
+}
+
+template <typename T, int DC>
+void launch_dim(const AttnArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)(a.blocks * (uint64_t)a.heads * (a.cu ? 1 : a.b)));
+    if (a.few) attn_fwd_few<T, DC><<<grid, 256, 0, s>>>(a);
+    else attn_fwd<T, DC><<<grid, 256, 0, s>>>(a);
+}
 template <typename T>
 hipError_t launch_type(const AttnArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)(a.blocks * (uint64_t)a.heads * (a.cu ? 1 : a.b)));
-    if (a.dim <= 32) attn_fwd<T, 32><<<grid, 256, 0, s>>>(a);
-    else if (a.dim <= 64) attn_fwd<T, 64><<<grid, 256, 0, s>>>(a);
-    else if (a.dim <= 96) attn_fwd<T, 96><<<grid, 256, 0, s>>>(a);
-    else attn_fwd<T, 128><<<grid, 256, 0, s>>>(a);
+    if (a.dim <= 32) launch_dim<T, 32>(a, s);
+    else if (a.dim <= 64) launch_dim<T, 64>(a, s);
+    else if (a.dim <= 96) launch_dim<T, 96>(a, s);
+    else launch_dim<T, 128>(a, s);
     return hipGetLastError();
 }
 

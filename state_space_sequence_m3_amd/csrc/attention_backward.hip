@@ -9,6 +9,66 @@
 namespace m3 {
 namespace {
 
+// Adds up four waves' sums of the same columns, into the first's.
+template <int DB>
+__device__ __forceinline__ void join_sums(float* lds, int wave, int lane, floatx16 (&acc)[DB]) {
+    join_waves<16 * DB>(lds, wave, lane,
+        [&](float* at) __attribute__((always_inline)) {
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) at[(db * 16 + i) * 64] = acc[db][i];
+        },
+        [&](float* at) __attribute__((always_inline)) {
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[db][i] += at[(db * 16 + i) * 64];
+        });
+}
+
+// One wave's 32 query rows for dq, along the lanes as in the forward pass.
+template <typename T, int DC>
+struct DqRows {
+    using X = HeadTile<T, DC>;
+    uint4 q[X::SG], dout[X::SG];
+    floatx16 dq[X::DB] = {};
+    float lse, delta;
+
+    // reads the rows, and computes delta; `write`: keeps it for the second launch
+    __device__ __forceinline__ DqRows(const AttnArgs& a, const RowBlock& w, int64_t q0, bool write, int lane) {
+        const int row = lane & 31, row_bytes = a.dim * X::ES;
+        load_rows<X>(q, head_rows(a.o, w, w.head, row_bytes), q0, w.len, lane);
+        load_rows<X>(dout, head_rows(a.dout, w, w.head, row_bytes), q0, w.len, lane);
+        float d = 0.f;
+#pragma unroll
+        for (int g = 0; g < X::SG; ++g) d += X::dot(q[g], dout[g]);
+        delta = halves_sum(d);
+        load_rows<X>(q, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
+        const int64_t at = token_row(a, w, w.head) + q0 + row;
+        lse = 1e30f;   // rows that are not there: probabilities of 0
+        if (q0 + row < w.len) {
+            lse = a.lse[at] * kLog2e;
+            if (write && lane < 32) a.delta[at] = delta;
+        }
+    }
+    // scores and the products of dout with the values become ds
+    __device__ __forceinline__ void turn(floatx16& s, const floatx16& dp, float c, bool diagonal, int lane) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = fast_exp2(fmaf(s[i], c, -lse)) * (dp[i] - delta);
+        if (diagonal) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = acc_row(i, lane >> 5) > (lane & 31) ? 0.f : s[i];
+        }
+    }
+    __device__ __forceinline__ void add(const char* K, const char* V, int r0, float c, bool diagonal, int lane) {
+        floatx16 s = X::rows_by(K, r0, q, lane);
+        const floatx16 dp = X::rows_by(V, r0, dout, lane);
+        turn(s, dp, c, diagonal, lane);
+        X::columns_by(K, r0, s, dq, lane);
+    }
+};
+
 // dq: as the forward pass, scores transposed, 128 query rows to a workgroup and 32 to a wave.
 template <typename T, int DC>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq(const AttnArgs a) {
@@ -18,7 +78,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq(const Att
     __shared__ alignas(16) char v0[X::BYTES];
     __shared__ alignas(16) char v1[X::BYTES];
     RowBlock w;
-    if (!locate_rows<true>(a, a.heads, blockIdx.x, w)) return;
+    if (!locate_rows<kAttnRows, true>(a, a.heads, blockIdx.x, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kv_head = w.head / (a.heads / a.kv_heads), row_bytes = a.dim * X::ES;
     const TileLoad<X> load_k(head_rows(a.k, w, kv_head, row_bytes), tid);
@@ -29,46 +89,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq(const Att
     load_k(k0, 0, w.len, wave);
     load_v(v0, 0, w.len, wave);
     const int64_t q0 = w.r0 + 32 * wave;
-    const int half = lane >> 5, row = lane & 31;
     const bool active = q0 < w.len;
-
-    uint4 qf[X::SG], df[X::SG];
-    float delta = 0.f;
-    {
-        load_rows<X>(qf, head_rows(a.o, w, w.head, row_bytes), q0, w.len, lane);
-        load_rows<X>(df, head_rows(a.dout, w, w.head, row_bytes), q0, w.len, lane);
-#pragma unroll
-        for (int g = 0; g < X::SG; ++g) delta += X::dot(qf[g], df[g]);
-        delta = halves_sum(delta);
-    }
-    load_rows<X>(qf, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
-    const int64_t at = token_row(a, w, w.head) + q0 + row;
-    float lse = 1e30f;   // rows that are not there: probabilities of 0
-    if (q0 + row < w.len) {
-        lse = a.lse[at] * kLog2e;
-        if (half == 0) a.delta[at] = delta;
-    }
+    DqRows<T, DC> rows(a, w, q0, true, lane);
     const float c = a.scale * kLog2e;
-    floatx16 dq[X::DB] = {};
-
-    auto add = [&](const char* K, const char* V, int r0, bool diagonal) __attribute__((always_inline)) {
-        floatx16 s = X::rows_by(K, r0, qf, lane);
-        const floatx16 dp = X::rows_by(V, r0, df, lane);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = fast_exp2(fmaf(s[i], c, -lse)) * (dp[i] - delta);
-        if (diagonal) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = acc_row(i, half) > row ? 0.f : s[i];
-        }
-        X::columns_by(K, r0, s, dq, lane);
-    };
 
     auto turn = [&](int t, const char* K, const char* V, char* next_k, char* next_v) __attribute__((always_inline)) {
         tiles_ready();
         load_k(next_k, (int64_t)(t + 1) * X::ROWS, w.len, wave);
         load_v(next_v, (int64_t)(t + 1) * X::ROWS, w.len, wave);
 #pragma unroll
-        for (int r0 = 0; r0 < X::ROWS; r0 += 32) add(K, V, r0, false);
+        for (int r0 = 0; r0 < X::ROWS; r0 += 32) rows.add(K, V, r0, c, false, lane);
     };
     for (int t = 0; t < before; t += 2) {
         turn(t, k0, v0, k1, v1);
@@ -84,10 +114,92 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq(const Att
 #pragma unroll 1
         for (int r0 = 0; r0 < X::ROWS; r0 += 32) {
             const int64_t at = (int64_t)t * X::ROWS + r0;
-            if (active && at <= q0) add(odd ? k1 : k0, odd ? v1 : v0, r0, at == q0);
+            if (active && at <= q0) rows.add(odd ? k1 : k0, odd ? v1 : v0, r0, c, at == q0, lane);
         }
     }
-    if (active) store_columns<T, X::DB>(dq, a.scale, head_rows(a.dq, w, w.head, row_bytes), q0, w.len, lane);
+    if (active) store_columns<T, X::DB>(rows.dq, a.scale, head_rows(a.dq, w, w.head, row_bytes), q0, w.len, lane);
+}
+
+// For few rows: 32 of them to a workgroup, and the four parts of 32 keys of each tile of 128 to its waves, whose sums
+// are joined at the end.
+template <typename T, int DC>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_few(const AttnArgs a) {
+    using X = HeadTile<T, DC, 128>;
+    using R = DqRows<T, DC>;
+    __shared__ alignas(16) char ks[X::BYTES];
+    __shared__ alignas(16) char vs[X::BYTES];
+    RowBlock w;
+    if (!locate_rows<kAttnFew, true>(a, a.heads, blockIdx.x, w)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kv_head = w.head / (a.heads / a.kv_heads), row_bytes = a.dim * X::ES;
+    const TileLoad<X> load_k(head_rows(a.k, w, kv_head, row_bytes), tid);
+    const TileLoad<X> load_v(head_rows(a.v, w, kv_head, row_bytes), tid);
+    const int64_t q0 = w.r0, kend = w.len < q0 + kAttnFew ? w.len : q0 + kAttnFew;
+    R rows(a, w, q0, wave == 0, lane);
+    const float c = a.scale * kLog2e;
+    load_v(vs, 0, kend, wave);
+    load_k(ks, 0, kend, wave);
+    for (int64_t t = 0; t < kend; t += 128) {
+        const int64_t k0 = t + 32 * wave;
+        const bool mine = k0 < kend, more = t + 128 < kend;
+        floatx16 s, dp;
+        tiles_ready_but<X::NLD>();
+        if (mine) dp = X::rows_by(vs, 32 * wave, rows.dout, lane);
+        tiles_ready();
+        if (more) load_v(vs, t + 128, kend, wave);
+        if (mine) {
+            s = X::rows_by(ks, 32 * wave, rows.q, lane);
+            rows.turn(s, dp, c, k0 == q0, lane);
+            X::columns_by(ks, 32 * wave, s, rows.dq, lane);
+        }
+        __syncthreads();
+        if (more) load_k(ks, t + 128, kend, wave);
+    }
+    join_sums<X::DB>((float*)ks, wave, lane, rows.dq);
+    if (wave == 0) store_columns<T, X::DB>(rows.dq, a.scale, head_rows(a.dq, w, w.head, row_bytes), q0, w.len, lane);
+}
+
+// Scores of 32 query rows against the keys along the lanes become probabilities, and with the products of dout and
+// the values ds.  lse (log2 units) and delta: of the rows; `diagonal`: the rows are the keys' own tokens.
+__device__ __forceinline__ void soften(floatx16& s, const float* lse, float c, bool diagonal, int lane) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const floatx4 e = *(const floatx4*)(lse + 8 * n + 4 * (lane >> 5));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = fast_exp2(fmaf(s[4 * n + i], c, -e[i]));
+            s[4 * n + i] = diagonal && acc_row(4 * n + i, lane >> 5) < (lane & 31) ? 0.f : x;
+        }
+    }
+}
+__device__ __forceinline__ void turn(floatx16& p, const floatx16& dp, const float* delta, bool diagonal, int lane) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const floatx4 e = *(const floatx4*)(delta + 8 * n + 4 * (lane >> 5));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = p[4 * n + i] * (dp[4 * n + i] - e[i]);
+            p[4 * n + i] = diagonal && acc_row(4 * n + i, lane >> 5) < (lane & 31) ? 0.f : x;
+        }
+    }
+}
+
+// 32 keys' dk and dv, as they are or as part `split` of what is added up by another launch.
+template <typename T, int DB>
+__device__ __forceinline__ void store_grads(const AttnArgs& a, const RowBlock& w, uint32_t split, const floatx16 (&dk)[DB],
+                                            const floatx16 (&dv)[DB], int64_t k0, int lane) {
+    const int row_bytes = a.dim * (int)sizeof(T);
+    if (a.splits == 1) {
+        store_columns<T, DB>(dk, a.scale, head_rows(a.dk, w, w.head, row_bytes), k0, w.len, lane);
+        store_columns<T, DB>(dv, 1.f, head_rows(a.dv, w, w.head, row_bytes), k0, w.len, lane);
+        return;
+    }
+    const int64_t tokens = a.cu ? a.L : a.b * a.L, first = a.cu ? w.start : w.seq * a.L;
+    const uint32_t token = (uint32_t)a.kv_heads * a.dim * 4;
+    char* p = (char*)a.part + (split * tokens + first) * token + w.head * a.dim * 4;
+    const RowSource rk{p, token, a.dim * 4}, rv{p + a.splits * tokens * (int64_t)token, token, a.dim * 4};
+    store_columns<float, DB>(dk, a.scale, rk, k0, w.len, lane);
+    store_columns<float, DB>(dv, 1.f, rv, k0, w.len, lane);
 }
 
 // dk and dv: 128 keys to a workgroup and 32 to a wave, the keys along the lanes; query rows and their gradients
@@ -109,29 +221,12 @@ struct Grads {
         // what follows from the lane is computed again for every tile: kept over the loop (with the values' rows, which
         // do not change either) it would not fit the registers
         asm volatile("" : "+v"(lane));
-        const int half = lane >> 5, col = lane & 31;
         floatx16 p = X::rows_by(Q, 0, k, lane), dp;
         if constexpr (V_LDS) dp = X::rows_by_rows(D, 0, V, 32 * wave, lane);
         else dp = X::rows_by(D, 0, v, lane);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const floatx4 e = *(const floatx4*)(lse + 8 * n + 4 * half);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = fast_exp2(fmaf(p[4 * n + i], c, -e[i]));
-                p[4 * n + i] = OWN && diagonal && acc_row(4 * n + i, half) < col ? 0.f : x;
-            }
-        }
+        soften(p, lse, c, OWN && diagonal, lane);
         X::columns_by(D, 0, p, dv, lane);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const floatx4 e = *(const floatx4*)(delta + 8 * n + 4 * half);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = p[4 * n + i] * (dp[4 * n + i] - e[i]);
-                p[4 * n + i] = OWN && diagonal && acc_row(4 * n + i, half) < col ? 0.f : x;
-            }
-        }
+        turn(p, dp, delta, OWN && diagonal, lane);
         X::columns_by(Q, 0, p, dk, lane);
     }
 };
@@ -149,15 +244,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const At
     __shared__ alignas(16) float ra[2][32];   // lse in log2 units, delta
     __shared__ alignas(16) float rb[2][32];
     RowBlock w;
-    if (!locate_rows<false>(a, a.kv_heads, blockIdx.x, w)) return;
+    const uint32_t split = blockIdx.x % a.splits;
+    if (!locate_rows<kAttnRows, false>(a, a.kv_heads, blockIdx.x / a.splits, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int group = a.heads / a.kv_heads, row_bytes = a.dim * X::ES;
+    const int group = a.heads / a.kv_heads / a.splits, head0 = (w.head * a.splits + split) * group;
+    const int row_bytes = a.dim * X::ES;
     const int64_t k0 = w.r0 + 32 * wave;
     const bool active = k0 < w.len;
 
     G grads;
-    const TileLoad<X> load_q(head_rows(a.q, w, w.head * group, row_bytes), tid);
-    const TileLoad<X> load_d(head_rows(a.dout, w, w.head * group, row_bytes), tid);
+    const TileLoad<X> load_q(head_rows(a.q, w, head0, row_bytes), tid);
+    const TileLoad<X> load_d(head_rows(a.dout, w, head0, row_bytes), tid);
     // Lanes i and 32 + i of the first wave bring lse and delta of row i.  Without divergent branches, here and in all that
     // runs at the full number of registers: a compiler that has none to spare may put the copies that it splits
     // values with before the execution mask is whole again.
@@ -168,7 +265,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const At
         lq(Q, r0, w.len, wave);
         ld(D, r0, w.len, wave);
         if (wave == 0) {
-            const int64_t at = token_row(a, w, w.head * group + h) + r0;
+            const int64_t at = token_row(a, w, head0 + h) + r0;
             const int left = (int)(w.len - r0 < 32 ? w.len - r0 : 32), row = lane & 31;
             const float e = bits_to_f32(buffer_load_bits(make_rsrc(a.lse + at, left * 4), row * 4, 0.f)) * kLog2e;
             const float d = bits_to_f32(buffer_load_bits(make_rsrc(a.delta + at, left * 4), row * 4, 0.f));
@@ -217,17 +314,107 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const At
         grads.template add<false>(Q, D, vs, rows[0], rows[1], c, false, wave, lane);
     });
     if (!active) return;
-    store_columns<T, X::DB>(grads.dk, a.scale, head_rows(a.dk, w, w.head, row_bytes), k0, w.len, lane);
-    store_columns<T, X::DB>(grads.dv, 1.f, head_rows(a.dv, w, w.head, row_bytes), k0, w.len, lane);
+    store_grads<T>(a, w, split, grads.dk, grads.dv, k0, lane);
+}
+
+// For few keys: 32 of them to a workgroup, and the four parts of 32 rows of each tile of 128 to its waves, whose sums
+// are joined at the end.
+template <typename T, int DC>
+__global__ __launch_bounds__(256, sizeof(T) == 2 && DC <= 64 ? 2 : 1) void attn_dkv_few(const AttnArgs a) {
+    using X = HeadTile<T, DC, 128>;
+    __shared__ alignas(16) char qs[X::BYTES];
+    __shared__ alignas(16) char ds[X::BYTES];
+    __shared__ alignas(16) float rows[4][2][32];   // each wave's lse in log2 units, delta
+    RowBlock w;
+    const uint32_t split = blockIdx.x % a.splits;
+    if (!locate_rows<kAttnFew, false>(a, a.kv_heads, blockIdx.x / a.splits, w)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = lane >> 5, col = lane & 31;
+    const int group = a.heads / a.kv_heads / a.splits, head0 = (w.head * a.splits + split) * group;
+    const int row_bytes = a.dim * X::ES;
+    const int64_t k0 = w.r0;
+    TileLoad<X> load_q(head_rows(a.q, w, head0, row_bytes), tid);
+    TileLoad<X> load_d(head_rows(a.dout, w, head0, row_bytes), tid);
+    const float c = a.scale * kLog2e;
+    uint4 k[X::SG], v[X::SG];
+    load_rows<X>(k, head_rows(a.k, w, w.head, row_bytes), k0, w.len, lane);
+    load_rows<X>(v, head_rows(a.v, w, w.head, row_bytes), k0, w.len, lane);
+    floatx16 dk[X::DB] = {}, dv[X::DB] = {};
+    load_d(ds, k0, w.len, wave);
+    load_q(qs, k0, w.len, wave);
+    int64_t t = k0;
+    for (int h = 0; h < group;) {
+        const int64_t r0 = t + 32 * wave;
+        const bool mine = r0 < w.len, last = t + 128 >= w.len, more = !last || h + 1 < group;
+        const int head = head0 + h;
+        t = last ? k0 : t + 128;
+        if (last) {
+            ++h;
+            load_q.src.p += a.q.head;
+            load_d.src.p += a.dout.head;
+        }
+        floatx16 p, dp;
+        tiles_ready_but<X::NLD>();
+        if (mine) dp = X::rows_by(ds, 32 * wave, v, lane);
+        tiles_ready();
+        if (mine) {
+            p = X::rows_by(qs, 32 * wave, k, lane);
+            const int64_t at = token_row(a, w, head) + r0;
+            const int left = (int)(w.len - r0 < 32 ? w.len - r0 : 32);
+            const float e = bits_to_f32(buffer_load_bits(make_rsrc(a.lse + at, left * 4), col * 4, 0.f)) * kLog2e;
+            const float d = bits_to_f32(buffer_load_bits(make_rsrc(a.delta + at, left * 4), col * 4, 0.f));
+            rows[wave][half][col] = half ? d : col < left ? e : 1e30f;
+            __builtin_amdgcn_wave_barrier();
+            soften(p, rows[wave][0], c, r0 == k0, lane);
+            X::columns_by(ds, 32 * wave, p, dv, lane);
+            turn(p, dp, rows[wave][1], r0 == k0, lane);
+            __builtin_amdgcn_wave_barrier();
+        }
+        __syncthreads();
+        if (more) load_d(ds, t, w.len, wave);
+        if (mine) X::columns_by(qs, 32 * wave, p, dk, lane);
+        __syncthreads();
+        if (more) load_q(qs, t, w.len, wave);
+    }
+    join_sums<X::DB>((float*)qs, wave, lane, dk);
+    join_sums<X::DB>((float*)ds, wave, lane, dv);
+    if (wave != 0) return;
+    store_grads<T>(a, w, split, dk, dv, k0, lane);
+}
+
+// dk and dv out of the parts that the heads of a group were split into, 4 elements to a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_dkv_join(const AttnArgs a) {
+    const int64_t tokens = a.cu ? a.L : a.b * a.L, quads = a.dim / 4, n = tokens * a.kv_heads * quads;
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, i = e < n ? e : e - n;
+    if (e >= 2 * n) return;
+    const int d = (int)(i % quads) * 4, head = (int)(i / quads % a.kv_heads);
+    const int64_t t = i / quads / a.kv_heads;
+    if (a.cu && t >= packed_offset(a.cu, a.b, a.L)) return;
+    const float* p = a.part + (e < n ? 0 : a.splits) * n * 4 + i * 4;
+    floatx4 v = *(const floatx4*)p;
+    for (int j = 1; j < a.splits; ++j) v += *(const floatx4*)(p + j * n * 4);
+    const HeadRows& to = e < n ? a.dk : a.dv;
+    char* at = to.p + head * to.head + d * (int)sizeof(T);
+    at += a.cu ? t * to.token : t / a.L * to.batch + t % a.L * to.token;
+    if constexpr (sizeof(T) == 2) *(uint2*)at = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else *(floatx4*)at = v;
 }
 
 template <typename T, int DC>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
-    const uint64_t blocks = a.blocks * (uint64_t)(a.cu ? 1 : a.b);
-    attn_dq<T, DC><<<dim3((uint32_t)(blocks * a.heads)), 256, 0, s>>>(a);
+    const uint64_t b = a.cu ? 1 : a.b;
+    const dim3 rows((uint32_t)(a.blocks * b * a.heads)), keys((uint32_t)(a.kblocks * b * a.kv_heads * a.splits));
+    if (a.few) attn_dq_few<T, DC><<<rows, 256, 0, s>>>(a);
+    else attn_dq<T, DC><<<rows, 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_dkv<T, DC><<<dim3((uint32_t)(blocks * a.kv_heads)), 256, 0, s>>>(a);
+    if (a.kfew) attn_dkv_few<T, DC><<<keys, 256, 0, s>>>(a);
+    else attn_dkv<T, DC><<<keys, 256, 0, s>>>(a);
+    const hipError_t k = hipGetLastError();
+    if (k != hipSuccess || a.splits == 1) return k;
+    const int64_t quads = 2 * (a.cu ? a.L : a.b * a.L) * a.kv_heads * (a.dim / 4);
+    attn_dkv_join<T><<<dim3((uint32_t)((quads + 255) / 256)), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 template <typename T>

@@ -160,6 +160,49 @@ m3_status check_groups(int64_t a, int64_t b, int64_t c) {
 }
 
 // ------------------------------------------------------------------------- whole prompts
+// Blocks of R rows of all sequences of a head (packed: as many as there can be).
+int64_t row_blocks(const m3_attn_dims* d, bool packed, int64_t R) {
+    return packed ? d->seqlen / R + d->batch : (d->seqlen + R - 1) / R * d->batch;
+}
+// Workgroups of 128 rows need to be many: where they are at most so many, blocks of 32 rows are taken, whose waves
+// share the other axis.  Forward, at 256 of them: 4096 x 8 heads of 128 bf16 86 -> 73 us, 4 x 1024 29.5 -> 29.6, fp32
+// 155 -> 129; at 512: 2 x 2048 x 16 heads bf16 57 -> 80, fp32 321 -> 429.  dk and dv in bf16 at 512 blocks of keys lose (2
+// x 2048 x 16 heads, with dq: 202 -> 287 us), in fp32 they gain (4 x 2048, 32/8 heads 5051 -> 4704, 4096, 32/16 heads
+// 4897 -> 4468) and lose at 1024 (1394 -> 1498).
+// (A packed batch's block numbers are taken to be half a sequence's too many each.)
+constexpr int64_t kFewBlocks = 256, kFewKeyBlocks = 256, kFewKeyBlocks32 = 512;
+// dk and dv: the heads of a group are summed by one workgroup, or split over as many as make this number of blocks,
+// whose parts are added up by another launch.  Bf16, with dq, parts for 512, 1024 and 2048 blocks: 2 x 2048, 64/8 heads
+// of 128 758, 577 and 638 us, 4 x 2048, 32/8 heads 733, 586 and 653 us, 16 x 512, 32/8 heads 240, 269 and 330 us.  Blocks of
+// 32 keys, for 64, 128 and 256: 2048 x 8/2 heads 113, 93 and 92 us, fp32 482, 345 and 344.
+constexpr int64_t kSplitBlocks = 1024, kSplitFew = 128;
+struct KeyPlan {
+    int splits = 1;
+    bool few = false;
+};
+int64_t full_blocks(const m3_attn_dims* d, bool packed) {
+    return row_blocks(d, packed, m3::kAttnRows) - (packed ? d->batch / 2 : 0);
+}
+KeyPlan plan_keys(const m3_attn_dims* d, bool packed) {
+    const int64_t n = full_blocks(d, packed) * d->kv_heads;
+    auto split = [&](int64_t to) {
+        const int64_t group = d->kv_heads * d->head_dim * 4 < kMaxTokenBytes ? d->heads / d->kv_heads : 1;
+        int64_t best = 1;
+        for (int64_t s = 2; s <= group && n * best < to; ++s)
+            if (group % s == 0) best = s;
+        return (int)best;
+    };
+    KeyPlan p;
+    if (d->io == M3_BF16) {
+        p.splits = split(kSplitBlocks);
+        p.few = n * p.splits <= kFewKeyBlocks;
+    } else {
+        p.few = n <= kFewKeyBlocks32;
+    }
+    if (p.few) p.splits = split(kSplitFew);
+    return p;
+}
+
 struct Attn {
     int64_t b, L, rows;   // rows: tokens of all sequences
     float scale;
@@ -176,8 +219,11 @@ m3_status check_attn(const m3_attn_dims* d, bool packed) {
     M3_TRY(check_heads(d->heads, d->kv_heads, d->head_dim, d->io));
     if (d->flags != 0) return fail(M3_E_DIMS, "dims->flags must be 0");
     M3_TRY(check_counts(d->batch, d->seqlen));
-    const int64_t blocks = packed ? d->seqlen / m3::kAttnRows + d->batch : (d->seqlen + m3::kAttnRows - 1) / m3::kAttnRows;
-    return check_groups(blocks, d->heads, packed ? 1 : d->batch);
+    return check_groups(row_blocks(d, packed, m3::kAttnRows), d->heads, 1);
+}
+uint32_t blocks_of(const m3_attn_dims* d, bool packed, bool few) {   // of the batch, dense: of a sequence
+    const int64_t n = row_blocks(d, packed, few ? m3::kAttnFew : m3::kAttnRows);
+    return (uint32_t)(packed || d->batch == 0 ? n : n / d->batch);
 }
 m3_status plan_attn(Attn* p, const m3_attn_dims* d, const int32_t* cu, const void* q, const void* k, const void* v,
                     const void* o, const float* lse) {
@@ -201,12 +247,21 @@ m3_status plan_attn(Attn* p, const m3_attn_dims* d, const int32_t* cu, const voi
     a.b = d->batch, a.L = d->seqlen;
     a.heads = (int)d->heads, a.kv_heads = (int)d->kv_heads, a.dim = (int)d->head_dim;
     a.scale = p->scale;
-    a.blocks = (uint32_t)(packed ? d->seqlen / m3::kAttnRows + d->batch
-                                 : (d->seqlen + m3::kAttnRows - 1) / m3::kAttnRows);
+    const KeyPlan keys = plan_keys(d, packed);
+    a.few = full_blocks(d, packed) * d->heads <= kFewBlocks;
+    a.kfew = keys.few;
+    a.splits = keys.splits;
+    a.blocks = blocks_of(d, packed, a.few);
+    a.kblocks = blocks_of(d, packed, a.kfew);
     return M3_OK;
 }
+// delta, then the parts of dk and dv
+size_t delta_bytes(const m3_attn_dims* d, bool packed) {
+    return ((size_t)(packed ? d->seqlen : d->batch * d->seqlen) * (size_t)d->heads * 4 + 15) & ~(size_t)15;
+}
 size_t backward_bytes(const m3_attn_dims* d, bool packed) {
-    return (size_t)(packed ? d->seqlen : d->batch * d->seqlen) * (size_t)d->heads * 4;
+    const size_t rows = (size_t)(packed ? d->seqlen : d->batch * d->seqlen), splits = (size_t)plan_keys(d, packed).splits;
+    return delta_bytes(d, packed) + (splits > 1 ? 2 * splits * rows * (size_t)(d->kv_heads * d->head_dim) * 4 : 0);
 }
 
 // --------------------------------------------------------------------------- paged cache
@@ -319,6 +374,7 @@ m3_status m3_attention_backward(const m3_attn_dims* d, const int32_t* cu_seqlens
     if (p.rows == 0 || p.b == 0) return M3_OK;
     p.args.dout = rows_of(ado), p.args.dq = rows_of(adq), p.args.dk = rows_of(adk), p.args.dv = rows_of(adv);
     p.args.delta = (float*)workspace;
+    p.args.part = (float*)((char*)workspace + delta_bytes(d, packed));
     return launched(m3::launch_attention_backward(p.args, d->io == M3_BF16, stream), "m3_attention_backward");
 }
 

@@ -11,6 +11,7 @@ namespace m3 {
 
 // ------------------------------------------------------------------------- whole prompts
 constexpr int kAttnRows = 128;        // query rows (backward: keys) of a workgroup, 32 to a wave
+constexpr int kAttnFew = 32;          // the same where the other axis is split over the waves
 constexpr int64_t kAttnMaxDim = 128;  // elements of a head
 
 // rows of heads: bytes between consecutive sequences (dense batches), tokens and heads
@@ -29,7 +30,10 @@ struct AttnArgs {
     int64_t b, L;                // sequences; tokens of each (dense) or of all (packed)
     int heads, kv_heads, dim;
     float scale;
-    uint32_t blocks;             // row blocks of all sequences (packed: as many as there can be)
+    uint32_t blocks, kblocks;    // blocks of query rows and of keys (packed: as many as there can be)
+    int few, kfew;               // they are kAttnFew rows, not kAttnRows
+    int splits;                  // backward: parts that the heads of a group are split into for dk and dv
+    float* part;                 // splits > 1: dk, then dv, of each part, [2, splits, tokens, kv_heads, D]
 };
 hipError_t launch_attention(const AttnArgs& a, bool bf16_io, hipStream_t s);
 hipError_t launch_attention_backward(const AttnArgs& a, bool bf16_io, hipStream_t s);

@@ -162,18 +162,19 @@ struct RowSource {
     }
 };
 
-// What a workgroup works on: kAttnRows rows of one head of one sequence.
+// What a workgroup works on: R rows of one head of one sequence.
 struct RowBlock {
     int64_t seq, start, len;   // sequence; its first token on the packed axis (dense: 0); its tokens
     int head;
     int64_t r0;                // first row, in the sequence
 };
 
-// Dense batches: blocks of equal numbers run side by side over all heads, from the one with most work on (the last
+// Of query rows (LAST_FIRST) or keys.  Dense batches: blocks of equal numbers run side by side over all heads, from the one with most work on (the last
 // queries, the first keys), and an XCD's workgroups share the heads of a contiguous range, so that query heads of a key head meet in one L2.
 // Packed ones: numbers that first_block's map leaves over have no rows.
-template <bool LAST_FIRST>
+template <int R, bool LAST_FIRST>
 __device__ __forceinline__ bool locate_rows(const AttnArgs& a, int heads, uint32_t id, RowBlock& w) {
+    const uint32_t blocks = LAST_FIRST ? a.blocks : a.kblocks;
     if (!a.cu) {
         const uint32_t pairs = (uint32_t)a.b * heads;
         uint32_t pair, blk;
@@ -185,22 +186,22 @@ __device__ __forceinline__ bool locate_rows(const AttnArgs& a, int heads, uint32
             pair = id % pairs;
             blk = id / pairs;
         }
-        if (LAST_FIRST) blk = a.blocks - 1 - blk;
+        if (LAST_FIRST) blk = blocks - 1 - blk;
         w.seq = pair / heads;
         w.head = (int)(pair % heads);
         w.start = 0;
         w.len = a.L;
-        w.r0 = (int64_t)blk * kAttnRows;
+        w.r0 = (int64_t)blk * R;
         return true;
     }
     w.head = (int)(id % heads);
-    const uint32_t slot = LAST_FIRST ? a.blocks - 1 - id / heads : id / heads;
+    const uint32_t slot = LAST_FIRST ? blocks - 1 - id / heads : id / heads;
     // the last sequence whose first number is at most the slot
-    const int64_t lo = last_at_most(a.b, slot, [&](int64_t s) { return first_block(packed_offset(a.cu, s, a.L), s, kAttnRows); });
+    const int64_t lo = last_at_most(a.b, slot, [&](int64_t s) { return first_block(packed_offset(a.cu, s, a.L), s, R); });
     w.seq = lo;
     w.start = packed_offset(a.cu, lo, a.L);
     w.len = packed_offset(a.cu, lo + 1, a.L) - w.start;
-    w.r0 = ((int64_t)slot - first_block(w.start, lo, kAttnRows)) * kAttnRows;
+    w.r0 = ((int64_t)slot - first_block(w.start, lo, R)) * R;
     return w.r0 >= 0 && w.r0 < w.len;
 }
 
@@ -241,6 +242,30 @@ struct TileLoad {
 __device__ __forceinline__ void tiles_ready() {
     __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): loads into LDS count there
     __syncthreads();
+}
+
+// The same for all but the last N loads of each wave.
+template <int N>
+__device__ __forceinline__ void tiles_ready_but() {
+    static_assert(N < 64, "vmcnt has 6 bits");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4 << 14));
+    __syncthreads();
+}
+
+// Adds up what the four waves of a workgroup hold for the same columns, into the first: `mine` is called with a place
+// of N floats per lane to put its values to, `theirs` with one to take another wave's from.  The place is
+// 2 * 64 * N floats of LDS that no tile needs any more.
+template <int N, typename F, typename G>
+__device__ __forceinline__ void join_waves(float* lds, int wave, int lane, F&& mine, G&& theirs) {
+    float* at = lds + (wave >> 1) * 64 * N + lane;
+    __syncthreads();
+    if (wave & 1) mine(at);
+    __syncthreads();
+    if (!(wave & 1)) theirs(at);
+    __syncthreads();
+    if (wave == 2) mine(lds + lane);
+    __syncthreads();
+    if (wave == 0) theirs(lds + lane);
 }
 
 // The chunks 2 g + h of row (lane % 32), for use as a right operand.

@@ -332,8 +332,11 @@ def test_workspaces():
     lib = m3attn.load()
     d = attn_dims()
     need = lib.m3_attention_backward_workspace_bytes(ctypes.byref(d), 0)
-    assert need == 2 * 300 * 8 * 4
-    assert lib.m3_attention_backward_workspace_bytes(ctypes.byref(d), 1) == 300 * 8 * 4
+    part = 2 * 600 * 2 * 64 * 4                             # dk and dv of one part of the heads of a group
+    assert need > 600 * 8 * 4 and (need - 600 * 8 * 4) % part == 0
+    alone = attn_dims(kv_heads=8)                           # nothing to split
+    assert lib.m3_attention_backward_workspace_bytes(ctypes.byref(alone), 0) == 600 * 8 * 4
+    assert lib.m3_attention_backward_workspace_bytes(ctypes.byref(alone), 1) == 300 * 8 * 4
     assert lib.m3_attention_backward_workspace_bytes(ctypes.byref(attn_dims(head_dim=7)), 0) == 0
     assert BWD(cu=0, ws_bytes=need - 1) == m3scan.M3_E_WORKSPACE
     assert BWD(cu=0, workspace=0) == m3scan.M3_E_WORKSPACE
