@@ -1,9 +1,9 @@
 // attention_step.hip -- one token's attention per sequence over a paged cache (m3_attention_step).
 //
-// Memory-bound: each key and value is read once for the query heads that share it.  A sequence's keys are cut into pieces
-// of a length that follows from all lengths together, so that pieces fill the GPU whatever the lengths are; a
-// piece is a workgroup's, whose 4 waves take its tiles in turn, each with a running maximum and sum of its own, and
-// the pieces of a sequence are joined by a second launch.
+// Memory-bound: each key and value is read once for the query heads that share it.  All sequences' keys, one after the
+// other, are cut into equal pieces, so that the GPU is filled once whatever the lengths are; a piece is a
+// workgroup's, whose 4 waves take the tiles of a sequence in turn, each with a running maximum and sum of its own, and what
+// pieces hold of a sequence that is cut is joined by a second launch.
 //
 // Up to 16 query heads of a key head are the columns of 16x16 products.  Scores are computed transposed (keys down), with
 // the keys in an order that makes a lane's probabilities those of 8 (fp32: 4) consecutive keys: the right operand of the
@@ -18,11 +18,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Pieces of a batch: all are `keys` long but the last of a sequence.
-struct Cut {
-    int64_t keys;
-    __device__ __forceinline__ int64_t pieces(int64_t len) const { return pieces_of(len, keys); }
-};
 __device__ __forceinline__ int64_t length_of(const StepArgs& a, int64_t s) {
     const int64_t n = a.lens[s], most = a.pages.table_w * (int64_t)a.pages.size;
     return n < 0 ? 0 : n > most ? most : n;
@@ -32,40 +27,41 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
     for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
     return v;
 }
-__device__ __forceinline__ Cut cut_batch(const StepArgs& a) {
-    int64_t all = 0;
-    for (int64_t s = threadIdx.x & 63; s < a.b; s += 64) all += length_of(a, s);
-    all = wave_sum(all);
-    return {piece_keys(all, a.items)};
+// The keys of a piece.  first: the lane's of the first 64 rounded lengths.
+__device__ __forceinline__ int64_t cut_batch(const StepArgs& a, int64_t& first) {
+    const int64_t lane = threadIdx.x & 63;
+    first = lane < a.b ? rounded_keys(length_of(a, lane)) : 0;
+    int64_t all = first;
+    for (int64_t s = lane + 64; s < a.b; s += 64) all += rounded_keys(length_of(a, s));
+    return piece_keys(wave_sum(all), a.items);
 }
-// The sequence that piece `item` belongs to (-1: there are fewer pieces), the pieces before it, and its length.
-__device__ __forceinline__ int64_t find_piece(const StepArgs& a, const Cut& cut, int64_t item, int64_t& before, int64_t& len) {
+// The sequence that key `at` of the batch belongs to (-1: there are fewer), and the keys before it.
+__device__ __forceinline__ int64_t find_key(const StepArgs& a, int64_t first, int64_t at, int64_t& before) {
     const int lane = threadIdx.x & 63;
     before = 0;
     for (int64_t s0 = 0; s0 < a.b; s0 += 64) {
-        const int64_t l = s0 + lane < a.b ? length_of(a, s0 + lane) : 0;
-        const int64_t mine = s0 + lane < a.b ? cut.pieces(l) : 0;
+        const int64_t mine = s0 == 0 ? first : s0 + lane < a.b ? rounded_keys(length_of(a, s0 + lane)) : 0;
         int64_t upto = mine;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int64_t u = __shfl_up(upto, d, 64);
             if (lane >= d) upto += u;
         }
-        const uint64_t past = __ballot(before + upto > item);
+        const uint64_t past = __ballot(before + upto > at);
         if (past) {
             const int i = __ffsll((unsigned long long)past) - 1;
             before += __shfl(upto - mine, i, 64);
-            len = __shfl(l, i, 64);
             return s0 + i;
         }
         before += __shfl(upto, 63, 64);
     }
     return -1;
 }
-// The pieces before sequence s.
-__device__ __forceinline__ int64_t pieces_before(const StepArgs& a, const Cut& cut, int64_t s) {
-    int64_t n = 0;
-    for (int64_t i = threadIdx.x & 63; i < s; i += 64) n += cut.pieces(length_of(a, i));
+// The keys before sequence s.
+__device__ __forceinline__ int64_t keys_before(const StepArgs& a, int64_t first, int64_t s) {
+    const int64_t lane = threadIdx.x & 63;
+    int64_t n = lane < s ? first : 0;
+    for (int64_t i = lane + 64; i < s; i += 64) n += rounded_keys(length_of(a, i));
     return wave_sum(n);
 }
 
@@ -88,16 +84,24 @@ struct Piece {
     // the key of score row r in block n
     static __device__ __forceinline__ int key_of(int r, int n) { return BF ? 8 * (r >> 2) + 4 * n + (r & 3) : r; }
 
-    __device__ __forceinline__ void load(const StepArgs& a, const int32_t* table, int kv_head, int64_t k0, int64_t kend,
-                                         int lane) {
+    // Where a tile's keys are: the tile's page and place (TILED), or lane i's those of key i.
+    struct Where {
+        int id = -1, place = 0;
+    };
+    static __device__ __forceinline__ Where look(const StepArgs& a, const int32_t* table, int64_t k0, int64_t kend, int lane) {
+        Where w;
+        const int64_t k = TILED ? k0 : k0 + (lane & 31);
+        if (k < kend && (TILED || (lane & 31) < TILE)) w.id = page_of(a.pages, table, (int32_t)k, w.place);
+        return w;
+    }
+
+    __device__ __forceinline__ void load(const StepArgs& a, Where w, int kv_head, int64_t k0, int64_t kend, int lane) {
         const int r16 = lane & 15, g = lane >> 4, row_bytes = a.dim * ES;
         const Pages& p = a.pages;
         const int left = (int)(kend - k0 < TILE ? kend - k0 : TILE);
         const int vcol = r16 * VE * ES;
         if constexpr (TILED) {
-            int place;
-            const int id = __builtin_amdgcn_readfirstlane(page_of(p, table, (int32_t)k0, place));
-            place = __builtin_amdgcn_readfirstlane(place);
+            const int id = __builtin_amdgcn_readfirstlane(w.id), place = __builtin_amdgcn_readfirstlane(w.place);
             const int rows = id >= 0 ? left : 0;
             const int64_t at = id >= 0 ? id : 0;
             const rsrc_t kr = make_rsrc(p.k + at * p.k_page + kv_head * p.k_head + place * (int64_t)p.k_token,
@@ -120,9 +124,7 @@ struct Piece {
 #pragma unroll
             for (int i = 0; i < 4 * BLK; ++i) there |= (VK * g + i < rows ? 1u : 0u) << i;
         } else {
-            // lane i looks key i up for all
-            int place = 0, id = -1;
-            if ((lane & 31) < left) id = page_of(p, table, (int32_t)(k0 + (lane & 31)), place);
+            const int id = w.id, place = w.place;
 #pragma unroll
             for (int n = 0; n < BLK; ++n) {
                 const int key = key_of(r16, n), kid = __shfl(id, key, 64), kplace = __shfl(place, key, 64);
@@ -214,148 +216,179 @@ struct Piece {
     }
 };
 
-// Partial results: a piece's heads one after another, {maximum (log2 units), sum, D unscaled elements} each.
-__device__ __forceinline__ int64_t part_row(const StepArgs& a, int64_t item, int head) {
-    return (item * a.heads + head) * (2 + a.dim);
+// Partial results: of each part (piece + sequence) the heads one after another, {maximum (log2 units), sum, D unscaled
+// elements} each.
+__device__ __forceinline__ int64_t part_row(const StepArgs& a, int64_t part, int head) {
+    return (part * a.heads + head) * (2 + a.dim);
 }
 
 template <typename T, int DC, bool TILED>
 __global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
     using P = Piece<T, DC, TILED>;
-    constexpr int VE = P::VE;
+    constexpr int VE = P::VE, STEP = 4 * P::TILE;
     __shared__ float tops[4][16], sums[4][16];
     __shared__ float outs[4][16][DC + 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int hb = blockIdx.x % a.head_blocks, kv_head = blockIdx.x / a.head_blocks % a.kv_heads;
     const int64_t item = blockIdx.x / a.head_blocks / a.kv_heads;
-    const int group = a.heads / a.kv_heads;
-    const Cut cut = cut_batch(a);
-    int64_t before, len = 0;
-    const int64_t s = find_piece(a, cut, item, before, len);
-    if (s < 0) return;
-    const int64_t k0 = (item - before) * cut.keys, kend = k0 + cut.keys < len ? k0 + cut.keys : len;
-    const int32_t* table = a.pages.table + s * a.pages.table_w;
-    const int in_group = hb * 16 + col, head = kv_head * group + in_group;
-
-    uint4 q[P::KS];
-#pragma unroll
-    for (int j = 0; j < P::KS; ++j) {
-        const int at = (4 * j + g) * 16;
-        q[j] = make_uint4(0, 0, 0, 0);
-        if (in_group < group && at < a.dim * P::ES) q[j] = *(const uint4*)(a.q.p + s * a.q.batch + head * a.q.head + at);
-    }
-    const float c = a.scale * kLog2e;
-    floatx4 acc[VE] = {};
-    float top = -1e37f, sum = 0.f;
-
-    P now, next;
-    int64_t k = k0 + wave * P::TILE;
-    if (k < kend) now.load(a, table, kv_head, k, kend, lane);
-    for (; k < kend; k += 4 * P::TILE) {
-        const bool more = k + 4 * P::TILE < kend;
-        if (more) next.load(a, table, kv_head, k + 4 * P::TILE, kend, lane);
-        float p[4 * P::BLK];
-        now.scores(q, p);
-        float m = p[0];
-#pragma unroll
-        for (int i = 1; i < 4 * P::BLK; ++i) m = fmaxf(m, p[i]);
-        m = fmaxf(m, __shfl_xor(m, 16, 64));
-        m = fmaxf(m, __shfl_xor(m, 32, 64)) * c;
-        if (__ballot(m > top)) {
-            const float to = fmaxf(top, m), f = fast_exp2(top - to);
-#pragma unroll
-            for (int j = 0; j < VE; ++j) acc[j] *= f;
-            sum *= f;
-            top = to;
-        }
-#pragma unroll
-        for (int i = 0; i < 4 * P::BLK; ++i) {
-            p[i] = fast_exp2(fmaf(p[i], c, -top));
-            sum += p[i];
-        }
-        now.values(p, acc);
-        now = next;
-    }
-    sum += __shfl_xor(sum, 16, 64);
-    sum += __shfl_xor(sum, 32, 64);
-
-    // the four waves' results
-    if (g == 0) {
-        tops[wave][col] = top;
-        sums[wave][col] = sum;
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int j = 0; j < VE; ++j) outs[wave][col][(4 * g + m) * VE + j] = acc[j][m];
-    __syncthreads();
-    const bool whole = cut.pieces(len) == 1;
+    const int group = a.heads / a.kv_heads, in_group = hb * 16 + col;
     const int heads_here = group - hb * 16 < 16 ? group - hb * 16 : 16;
-    for (int e = threadIdx.x; e < heads_here * a.dim; e += 256) {
-        const int h = e / a.dim, d = e % a.dim, at = kv_head * group + hb * 16 + h;
-        const float t = fmaxf(fmaxf(tops[0][h], tops[1][h]), fmaxf(tops[2][h], tops[3][h]));
-        float n = 0.f, o = 0.f;
+    const float c = a.scale * kLog2e;
+    int64_t first, start;
+    const int64_t keys = cut_batch(a, first), lo = item * keys;
+    int64_t s = find_key(a, first, lo, start);
+    if (s < 0) return;
+
+    while (true) {
+        // keys k0 .. kend - 1 of sequence s, which starts at `start`
+        const int64_t len = length_of(a, s), stop = start + rounded_keys(len);
+        const int64_t k0 = lo > start ? lo - start : 0;
+        const int64_t kend = lo + keys < start + len ? lo + keys - start : len;
+        const int32_t* table = a.pages.table + s * a.pages.table_w;
+        const int head = kv_head * group + in_group;
+
+        uint4 q[P::KS];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float f = fast_exp2(tops[w][h] - t);
-            n = fmaf(f, sums[w][h], n);
-            o = fmaf(f, outs[w][h][d], o);
+        for (int j = 0; j < P::KS; ++j) {
+            const int at = (4 * j + g) * 16;
+            q[j] = make_uint4(0, 0, 0, 0);
+            if (in_group < group && at < a.dim * P::ES) q[j] = *(const uint4*)(a.q.p + s * a.q.batch + head * a.q.head + at);
         }
-        if (whole) {
-            // nothing to attend to: zeros
-            *(T*)(a.o.p + s * a.o.batch + at * a.o.head + d * P::ES) = from_f32<T>(t > -1e37f || n != 0.f ? o / n : 0.f);
-            if (a.lse && d == 0) a.lse[s * a.heads + at] = (t + __builtin_amdgcn_logf(n)) * kLn2;
-        } else {
-            float* part = a.part + part_row(a, item, at);
-            part[2 + d] = o;
-            if (d == 0) part[0] = t, part[1] = n;
+        floatx4 acc[VE] = {};
+        float top = -1e37f, sum = 0.f;
+
+        // keys and values are loaded a tile ahead, and looked up two
+        P now, next;
+        int64_t k = k0 + wave * P::TILE;
+        typename P::Where ahead = P::look(a, table, k + STEP, kend, lane);
+        if (k < kend) now.load(a, P::look(a, table, k, kend, lane), kv_head, k, kend, lane);
+        for (; k < kend; k += STEP) {
+            const typename P::Where far = P::look(a, table, k + 2 * STEP, kend, lane);
+            if (k + STEP < kend) next.load(a, ahead, kv_head, k + STEP, kend, lane);
+            ahead = far;
+            float p[4 * P::BLK];
+            now.scores(q, p);
+            float m = p[0];
+#pragma unroll
+            for (int i = 1; i < 4 * P::BLK; ++i) m = fmaxf(m, p[i]);
+            m = fmaxf(m, __shfl_xor(m, 16, 64));
+            m = fmaxf(m, __shfl_xor(m, 32, 64)) * c;
+            if (__ballot(m > top)) {
+                const float to = fmaxf(top, m), f = fast_exp2(top - to);
+#pragma unroll
+                for (int j = 0; j < VE; ++j) acc[j] *= f;
+                sum *= f;
+                top = to;
+            }
+#pragma unroll
+            for (int i = 0; i < 4 * P::BLK; ++i) {
+                p[i] = fast_exp2(fmaf(p[i], c, -top));
+                sum += p[i];
+            }
+            now.values(p, acc);
+            now = next;
         }
+        sum += __shfl_xor(sum, 16, 64);
+        sum += __shfl_xor(sum, 32, 64);
+
+        // the four waves' results
+        __syncthreads();
+        if (g == 0) {
+            tops[wave][col] = top;
+            sums[wave][col] = sum;
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int j = 0; j < VE; ++j) outs[wave][col][(4 * g + m) * VE + j] = acc[j][m];
+        __syncthreads();
+        const bool whole = start >= lo && stop <= lo + keys;
+        for (int e = threadIdx.x; e < heads_here * a.dim; e += 256) {
+            const int h = e / a.dim, d = e % a.dim, at = kv_head * group + hb * 16 + h;
+            const float t = fmaxf(fmaxf(tops[0][h], tops[1][h]), fmaxf(tops[2][h], tops[3][h]));
+            float n = 0.f, o = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = fast_exp2(tops[w][h] - t);
+                n = fmaf(f, sums[w][h], n);
+                o = fmaf(f, outs[w][h][d], o);
+            }
+            if (whole) {
+                // nothing to attend to: zeros
+                *(T*)(a.o.p + s * a.o.batch + at * a.o.head + d * P::ES) = from_f32<T>(t > -1e37f || n != 0.f ? o / n : 0.f);
+                if (a.lse && d == 0) a.lse[s * a.heads + at] = (t + __builtin_amdgcn_logf(n)) * kLn2;
+            } else {
+                float* part = a.part + part_row(a, item + s, at);
+                part[2 + d] = o;
+                if (d == 0) part[0] = t, part[1] = n;
+            }
+        }
+        if (stop >= lo + keys || ++s >= a.b) return;
+        start = stop;
     }
 }
 
-// Joins the pieces of one head of one sequence.
+// Joins the parts of one head of one sequence: 16 groups of 16 lanes take a part each at a time, 8 elements to a lane.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_step_join(const StepArgs a) {
-    __shared__ float outs[2][128];
-    __shared__ float tops[4], sums[4];
+    __shared__ float outs[16][128 + 8];
+    __shared__ float tops[16], sums[16];
     const int64_t s = blockIdx.x / a.heads;
     const int head = (int)(blockIdx.x % a.heads);
-    const Cut cut = cut_batch(a);
-    const int64_t n = cut.pieces(length_of(a, s));
+    int64_t first;
+    const int64_t keys = cut_batch(a, first), start = keys_before(a, first, s);
+    const int64_t own = s < 64 ? __shfl(first, (int)s, 64) : rounded_keys(length_of(a, s));
+    const int64_t item = start / keys, n = (start + own - 1) / keys - item + 1;
     if (n <= 1) return;
-    const int64_t first = pieces_before(a, cut, s);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    float top = -1e37f;
-    for (int64_t i = tid; i < n; i += 256) top = fmaxf(top, a.part[part_row(a, first + i, head)]);
+    const float* part = a.part + part_row(a, item + s, head);
+    const int64_t next = (int64_t)a.heads * (2 + a.dim);   // from a part to the next one
+    const int tid = threadIdx.x, group = tid >> 4, d0 = (tid & 15) * 8;
+    float o[8] = {}, top = -1e37f, sum = 0.f;
+    for (int64_t i = group; i < n; i += 16) {
+        const float* p = part + i * next;
+        const float t = p[0], w = p[1];
+        float x[8] = {};
+        if (d0 < a.dim) {   // rows of 2 + dim floats: pairs are aligned
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
-    if (lane == 0) tops[wave] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    // two halves of the workgroup take every other piece, an element to a thread
-    const int d = tid & 127, from = tid >> 7;
-    float o = 0.f, sum = 0.f;
-    for (int64_t i = from; i < n; i += 2) {
-        const float* part = a.part + part_row(a, first + i, head);
-        const float f = fast_exp2(part[0] - top);
-        sum = fmaf(f, part[1], sum);
-        if (d < a.dim) o = fmaf(f, part[2 + d], o);
+            for (int j = 0; j < 8; j += 2) {
+                const float2 u = *(const float2*)(p + 2 + d0 + j);
+                x[j] = u.x, x[j + 1] = u.y;
+            }
+        }
+        const float to = fmaxf(top, t), f = fast_exp2(top - to), g = fast_exp2(t - to);
+        top = to;
+        sum = sum * f + w * g;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = o[j] * f + x[j] * g;
     }
-    outs[from][d] = o;
-    if (d == 0) sums[from] = sum;
+    if (d0 < a.dim) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) outs[group][d0 + j] = o[j];
+    }
+    if (d0 == 0) tops[group] = top, sums[group] = sum;
     __syncthreads();
     if (tid < a.dim) {
-        sum = sums[0] + sums[1];
+        float t = tops[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) t = fmaxf(t, tops[i]);
+        float v = 0.f, w = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float f = fast_exp2(tops[i] - t);
+            w = fmaf(f, sums[i], w);
+            v = fmaf(f, outs[i][tid], v);
+        }
+        // nothing to attend to: zeros
         *(T*)(a.o.p + s * a.o.batch + head * a.o.head + tid * (int)sizeof(T)) =
-            from_f32<T>(top > -1e37f || sum != 0.f ? (outs[0][tid] + outs[1][tid]) / sum : 0.f);
-        if (a.lse && tid == 0) a.lse[s * a.heads + head] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+            from_f32<T>(t > -1e37f || w != 0.f ? v / w : 0.f);
+        if (a.lse && tid == 0) a.lse[s * a.heads + head] = (t + __builtin_amdgcn_logf(w)) * kLn2;
     }
 }
 
 template <typename T, int DC>
 hipError_t launch_dim(const StepArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)((a.items + a.b) * a.kv_heads * a.head_blocks));
+    const dim3 grid((uint32_t)(a.items * a.kv_heads * a.head_blocks));
     if (a.pages.size % Piece<T, DC, true>::TILE == 0) attn_step<T, DC, true><<<grid, 256, 0, s>>>(a);
     else attn_step<T, DC, false><<<grid, 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();

@@ -303,8 +303,10 @@ m3_status plan_cache(Cache* c, const m3_cache_dims* d, const void* k, const void
     return M3_OK;
 }
 
-// How a decoding batch is cut: pieces of work per key head (and block of 16 query heads), so many that the GPU is
-// filled a few times over and lengths that differ even out, but none shorter than 256 keys.
+// How a decoding batch is cut: into as many pieces per key head (and block of 16 query heads) as fill the GPU once,
+// two workgroups to a compute unit, but none shorter than a round of a workgroup.  Sequences that cannot be longer than
+// a round are a piece each.  (64 sequences of 2048, 32/8 heads of 128 bf16, with one, two and four times as many pieces: 103,
+// 111 and 120 us.)
 struct StepPlan {
     int64_t items = 1, head_blocks = 1;
     bool joined = true;
@@ -314,14 +316,14 @@ m3_status plan_step(const m3_cache_dims* d, StepPlan* p) {
     M3_TRY(check_cache_dims(d, 0));
     p->head_blocks = (d->heads / d->kv_heads + 15) / 16;
     const int64_t most = d->table_width * d->page_size;   // below 2^62
-    p->joined = most <= m3::kMinPiece || d->batch == 0;
-    p->items = 1;
+    p->joined = most <= m3::kRound || d->batch == 0;
+    p->items = d->batch;
     if (!p->joined) {
-        const int64_t want = 4 * (int64_t)m3::device_cus() / (d->kv_heads * p->head_blocks);
-        const int64_t per = most / m3::kMinPiece + 1, all = per > kMaxCount / d->batch ? kMaxCount : per * d->batch;
+        const int64_t want = 2 * (int64_t)m3::device_cus() / (d->kv_heads * p->head_blocks);
+        const int64_t per = most / m3::kRound + 1, all = per > kMaxCount / d->batch ? kMaxCount : per * d->batch;
         p->items = std::max<int64_t>(1, std::min(want, all));
     }
-    M3_TRY(check_groups(p->items + d->batch, d->kv_heads, p->head_blocks));
+    M3_TRY(check_groups(p->items, d->kv_heads, p->head_blocks));
     M3_TRY(check_groups(d->batch, d->heads, 1));
     if (!p->joined) p->bytes = (size_t)(p->items + d->batch) * (size_t)d->heads * (size_t)(2 + d->head_dim) * 4;
     return M3_OK;

@@ -71,7 +71,7 @@ struct StepArgs {
     int64_t b;
     int heads, kv_heads, dim;
     float scale;
-    int64_t items;               // pieces of work per key head and block of query heads, without one per sequence
+    int64_t items;               // pieces of work per key head and block of query heads
     int head_blocks;             // blocks of 16 query heads of a key head
     int joined;                  // no sequence is cut: no second launch
 };

@@ -25,13 +25,16 @@ M3_HD int32_t page_place(const int32_t* row, int64_t width, int32_t pages, int32
 // The next sequence's first number leaves it at least as many as it has blocks, and all are below T / R + b.
 M3_HD int64_t first_block(int64_t start, int64_t s, int64_t R) { return start / R + s; }
 
-// Pieces of at most `keys` keys that a sequence of `len` is cut into: one at least.
-M3_HD int64_t pieces_of(int64_t len, int64_t keys) { return len <= keys ? 1 : (len + keys - 1) / keys; }
-// The length of pieces that makes at most items + b of them out of b sequences of `all` keys together.
-constexpr int64_t kMinPiece = 256;
+// A decoding batch as one row of keys, sequence after sequence, each rounded up to whole rounds of a workgroup (an empty
+// one to one round): piece i is keys i * n .. (i + 1) * n - 1 of it, whatever sequences they belong to.  Going along the
+// row, the piece or the sequence or both go up at each border, so that i + s numbers the parts of sequences in
+// pieces, below pieces + b.
+constexpr int64_t kRound = 128;
+M3_HD int64_t rounded_keys(int64_t len) { return len <= kRound ? kRound : (len + kRound - 1) / kRound * kRound; }
+// The length of pieces that makes at most `items` of them out of `all` keys.
 M3_HD int64_t piece_keys(int64_t all, int64_t items) {
     const int64_t even = (all + items - 1) / items;
-    return even < kMinPiece ? kMinPiece : (even + 127) / 128 * 128;
+    return rounded_keys(even);
 }
 
 }  // namespace m3

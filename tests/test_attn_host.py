@@ -105,20 +105,24 @@ int main() {
         }
         for (long t = 0; t < T; ++t) CHECK(seen[t] == (t < cu[b] ? 1 : 0));
     }
-    // pieces of a decoding batch: never more than items + b, none longer than the piece, an empty sequence has one
+    // pieces of a decoding batch: at most `items`, whole rounds, and numbers piece + sequence of their parts all
+    // different, those of a sequence in a row, below items + b
     for (int round = 0; round < 2000; ++round) {
         const long b = 1 + rnd(200), items = 1 + rnd(2000), most = 1 + rnd(100000);
-        std::vector<long> len(b);
-        long all = 0, n = 0;
-        for (long& l : len) all += l = rnd(3) ? rnd(most) : 0;
-        const long keys = piece_keys(all, items);
-        CHECK(keys >= kMinPiece && keys % 128 == 0);
-        for (long l : len) {
-            const long k = pieces_of(l, keys);
-            CHECK(k >= 1 && k * keys >= l && (k == 1 || (k - 1) * keys < l));
-            n += k;
+        std::vector<long> start(b + 1, 0);
+        for (long s = 0; s < b; ++s) {
+            const long len = rnd(3) ? rnd(most) : 0, n = rounded_keys(len);
+            CHECK(n >= kRound && n % kRound == 0 && n >= len && (n == kRound || n - kRound < len));
+            start[s + 1] = start[s] + n;
         }
-        CHECK(n <= items + b);
+        const long keys = piece_keys(start[b], items), pieces = (start[b] + keys - 1) / keys;
+        CHECK(keys >= kRound && keys % kRound == 0 && pieces <= items);
+        std::vector<int> seen(items + b, 0);
+        for (long s = 0; s < b; ++s)
+            for (long i = start[s] / keys; i <= (start[s + 1] - 1) / keys; ++i) {
+                CHECK(i < pieces && i + s < items + b);
+                CHECK(!seen[i + s]++);
+            }
     }
     std::printf("ok\n");
     return 0;
@@ -344,14 +348,14 @@ def test_workspaces():
     need = lib.m3_attention_step_workspace_bytes(ctypes.byref(d))
     assert need > 0 and need % (8 * (2 + 64) * 4) == 0
     assert STEP(ws_bytes=need - 1) == m3scan.M3_E_WORKSPACE
-    short = cache_dims(table_width=16)      # 256 positions: never cut
+    short = cache_dims(table_width=8)       # 128 positions: never cut
     assert lib.m3_attention_step_workspace_bytes(ctypes.byref(short)) == 0
     assert lib.m3_attention_step_workspace_bytes(ctypes.byref(cache_dims(flags=1))) == 0
 
 
 @pytest_nodev
 def test_step_needs_no_workspace_for_short_tables():
-    assert STEP(dims=cache_dims(table_width=16), workspace=0, ws_bytes=0) == NODEVICE
+    assert STEP(dims=cache_dims(table_width=8), workspace=0, ws_bytes=0) == NODEVICE
 
 
 def test_cache_sizes():
