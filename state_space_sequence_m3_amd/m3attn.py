@@ -17,7 +17,7 @@ import functools
 import torch
 
 from . import m3scan
-from .m3block import _alike, _check, _current_device, _dense, _io_code, _ptr, _raw_stream, _scope, _workspace
+from .m3block import _alike, _check, _current_device, _dense, _io_code, _new, _ptr, _raw_stream, _scope, _workspace
 from .m3scan import M3_BF16, M3_F32, M3Error, STATUS_NAMES  # noqa: F401
 
 EXPORTED = ["m3_attention", "m3_attention_backward_workspace_bytes", "m3_attention_backward", "m3_cache_append",
@@ -93,7 +93,7 @@ def _heads(t, name, shape, dtype, index):
     """Checks a tensor of heads (None passes) and returns its (batch, token, head) strides; dense: zeros."""
     if t is None:
         return _DENSE
-    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape):
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == index):
         _alike(t, name, shape, dtype, index)
     if t.is_contiguous():
         return _DENSE
@@ -106,6 +106,11 @@ def _heads(t, name, shape, dtype, index):
     return s
 
 
+def _like(t, dense):
+    """An output like t, dense."""
+    return _new(t) if dense is _DENSE else t.new_empty(t.shape)
+
+
 def _scale(scale):
     if scale is None:
         return 0.0
@@ -116,15 +121,22 @@ def _scale(scale):
 
 def _prompt_shape(q, k, cu_seqlens):
     """(b, L, Hq, Hkv, D) of q [b, L, Hq, D], or [T, Hq, D] with offsets [b + 1], and the shape of k and v."""
-    shape, rank = q.shape, 4 if cu_seqlens is None else 3
-    if len(shape) != rank:
-        raise ValueError("q must be [b, L, H, D] (or [T, H, D] with cu_seqlens), got %s" % (tuple(shape),))
-    if k.dim() != rank:
-        raise ValueError("k must be like q but for its heads, got %s" % (tuple(k.shape),))
-    hk = k.shape[-2]
-    kv = (*shape[:-2], hk, shape[-1])
     if cu_seqlens is None:
-        return (*shape[:3], hk, shape[3]), kv
+        try:
+            b, L, hq, d = q.shape
+        except ValueError:
+            raise ValueError("q must be [b, L, H, D] (or [T, H, D] with cu_seqlens), got %s" % (tuple(q.shape),)) from None
+        if k.dim() != 4:
+            raise ValueError("k must be like q but for its heads, got %s" % (tuple(k.shape),))
+        hk = k.shape[2]
+        return (b, L, hq, hk, d), (b, L, hk, d)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [b, L, H, D] (or [T, H, D] with cu_seqlens), got %s" % (tuple(shape),))
+    if k.dim() != 3:
+        raise ValueError("k must be like q but for its heads, got %s" % (tuple(k.shape),))
+    hk = k.shape[1]
+    kv = (shape[0], hk, shape[2])
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [b + 1], got %s" % (tuple(cu_seqlens.shape),))
     _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, q.get_device())
@@ -144,15 +156,16 @@ def m3_attention(q, k, v, cu_seqlens=None, scale=None, o=None, lse=None, save_ls
     sizes, kv = _prompt_shape(q, k, cu_seqlens)
     io, shape, dev = q.dtype, q.shape, q.get_device()
     packed = cu_seqlens is not None
-    ref = _attn_ref(*sizes, _heads(q, "q", shape, io, dev), _heads(k, "k", kv, io, dev), _heads(v, "v", kv, io, dev),
-                    _heads(o, "o", shape, io, dev), _DENSE, _DENSE, _DENSE, _DENSE, _io_code(q, "q"), 0, _scale(scale))
+    qs = _heads(q, "q", shape, io, dev)
+    ref = _attn_ref(*sizes, qs, _heads(k, "k", kv, io, dev), _heads(v, "v", kv, io, dev), _heads(o, "o", shape, io, dev),
+                    _DENSE, _DENSE, _DENSE, _DENSE, _io_code(q, "q"), 0, _scale(scale))
     if lse is not None:
         _dense(lse, "lse", _lse_shape(sizes, packed), torch.float32, dev)
     if stream is not None or dev < 0 or dev != _current_device():
         with _scope(q, stream):
             return m3_attention(q, k, v, cu_seqlens, scale, o, lse, save_lse)
     if o is None:
-        o = q.new_empty(shape)
+        o = _like(q, qs)
     if lse is None and save_lse:
         lse = q.new_empty(_lse_shape(sizes, packed), dtype=torch.float32)
     status = lib.m3_attention(ref, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse),
@@ -193,19 +206,19 @@ def m3_attention_backward(q, k, v, o, lse, dout, cu_seqlens=None, scale=None, gr
     return g
 
 
-def _page_strides(t, name, shape, dtype, index):
-    """(page, token, head) strides of a cache [pages, Hkv, page_size, D]; dense: zeros."""
-    page, head, token = _heads(t, name, shape, dtype, index)
-    return page, token, head
-
-
 def _cache_shape(k_cache, v_cache, page_table, b, hk, d, io, dev):
-    """(pages, page size, table width) and the caches' strides, checked."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, H, page_size, D], got %s" % (tuple(k_cache.shape),))
-    pages, page = k_cache.shape[0], k_cache.shape[2]
-    shape = (pages, hk, page, d)
-    ks, vs = _page_strides(k_cache, "k_cache", shape, io, dev), _page_strides(v_cache, "v_cache", shape, io, dev)
+    """(pages, page size, table width) and the caches' (page, token, head) strides, checked."""
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError("k_cache must be [pages, H, page_size, D], got %s" % (tuple(shape),))
+    pages, h, page, width = shape
+    if h != hk or width != d:
+        _alike(k_cache, "k_cache", (pages, hk, page, d), io, dev)
+    ks, vs = _heads(k_cache, "k_cache", shape, io, dev), _heads(v_cache, "v_cache", shape, io, dev)
+    if ks is not _DENSE:
+        ks = (ks[0], ks[2], ks[1])
+    if vs is not _DENSE:
+        vs = (vs[0], vs[2], vs[1])
     if page_table is None or page_table.dim() != 2:
         raise ValueError("page_table must be [b, pages of a sequence]")
     width = page_table.shape[1]
@@ -231,8 +244,9 @@ def m3_cache_append(k, v, k_cache=None, v_cache=None, page_table=None, lens=None
         if q_out is not None:
             raise ValueError("q_out without q")
         hq = hk
-    qs, ks, vs = _heads(q, "q", shape, io, dev), _heads(k, "k", kv, io, dev), _heads(v, "v", kv, io, dev)
-    kos = _heads(k_out, "k_out", kv, io, dev)
+    qs = _DENSE if q is None else _heads(q, "q", shape, io, dev)
+    ks, vs = _heads(k, "k", kv, io, dev), _heads(v, "v", kv, io, dev)
+    kos = _DENSE if k_out is None else _heads(k_out, "k_out", kv, io, dev)
     if lens is not None:
         _dense(lens, "lens", (b,), torch.int32, dev)
     rot = 0
@@ -253,7 +267,7 @@ def m3_cache_append(k, v, k_cache=None, v_cache=None, page_table=None, lens=None
         with _scope(k, stream):
             return m3_cache_append(k, v, k_cache, v_cache, page_table, lens, q, inv_freq, halves, cu_seqlens, q_out, k_out)
     if q is not None and q_out is None:
-        q_out = q.new_empty(shape)
+        q_out = _like(q, qs)
     status = lib.m3_cache_append(ref, _ptr(cu_seqlens), _ptr(lens), _ptr(inv_freq), _ptr(q), k.data_ptr(), _ptr(v),
                                  _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _raw_stream(dev))
     if status:
@@ -275,8 +289,9 @@ def m3_attention_step(q, k_cache, v_cache, page_table, lens, scale=None, o=None,
     if _dense(lens, "lens", (b,), torch.int32, dev) is None:
         raise ValueError("lens is required")
     code = _io_code(q, "q")
-    _, qb, qh = _heads(q, "q", shape, io, dev)
-    _, ob, oh = _heads(o, "o", shape, io, dev)
+    dense = _heads(q, "q", shape, io, dev)
+    _, qb, qh = dense
+    _, ob, oh = _DENSE if o is None else _heads(o, "o", shape, io, dev)
     ref = _cache_ref(b, 1, hq, hk, d, pages, page, width, 0, kcs, vcs, (qb, 0, qh), _DENSE, _DENSE, _DENSE, _DENSE,
                      (ob, 0, oh), code, 0, _scale(scale))
     if lse is not None:
@@ -285,7 +300,7 @@ def m3_attention_step(q, k_cache, v_cache, page_table, lens, scale=None, o=None,
         with _scope(q, stream):
             return m3_attention_step(q, k_cache, v_cache, page_table, lens, scale, o, lse, workspace)
     if o is None:
-        o = q.new_empty(shape)
+        o = _like(q, dense)
     workspace, ws_bytes = _workspace(workspace, _step_workspace(b, hq, hk, d, pages, page, width, code, dev), q)
     status = lib.m3_attention_step(ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
                                    lens.data_ptr(), o.data_ptr(), _ptr(lse), _ptr(workspace), ws_bytes, _raw_stream(dev))
