@@ -23,9 +23,9 @@ struct Rows {
     floatx16 o[X::DB] = {};
     float top = -1e37f, sum = 0.f;   // log2 units; this half's part of the sum
 
-    // the scores against 32 keys become probabilities
+    // makes room for scores against 32 N keys: the running maximum is their bound within kSlack
     template <int N>
-    __device__ __forceinline__ void soften(floatx16 (&s)[N], float c) {
+    __device__ __forceinline__ void raise(const floatx16 (&s)[N], float c) {
         float m = s[0][0];
 #pragma unroll
         for (int n = 0; n < N; ++n)
@@ -39,6 +39,10 @@ struct Rows {
             sum *= f;
             top = to;
         }
+    }
+    // they become probabilities
+    template <int N>
+    __device__ __forceinline__ void soften(floatx16 (&s)[N], float c) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             float part = 0.f;
@@ -62,6 +66,7 @@ struct Rows {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[0][i] = acc_row(i, half) > row ? -INFINITY : s[0][i];
         }
+        raise(s, c);
         soften(s, c);
         if (diagonal && any_odd(V, r0, lane)) {
             // key by key, each for the rows that see it
@@ -150,11 +155,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd(const At
         tiles_ready();
         if (t + 2 < ntiles) load_k(old_k, (int64_t)(t + 2) * X::ROWS, w.len, wave);
         load_v(old_v, (int64_t)(t + 1) * X::ROWS, w.len, wave);
-        rows.soften(s, c);
-        // a wave with products to issue goes first: 343 -> 327 us at b8 L2048, 32/8 heads of 128 bf16
+        rows.raise(s, c);
+        // a wave with products to issue goes first: 343 -> 323 us at b8 L2048, 32/8 heads of 128 bf16
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int n = 0; n < X::SUB; ++n) ahead[n] = X::rows_by(K, 32 * n, rows.q, lane);
+        rows.soften(s, c);
 #pragma unroll
         for (int n = 0; n < X::SUB; ++n) X::columns_by(V, 32 * n, s[n], rows.o, lane);
         __builtin_amdgcn_s_setprio(0);
