@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd(const At
 #pragma unroll
         for (int n = 0; n < X::SUB; ++n) ahead[n] = X::rows_by(K, 32 * n, rows.q, lane);
         rows.soften(s, c);
-#pragma unroll
+        // (no pragma: unrolled at once, this takes registers that are not there)
         for (int n = 0; n < X::SUB; ++n) X::columns_by(V, 32 * n, s[n], rows.o, lane);
         __builtin_amdgcn_s_setprio(0);
 #pragma unroll
