@@ -299,3 +299,124 @@ def test_graph(io):
         torch.cuda.synchronize()
         assert torch.equal(o, want_o)
         assert all(torch.equal(g[x], want[x]) for x in "qkv")
+
+
+# Batches above are small, so blocks of 32 rows whose waves share the other axis; with many heads the kernels take
+# blocks of 128 rows.  What the heads' number decides: rows (over 256 blocks), keys (over 256, fp32 512), and into how
+# many parts the heads of a group are split for dk and dv (up to 1024 blocks; small ones up to 128).
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [32, 40, 64, 96, 104, 128])
+def test_many_heads(io, d):
+    lens = [129, 0, 1, 300, 33, 64]
+    q, k, v, dout = draw(sum(lens), 180, 180, d, IO[io], 40 + d)
+    check_packed(q, k, v, dout, lens)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [100, 128, 256, 290])
+def test_many_heads_dense(io, n):
+    b, hq, hk, d = 2, 320, 160, 64
+    q, k, v, dout = draw(b * n, hq, hk, d, IO[io], n)
+    ref = attn_ref.prompt(q, k, v, [n] * b, None, dout)
+    qd, kd, vd, dd = (x.to(DEV).unflatten(0, (b, n)) for x in (q, k, v, dout))
+    o, lse = m3attn.m3_attention(qd, kd, vd, save_lse=True)
+    g = m3attn.m3_attention_backward(qd, kd, vd, o, lse, dd)
+    torch.cuda.synchronize()
+    assert_close(o.flatten(0, 1), ref["o"], ref["tol"]["o"], "o")
+    assert_close(lse.transpose(0, 1).flatten(1), ref["lse"], ref["tol"]["lse"], "lse")
+    for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        assert_close(g[key].flatten(0, 1), ref[name], ref["tol"][name], name)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hk,d", [(160, 40, 64), (240, 40, 128), (96, 16, 32), (30, 5, 96), (12, 2, 128)])
+def test_groups_split_over_workgroups(io, hq, hk, d):
+    """dk and dv out of parts, dense and packed with rows behind the last sequence."""
+    lens, more = [200, 0, 33], 9
+    n = sum(lens)
+    q, k, v, dout = draw(n + more, hq, hk, d, IO[io], hq + d)
+    ref = attn_ref.prompt(q[:n], k[:n], v[:n], lens, None, dout[:n])
+    qd, kd, vd, dd, cu = q.to(DEV), k.to(DEV), v.to(DEV), dout.to(DEV), offsets(lens)
+    o, lse = m3attn.m3_attention(qd, kd, vd, cu, save_lse=True)
+    wide = torch.full((n + more, hq + 2 * hk, d), 7.0, dtype=IO[io], device=DEV)
+    grads = {"q": wide[:, :hq], "k": wide[:, hq:hq + hk], "v": wide[:, hq + hk:]}
+    m3attn.m3_attention_backward(qd, kd, vd, o, lse, dd, cu, grads=grads)
+    torch.cuda.synchronize()
+    for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        assert_close(grads[key][:n], ref[name], ref["tol"][name], name)
+    assert (wide[n:] == 7.0).all()
+    b, rows = 2, 116
+    x = [t[:b * rows].to(DEV).unflatten(0, (b, rows)) for t in (q, k, v, dout)]
+    ref = attn_ref.prompt(q[:b * rows], k[:b * rows], v[:b * rows], [rows] * b, None, dout[:b * rows])
+    o, lse = m3attn.m3_attention(*x[:3], save_lse=True)
+    first = [torch.empty(b, h, rows, d, dtype=IO[io], device=DEV).transpose(1, 2) for h in (hq, hk, hk)]
+    g = m3attn.m3_attention_backward(*x[:3], o, lse, x[3], grads=dict(zip("qkv", first)))
+    torch.cuda.synchronize()
+    for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        assert_close(g[key].flatten(0, 1), ref[name], ref["tol"][name], name)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_later_tokens_do_not_reach_a_row_of_many_heads(io, bad):
+    lens, d, h = [300, 20], 64, 130
+    q, k, v, _ = draw(sum(lens), h, 1, d, IO[io], 41)
+    cu = offsets(lens)
+    want = m3attn.m3_attention(q.to(DEV), k.to(DEV), v.to(DEV), cu)
+    for at in (0, 40, 127, 200, 299):
+        x = v.clone()
+        x[at, 0, 3] = bad
+        o = m3attn.m3_attention(q.to(DEV), k.to(DEV), x.to(DEV), cu)
+        torch.cuda.synchronize()
+        tol = 2.0 ** -6 if io == "bf16" else 2.0 ** -18
+        assert torch.allclose(o[:at].float(), want[:at].float(), atol=tol, rtol=tol), at
+        assert torch.equal(o[300:], want[300:])
+        touched = o[at:300, :, 3].float()
+        assert (torch.isnan(touched) if bad != bad else touched == bad).all(), at
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_graph_of_many_heads(io):
+    """Blocks of 128 rows and split groups, captured and replayed between eager work: equal bits."""
+    b, n, hq, hk, d = 2, 150, 160, 40, 128
+    q, k, v, dout = (x.to(DEV).unflatten(0, (b, n)) for x in draw(b * n, hq, hk, d, IO[io], 42))
+
+    def once():
+        o, lse = m3attn.m3_attention(q, k, v, save_lse=True)
+        return o, m3attn.m3_attention_backward(q, k, v, o, lse, dout)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        once()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, g = once()
+    for i in range(4):
+        for t, x in zip((q, k, v, dout), draw(b * n, hq, hk, d, IO[io], 50 + i)):
+            t.copy_(x.unflatten(0, (b, n)))
+        want_o, want = once()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want_o)
+        assert all(torch.equal(g[x], want[x]) for x in "qkv")
+
+
+def test_tokens_far_apart():
+    """Rows over 4 GB of a buffer: addresses beyond 32 bits."""
+    n, d, token = 2100, 64, 1 << 20
+    room = torch.empty(n * token, dtype=torch.bfloat16, device=DEV)
+    rows = lambda at: room.as_strided((n, 1, d), (token, d, 1), at * d)
+    q, k, v, dout = draw(n, 1, 1, d, torch.bfloat16, 43)
+    ins = [rows(i) for i in range(4)]
+    for t, x in zip(ins, (q, k, v, dout)):
+        t.copy_(x)
+    ref = attn_ref.prompt(q, k, v, [n], None, dout)
+    cu = offsets([n])
+    o, lse = m3attn.m3_attention(*ins[:3], cu, o=rows(4), save_lse=True)
+    g = m3attn.m3_attention_backward(*ins[:3], o, lse, ins[3], cu, grads={x: rows(5 + i) for i, x in enumerate("qkv")})
+    torch.cuda.synchronize()
+    assert_close(o, ref["o"], ref["tol"]["o"], "o")
+    for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        assert_close(g[key], ref[name], ref["tol"][name], name)

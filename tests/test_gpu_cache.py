@@ -389,3 +389,22 @@ def test_step_streams():
         for s in streams:
             s.synchronize()
         assert all(torch.equal(x, want) for x in got)
+
+
+def test_large_cache():
+    """Caches of 5 GB each: pages beyond 32 bits, appended to and read."""
+    hk, hq, d, page, pages = 8, 16, 128, 64, 40000
+    kd, vd = (torch.empty(pages, hk, page, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    table = torch.tensor([[39999, 17], [20001, 39000]], dtype=torch.int32)
+    n = 100
+    g = torch.Generator().manual_seed(22)
+    k, v = (torch.randn(2, n, hk, d, generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(2, hq, d, generator=g).bfloat16()
+    m3attn.m3_cache_append(k.to(DEV), v.to(DEV), kd, vd, table.to(DEV))
+    o = m3attn.m3_attention_step(q.to(DEV), kd, vd, table.to(DEV), torch.full((2,), n, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    for s in range(2):
+        for i in (0, 63, 64, 99):
+            assert torch.equal(kd[table[s, i // page], :, i % page].cpu(), k[s, i])
+    ref = attn_ref.step(q, [x.transpose(0, 1) for x in k], [x.transpose(0, 1) for x in v])
+    assert_close(o, ref["o"], ref["tol"]["o"], "o")
