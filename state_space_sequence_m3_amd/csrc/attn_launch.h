@@ -32,6 +32,7 @@ struct AttnArgs {
     float scale;
     uint32_t blocks, kblocks;    // blocks of query rows and of keys (packed: as many as there can be)
     int few, kfew;               // they are kAttnFew rows, not kAttnRows
+    int paired;                  // two workgroups to a compute unit: paired_item's order
     int splits;                  // backward: parts that the heads of a group are split into for dk and dv
     float* part;                 // splits > 1: dk, then dv, of each part, [2, splits, tokens, kv_heads, D]
 };

@@ -177,6 +177,7 @@ __device__ __forceinline__ bool locate_rows(const AttnArgs& a, int heads, uint32
     const uint32_t blocks = LAST_FIRST ? a.blocks : a.kblocks;
     if (!a.cu) {
         const uint32_t pairs = (uint32_t)a.b * heads;
+        if (a.paired) id = (uint32_t)paired_item(id, (int64_t)pairs * blocks);
         uint32_t pair, blk;
         if (pairs % kXcds == 0) {
             const uint32_t per = pairs / kXcds, r = id / kXcds;

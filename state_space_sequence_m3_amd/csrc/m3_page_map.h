@@ -25,6 +25,17 @@ M3_HD int32_t page_place(const int32_t* row, int64_t width, int32_t pages, int32
 // The next sequence's first number leaves it at least as many as it has blocks, and all are below T / R + b.
 M3_HD int64_t first_block(int64_t start, int64_t s, int64_t R) { return start / R + s; }
 
+// Workgroups that are given out from the heaviest on meet two to a compute unit, 256 numbers apart: the second 256 (in
+// steps of 8, so that each stays on its XCD) are taken from the other end, heavy ones with light ones.  A permutation of
+// [0, n).
+constexpr int64_t kUnits = 256;
+M3_HD int64_t paired_item(int64_t i, int64_t n) {
+    const int64_t end = (n < 2 * kUnits ? n : 2 * kUnits) / kXcds * kXcds;
+    if (i < kUnits || i >= end) return i;
+    const int64_t r = i / kXcds, first = kUnits / kXcds, last = end / kXcds - 1;
+    return (first + last - r) * kXcds + i % kXcds;
+}
+
 // A decoding batch as one row of keys, sequence after sequence, each rounded up to whole rounds of a workgroup (an empty
 // one to one round): piece i is keys i * n .. (i + 1) * n - 1 of it, whatever sequences they belong to.  Going along the
 // row, the piece or the sequence or both go up at each border, so that i + s numbers the parts of sequences in

@@ -105,6 +105,15 @@ int main() {
         }
         for (long t = 0; t < T; ++t) CHECK(seen[t] == (t < cu[b] ? 1 : 0));
     }
+    // the order of workgroups: a permutation that keeps each on its XCD
+    for (long n = 1; n <= 2000; ++n) {
+        std::vector<int> seen(n, 0);
+        for (long i = 0; i < n; ++i) {
+            const long j = (long)paired_item(i, n);
+            CHECK(j >= 0 && j < n && !seen[j]++ && j % kXcds == i % kXcds);
+            CHECK(j == i || (i >= kUnits && i < 2 * kUnits));
+        }
+    }
     // pieces of a decoding batch: at most `items`, whole rounds, and numbers piece + sequence of their parts all
     // different, those of a sequence in a row, below items + b
     for (int round = 0; round < 2000; ++round) {
