@@ -251,8 +251,6 @@ m3_status plan_attn(Attn* p, const m3_attn_dims* d, const int32_t* cu, const voi
     a.few = full_blocks(d, packed) * d->heads <= kFewBlocks;
     a.kfew = keys.few;
     a.splits = keys.splits;
-    // 4096 tokens, 16/8 heads of 128 bf16, 512 workgroups: 94 -> 90 us; fp32, one to a compute unit, 611 -> 758 us
-    a.paired = d->io == M3_BF16;
     a.blocks = blocks_of(d, packed, a.few);
     a.kblocks = blocks_of(d, packed, a.kfew);
     return M3_OK;
