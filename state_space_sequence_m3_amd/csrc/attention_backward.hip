@@ -202,50 +202,51 @@ __device__ __forceinline__ void store_grads(const AttnArgs& a, const RowBlock& w
     store_columns<float, DB>(dv, 1.f, rv, k0, w.len, lane);
 }
 
-// dk and dv: 128 keys to a workgroup and 32 to a wave, the keys along the lanes; query rows and their gradients
-// go by in tiles of 32, head after head of the group.
+// dk and dv: 32 keys to a wave and 128 (4 waves) or 256 (8) to a workgroup, the keys along the lanes; query rows and their
+// gradients go by in tiles of 32 or 64, head after head of the group.
 //
 // Registers bound it: keys, dk and dv of 32 x 128 elements are 160 of the 256 that two waves to a SIMD have, so bf16 heads
 // over 64 elements keep their values in LDS, a right operand that is read again for every tile.
 template <typename T, int DC>
 struct Grads {
     static constexpr bool V_LDS = sizeof(T) == 2 && DC > 64;
-    using X = HeadTile<T, DC, 32>;
+    using X = HeadTile<T, DC>;
     uint4 k[X::SG], v[V_LDS ? 1 : X::SG];
     floatx16 dk[X::DB] = {}, dv[X::DB] = {};
 
-    // rows of one tile; OWN: they may be the keys' own tokens (`diagonal`)
+    // rows r0 .. r0 + 31 of a tile; OWN: they may be the keys' own tokens (`diagonal`)
     template <bool OWN>
     __device__ __forceinline__ void add(const char* Q, const char* D, const char* V, const float* lse, const float* delta,
-                                        float c, bool diagonal, int wave, int lane) {
+                                        int r0, float c, bool diagonal, int wave, int lane) {
         // what follows from the lane is computed again for every tile: kept over the loop (with the values' rows, which
         // do not change either) it would not fit the registers
         asm volatile("" : "+v"(lane));
-        floatx16 p = X::rows_by(Q, 0, k, lane), dp;
-        if constexpr (V_LDS) dp = X::rows_by_rows(D, 0, V, 32 * wave, lane);
-        else dp = X::rows_by(D, 0, v, lane);
-        soften(p, lse, c, OWN && diagonal, lane);
-        X::columns_by(D, 0, p, dv, lane);
-        turn(p, dp, delta, OWN && diagonal, lane);
-        X::columns_by(Q, 0, p, dk, lane);
+        floatx16 p = X::rows_by(Q, r0, k, lane), dp;
+        if constexpr (V_LDS) dp = X::rows_by_rows(D, r0, V, 32 * wave, lane);
+        else dp = X::rows_by(D, r0, v, lane);
+        soften(p, lse + r0, c, OWN && diagonal, lane);
+        X::columns_by(D, r0, p, dv, lane);
+        turn(p, dp, delta + r0, OWN && diagonal, lane);
+        X::columns_by(Q, r0, p, dk, lane);
     }
 };
 
-template <typename T, int DC>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const AttnArgs a) {
+template <typename T, int DC, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const AttnArgs a) {
     using G = Grads<T, DC>;
-    using X = typename G::X;
-    using Y = HeadTile<T, DC, kAttnRows>;
+    constexpr int KEYS = 32 * WAVES, ROWS = 8 * WAVES, N = 64 * WAVES;
+    using X = HeadTile<T, DC, ROWS>;
+    using Y = HeadTile<T, DC, KEYS>;
     __shared__ alignas(16) char qa[X::BYTES];
     __shared__ alignas(16) char qb[X::BYTES];
     __shared__ alignas(16) char da[X::BYTES];
     __shared__ alignas(16) char db[X::BYTES];
     __shared__ alignas(16) char vs[G::V_LDS ? Y::BYTES : 16];
-    __shared__ alignas(16) float ra[2][32];   // lse in log2 units, delta
-    __shared__ alignas(16) float rb[2][32];
+    __shared__ alignas(16) float ra[2][ROWS];   // lse in log2 units, delta
+    __shared__ alignas(16) float rb[2][ROWS];
     RowBlock w;
     const uint32_t split = blockIdx.x % a.splits;
-    if (!locate_rows<kAttnRows, false>(a, a.kv_heads, blockIdx.x / a.splits, w)) return;
+    if (!locate_rows<KEYS, false>(a, a.kv_heads, blockIdx.x / a.splits, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = a.heads / a.kv_heads / a.splits, head0 = (w.head * a.splits + split) * group;
     const int row_bytes = a.dim * X::ES;
@@ -253,28 +254,33 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const At
     const bool active = k0 < w.len;
 
     G grads;
-    const TileLoad<X> load_q(head_rows(a.q, w, head0, row_bytes), tid);
-    const TileLoad<X> load_d(head_rows(a.dout, w, head0, row_bytes), tid);
-    // Lanes i and 32 + i of the first wave bring lse and delta of row i.  Without divergent branches, here and in all that
+    const TileLoad<X, N> load_q(head_rows(a.q, w, head0, row_bytes), tid);
+    const TileLoad<X, N> load_d(head_rows(a.dout, w, head0, row_bytes), tid);
+    // The first wave brings lse and delta of the tile's rows.  Without divergent branches, here and in all that
     // runs at the full number of registers: a compiler that has none to spare may put the copies that it splits
     // values with before the execution mask is whole again.
-    auto load = [&](int h, int64_t r0, char* Q, char* D, float (&rows)[2][32]) __attribute__((always_inline)) {
-        TileLoad<X> lq = load_q, ld = load_d;
+    auto load = [&](int h, int64_t r0, char* Q, char* D, float (&rows)[2][ROWS]) __attribute__((always_inline)) {
+        TileLoad<X, N> lq = load_q, ld = load_d;
         lq.src.p += h * a.q.head;
         ld.src.p += h * a.dout.head;
         lq(Q, r0, w.len, wave);
         ld(D, r0, w.len, wave);
         if (wave == 0) {
             const int64_t at = token_row(a, w, head0 + h) + r0;
-            const int left = (int)(w.len - r0 < 32 ? w.len - r0 : 32), row = lane & 31;
+            const int left = (int)(w.len - r0 < ROWS ? w.len - r0 : ROWS), row = lane % ROWS;
             const float e = bits_to_f32(buffer_load_bits(make_rsrc(a.lse + at, left * 4), row * 4, 0.f)) * kLog2e;
             const float d = bits_to_f32(buffer_load_bits(make_rsrc(a.delta + at, left * 4), row * 4, 0.f));
             // rows that are not there: probabilities of 0
-            rows[lane >> 5][row] = lane >= 32 ? d : row < left ? e : 1e30f;
+            if constexpr (ROWS == 32) {
+                rows[lane >> 5][row] = lane >= 32 ? d : row < left ? e : 1e30f;
+            } else {
+                rows[0][row] = row < left ? e : 1e30f;
+                rows[1][row] = d;
+            }
         }
     };
     if constexpr (G::V_LDS) {
-        const TileLoad<Y> load_v(head_rows(a.v, w, w.head, row_bytes), tid);
+        const TileLoad<Y, N> load_v(head_rows(a.v, w, w.head, row_bytes), tid);
         load_v(vs, w.r0, w.len, wave);
     } else {
         load_rows<X>(grads.v, head_rows(a.v, w, w.head, row_bytes), k0, w.len, lane);
@@ -288,12 +294,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const At
         int h = 0;
         int64_t r0 = from;   // the tile at hand
         load(0, r0, qa, da, ra);
-        auto turn = [&](const char* Q, const char* D, const float (&rows)[2][32], char* next_q, char* next_d,
-                        float (&next_rows)[2][32]) __attribute__((always_inline)) {
+        auto turn = [&](const char* Q, const char* D, const float (&rows)[2][ROWS], char* next_q, char* next_d,
+                        float (&next_rows)[2][ROWS]) __attribute__((always_inline)) {
             tiles_ready();
-            const bool more = r0 + 32 < to;
+            const bool more = r0 + ROWS < to;
             const int64_t at = r0;
-            r0 = more ? r0 + 32 : from;
+            r0 = more ? r0 + ROWS : from;
             h += more ? 0 : 1;
             if (h < group) load(h, r0, next_q, next_d, next_rows);
             work(at, Q, D, rows);
@@ -306,12 +312,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const At
         }
         tiles_ready();
     };
-    const int64_t own = w.len < w.r0 + kAttnRows ? w.len : w.r0 + kAttnRows;
-    run(w.r0, own, [&](int64_t r0, const char* Q, const char* D, const float (&rows)[2][32]) __attribute__((always_inline)) {
-        if (active && r0 >= k0) grads.template add<true>(Q, D, vs, rows[0], rows[1], c, r0 == k0, wave, lane);
+    const int64_t own = w.len < w.r0 + KEYS ? w.len : w.r0 + KEYS;
+    run(w.r0, own, [&](int64_t r0, const char* Q, const char* D, const float (&rows)[2][ROWS]) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (int n = 0; n < ROWS; n += 32)
+            if (active && r0 + n >= k0) grads.template add<true>(Q, D, vs, rows[0], rows[1], n, c, r0 + n == k0, wave, lane);
     });
-    run(own, w.len, [&](int64_t, const char* Q, const char* D, const float (&rows)[2][32]) __attribute__((always_inline)) {
-        grads.template add<false>(Q, D, vs, rows[0], rows[1], c, false, wave, lane);
+    run(own, w.len, [&](int64_t, const char* Q, const char* D, const float (&rows)[2][ROWS]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < ROWS; n += 32) grads.template add<false>(Q, D, vs, rows[0], rows[1], n, c, false, wave, lane);
     });
     if (!active) return;
     store_grads<T>(a, w, split, grads.dk, grads.dv, k0, lane);
@@ -411,8 +420,10 @@ hipError_t launch_dim(AttnArgs a, hipStream_t s) {
     else attn_dq<T, DC><<<rows, 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    a.paired = sizeof(T) == 2 && !a.kwide;
     if (a.kfew) attn_dkv_few<T, DC><<<keys, 256, 0, s>>>(a);
-    else attn_dkv<T, DC><<<keys, 256, 0, s>>>(a);
+    else if (!a.kwide) attn_dkv<T, DC, 4><<<keys, 256, 0, s>>>(a);
+    else if constexpr (Grads<T, DC>::V_LDS) attn_dkv<T, DC, 8><<<keys, 512, 0, s>>>(a);
     const hipError_t k = hipGetLastError();
     if (k != hipSuccess || a.splits == 1) return k;
     const int64_t quads = 2 * (a.cu ? a.L : a.b * a.L) * a.kv_heads * (a.dim / 4);

@@ -176,9 +176,13 @@ constexpr int64_t kFewBlocks = 256, kFewKeyBlocks = 256, kFewKeyBlocks32 = 512;
 // of 128 758, 577 and 638 us, 4 x 2048, 32/8 heads 733, 586 and 653 us, 16 x 512, 32/8 heads 240, 269 and 330 us.  Blocks of
 // 32 keys, for 64, 128 and 256: 2048 x 8/2 heads 113, 93 and 92 us, fp32 482, 345 and 344.
 constexpr int64_t kSplitBlocks = 1024, kSplitFew = 128;
+// dk and dv of long sequences in bf16, heads over 64 elements: 8 waves with 256 keys share tiles of 64 rows instead of 4
+// waves with 128 tiles of 32, half as many barriers and loads (8 x 2048, 32/8 heads of 128, with dq: 1108 -> 1056 us, 8 x
+// 1024 408 -> 383; but 16 x 768, 16 heads 245 -> 258, 32 x 300 282 -> 306, since a last block is half empty on average).
+constexpr int64_t kWideLength = 1024;
 struct KeyPlan {
     int splits = 1;
-    bool few = false;
+    bool few = false, wide = false;
 };
 int64_t full_blocks(const m3_attn_dims* d, bool packed) {
     return row_blocks(d, packed, m3::kAttnRows) - (packed ? d->batch / 2 : 0);
@@ -200,6 +204,8 @@ KeyPlan plan_keys(const m3_attn_dims* d, bool packed) {
         p.few = n <= kFewKeyBlocks32;
     }
     if (p.few) p.splits = split(kSplitFew);
+    const int64_t length = packed ? d->seqlen / std::max<int64_t>(1, d->batch) : d->seqlen;
+    p.wide = !p.few && d->io == M3_BF16 && d->head_dim > 64 && length >= kWideLength;
     return p;
 }
 
@@ -221,8 +227,8 @@ m3_status check_attn(const m3_attn_dims* d, bool packed) {
     M3_TRY(check_counts(d->batch, d->seqlen));
     return check_groups(row_blocks(d, packed, m3::kAttnRows), d->heads, 1);
 }
-uint32_t blocks_of(const m3_attn_dims* d, bool packed, bool few) {   // of the batch, dense: of a sequence
-    const int64_t n = row_blocks(d, packed, few ? m3::kAttnFew : m3::kAttnRows);
+uint32_t blocks_of(const m3_attn_dims* d, bool packed, int64_t R) {   // of the batch, dense: of a sequence
+    const int64_t n = row_blocks(d, packed, R);
     return (uint32_t)(packed || d->batch == 0 ? n : n / d->batch);
 }
 m3_status plan_attn(Attn* p, const m3_attn_dims* d, const int32_t* cu, const void* q, const void* k, const void* v,
@@ -251,8 +257,10 @@ m3_status plan_attn(Attn* p, const m3_attn_dims* d, const int32_t* cu, const voi
     a.few = full_blocks(d, packed) * d->heads <= kFewBlocks;
     a.kfew = keys.few;
     a.splits = keys.splits;
-    a.blocks = blocks_of(d, packed, a.few);
-    a.kblocks = blocks_of(d, packed, a.kfew);
+    // a tile of kAttnWide values is addressed with 31 bits
+    a.kwide = keys.wide && p->v.s[1] < kMaxTokenBytes / 2;
+    a.blocks = blocks_of(d, packed, a.few ? m3::kAttnFew : m3::kAttnRows);
+    a.kblocks = blocks_of(d, packed, a.kfew ? m3::kAttnFew : a.kwide ? m3::kAttnWide : m3::kAttnRows);
     return M3_OK;
 }
 // delta, then the parts of dk and dv

@@ -11,6 +11,7 @@ namespace m3 {
 
 // ------------------------------------------------------------------------- whole prompts
 constexpr int kAttnRows = 128;        // query rows (backward: keys) of a workgroup, 32 to a wave
+constexpr int kAttnWide = 256;        // keys of a workgroup of 8 waves
 constexpr int kAttnFew = 32;          // the same where the other axis is split over the waves
 constexpr int64_t kAttnMaxDim = 128;  // elements of a head
 
@@ -31,7 +32,7 @@ struct AttnArgs {
     int heads, kv_heads, dim;
     float scale;
     uint32_t blocks, kblocks;    // blocks of query rows and of keys (packed: as many as there can be)
-    int few, kfew;               // they are kAttnFew rows, not kAttnRows
+    int few, kfew, kwide;        // they are kAttnFew rows (kwide: kAttnWide), not kAttnRows
     int paired;                  // two workgroups to a compute unit: paired_item's order
     int splits;                  // backward: parts that the heads of a group are split into for dk and dv
     float* part;                 // splits > 1: dk, then dv, of each part, [2, splits, tokens, kv_heads, D]

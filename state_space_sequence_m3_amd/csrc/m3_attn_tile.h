@@ -215,14 +215,14 @@ __device__ __forceinline__ int64_t token_row(const AttnArgs& a, const RowBlock& 
     return a.cu ? head * a.L + w.start : (w.seq * a.heads + head) * a.L;
 }
 
-// A tile from global memory straight into LDS, by 256 threads.  Lanes fill consecutive chunks of LDS, so each
+// A tile from global memory straight into LDS, by N threads.  Lanes fill consecutive chunks of LDS, so each
 // asks for the chunk that swz puts there; what the descriptor does not cover arrives as zero.  Buffers that are
 // filled while others are read have to be arrays of their own: the compiler then knows that reads need not wait for
 // the fill.  A wave knows of its own loads only: tiles_ready lets each wait for its own and then for the others.
 typedef __attribute__((address_space(3))) void lds_void;
-template <typename X>
+template <typename X, int N = 256>
 struct TileLoad {
-    static constexpr int STEP = 256 / X::CPR;   // rows that one load of all threads covers
+    static constexpr int STEP = N / X::CPR;   // rows that one load of all threads covers
     RowSource src;
     uint32_t off;
     __device__ __forceinline__ TileLoad(const RowSource& s, int tid) : src(s) {
@@ -233,8 +233,8 @@ struct TileLoad {
     __device__ __forceinline__ void operator()(char* tile, int64_t r0, int64_t len, int wave) const {
         const rsrc_t r = src.rows(r0, len, X::ROWS);
 #pragma unroll
-        for (int i = 0; i < X::NLD; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(tile + (i * 4 + wave) * 1024), 16,
+        for (int i = 0; i < X::BYTES / 16 / N; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(tile + (i * (N / 64) + wave) * 1024), 16,
                                                      (int)(off + (uint32_t)(i * STEP) * src.token), 0, 0, 0);
     }
 };

@@ -357,6 +357,24 @@ def test_groups_split_over_workgroups(io, hq, hk, d):
         assert_close(g[key].flatten(0, 1), ref[name], ref["tol"][name], name)
 
 
+@pytest.mark.parametrize("hq,hk,d,lens", [(36, 36, 128, [1100]), (40, 40, 72, [1500, 600, 1024]), (24, 12, 128, [1024, 1290]),
+                                          (33, 33, 96, [1025])])
+def test_long_sequences_of_many_heads(hq, hk, d, lens):
+    """dk and dv by workgroups of 256 keys."""
+    q, k, v, dout = draw(sum(lens), hq, hk, d, torch.bfloat16, d)
+    if len(lens) > 1:
+        check_packed(q, k, v, dout, lens)
+        return
+    ref = attn_ref.prompt(q, k, v, lens, None, dout)
+    x = [t.to(DEV).unsqueeze(0) for t in (q, k, v, dout)]
+    o, lse = m3attn.m3_attention(*x[:3], save_lse=True)
+    g = m3attn.m3_attention_backward(*x[:3], o, lse, x[3])
+    torch.cuda.synchronize()
+    assert_close(o[0], ref["o"], ref["tol"]["o"], "o")
+    for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        assert_close(g[key][0], ref[name], ref["tol"][name], name)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 def test_later_tokens_do_not_reach_a_row_of_many_heads(io, bad):
