@@ -9,6 +9,9 @@
 // the keys in an order that makes a lane's probabilities those of 8 (fp32: 4) consecutive keys: the right operand of the
 // product with the values, whose left operand is the values' rows as they are loaded, 16 lanes to a row, with (bf16) an
 // 8 x 8 transpose inside each lane.  Nothing goes through LDS but the join of the waves.
+//
+// 32/8 heads of 128 bf16: 64 sequences of up to 8192 178 us and 6.5 for the join (5.5 TB/s over the call); one of 32768
+// 24.2 and 4.4 us.
 #include "m3_mma.h"
 #include "m3_pages.h"
 
