@@ -63,7 +63,9 @@ typedef struct {
  *
  * For: the forward pass of training, prefill.  Scores, maxima, sums and o are fp32; with bf16 io the
  * probabilities are rounded to bf16 for their product with v (relative to the largest score of their row so
- * far, within 2^8).  What later tokens hold, infinities and NaN included, does not reach a row.
+ * far, within 2^8).  q . k and scale log2(e) q . k may be any fp32 numbers; beyond them they are infinite.  A row whose
+ * scores are all -infinity is NaN (0 / 0).  What later tokens hold, infinities and NaN included, does not reach a
+ * row.
  *
  *   q        [b, L, Hq, D] or [T, Hq, D] io;  k, v with Hkv heads            required
  *   o        like q                                                         required
@@ -80,7 +82,8 @@ m3_status m3_attention(const m3_attn_dims* dims, const int32_t* cu_seqlens, cons
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
  *
  * dk and dv are summed over the query heads of their group.  With bf16 io, p and ds are rounded to bf16 for
- * their products; sums are fp32.  An infinity or NaN in a row of an input makes gradients of up to 31 other rows
+ * their products; sums are fp32.  p is off by |lse| 2^-23 of itself, as much as lse is: it has no digits where scores
+ * reach 2^24, and from 2^30 on gradients may not be finite.  An infinity or NaN in a row of an input makes gradients of up to 31 other rows
  * of its block of 32 tokens NaN beside those that the formulas make so.
  *
  *   o, lse     what m3_attention wrote for the same dims, offsets and inputs      required

@@ -6,14 +6,15 @@
 // between the wave's halves, the probabilities are the right operand of the product with the values as they lie in
 // their registers, and rescaling a row is one factor per lane.
 #include "m3_attn_tile.h"
+#include "m3_softmax.h"
 
 namespace m3 {
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-// The running maximum (in log2 units) is moved only when a score exceeds it by more: until then
-// probabilities are up to 2^8 larger, which costs no digits.
-constexpr float kSlack = 8.f;
+// The running maximum is moved only when a score exceeds it by more (in log2 units): until then probabilities are up to
+// 2^8 larger, which costs no digits.  Less than half a unit in the last place of a maximum of kFar, so that it is
+// nothing there.
+constexpr float kSlack = 7.9f;
 
 // One wave's 32 query rows.
 template <typename T, int DC>
@@ -21,34 +22,39 @@ struct Rows {
     using X = HeadTile<T, DC>;
     uint4 q[X::SG];
     floatx16 o[X::DB] = {};
-    float top = -1e37f, sum = 0.f;   // log2 units; this half's part of the sum
+    float top = kLowest, sum = 0.f;   // this half's part of the sum
+    float by;                         // score_factor of top
+
+    __device__ __forceinline__ explicit Rows(float c) : by(score_factor(kLowest, c)) {}
 
     // makes room for scores against 32 N keys: the running maximum is their bound within kSlack
     template <int N>
-    __device__ __forceinline__ void raise(const floatx16 (&s)[N], float c) {
+    __device__ __forceinline__ void raise(const floatx16 (&s)[N], float c, float slack) {
         float m = s[0][0];
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int i = 0; i < 16; ++i) m = fmaxf(m, s[n][i]);
-        m = halves_max(m) * c;
-        if (__ballot(m > top + kSlack)) {
-            const float to = fmaxf(top, m), f = fast_exp2(top - to);
+        m = halves_max(m);
+        if (__ballot(m > top + slack)) {
+            const float to = fmaxf(top, m), f = top_moved(top, to, c);
 #pragma unroll
             for (int db = 0; db < X::DB; ++db) o[db] *= f;
             sum *= f;
             top = to;
+            by = score_factor(to, c);
         }
     }
     // they become probabilities
     template <int N>
-    __device__ __forceinline__ void soften(floatx16 (&s)[N], float c) {
+    __device__ __forceinline__ void soften(floatx16 (&s)[N]) {
+        const float base = top * by;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             float part = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[n][i] = fast_exp2(fmaf(s[n][i], c, -top));
+                s[n][i] = fast_exp2(fmaf(s[n][i], by, -base));
                 part += s[n][i];
             }
             sum += part;
@@ -56,18 +62,19 @@ struct Rows {
     }
 
     // 32 keys at tile row r0 that are the rows' own tokens (`diagonal`), or earlier ones
-    __device__ __forceinline__ void add(const char* K, const char* V, int r0, float c, bool diagonal, int lane) {
+    __device__ __forceinline__ void add(const char* K, const char* V, int r0, float c, float slack, bool diagonal, int lane) {
         floatx16 s[1] = {X::rows_by(K, r0, q, lane)};
-        add_scores(s, V, r0, c, diagonal, lane);
+        add_scores(s, V, r0, c, slack, diagonal, lane);
     }
-    __device__ __forceinline__ void add_scores(floatx16 (&s)[1], const char* V, int r0, float c, bool diagonal, int lane) {
+    __device__ __forceinline__ void add_scores(floatx16 (&s)[1], const char* V, int r0, float c, float slack, bool diagonal,
+                                               int lane) {
         const int half = lane >> 5, row = lane & 31;
         if (diagonal) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[0][i] = acc_row(i, half) > row ? -INFINITY : s[0][i];
         }
-        raise(s, c);
-        soften(s, c);
+        raise(s, c, slack);
+        soften(s);
         if (diagonal && any_odd(V, r0, lane)) {
             // key by key, each for the rows that see it
 #pragma unroll 1
@@ -89,11 +96,11 @@ struct Rows {
         }
     }
 
-    __device__ __forceinline__ void finish(const AttnArgs& a, const RowBlock& w, int64_t q0, int row_bytes, int lane) {
+    __device__ __forceinline__ void finish(const AttnArgs& a, const RowBlock& w, int64_t q0, int row_bytes, float c, int lane) {
         const float all = halves_sum(sum);
         store_columns<T, X::DB>(o, 1.f / all, head_rows(a.o, w, w.head, row_bytes), q0, w.len, lane);
         if (a.lse && lane < 32 && q0 + lane < w.len)
-            a.lse[token_row(a, w, w.head) + q0 + lane] = (top + __builtin_amdgcn_logf(all)) * kLn2;
+            a.lse[token_row(a, w, w.head) + q0 + lane] = log_sum(top, all, c);
     }
 
     // A probability of 0 times an infinity or NaN in a later token's value would be NaN: the values of the one block
@@ -142,9 +149,9 @@ __global__ __launch_bounds__(256, PER_CU) void attn_fwd(const AttnArgs a) {
     load_v(v0, 0, w.len, wave);
     if (ntiles > 1) load_k(k1, X::ROWS, w.len, wave);
 
-    Rows<T, DC> rows;
+    const float c = a.scale * kLog2e, slack = kSlack / c;
+    Rows<T, DC> rows(c);
     load_rows<X>(rows.q, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
-    const float c = a.scale * kLog2e;
 
     // Tile t's keys are in k0 (t even) or k1, its values in v0 or v1.  Scores of tile t + 1 are computed while tile
     // t's become probabilities, keys are loaded two tiles ahead and values one.
@@ -158,12 +165,12 @@ __global__ __launch_bounds__(256, PER_CU) void attn_fwd(const AttnArgs a) {
         tiles_ready();
         if (t + 2 < ntiles) load_k(old_k, (int64_t)(t + 2) * X::ROWS, w.len, wave);
         load_v(old_v, (int64_t)(t + 1) * X::ROWS, w.len, wave);
-        rows.raise(s, c);
+        rows.raise(s, c, slack);
         // a wave with products to issue goes first: 343 -> 323 us at b8 L2048, 32/8 heads of 128 bf16
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int n = 0; n < X::SUB; ++n) ahead[n] = X::rows_by(K, 32 * n, rows.q, lane);
-        rows.soften(s, c);
+        rows.soften(s);
         // (no pragma: unrolled at once, this takes registers that are not there)
         for (int n = 0; n < X::SUB; ++n) X::columns_by(V, 32 * n, s[n], rows.o, lane);
         __builtin_amdgcn_s_setprio(0);
@@ -185,10 +192,10 @@ __global__ __launch_bounds__(256, PER_CU) void attn_fwd(const AttnArgs a) {
 #pragma unroll 1
         for (int r0 = 0; r0 < X::ROWS; r0 += 32) {
             const int64_t at = (int64_t)t * X::ROWS + r0;
-            if (active && at <= q0) rows.add(odd ? k1 : k0, odd ? v1 : v0, r0, c, at == q0, lane);
+            if (active && at <= q0) rows.add(odd ? k1 : k0, odd ? v1 : v0, r0, c, slack, at == q0, lane);
         }
     }
-    if (active) rows.finish(a, w, q0, row_bytes, lane);
+    if (active) rows.finish(a, w, q0, row_bytes, c, lane);
 }
 
 // For few rows: a workgroup takes 32 query rows, and its waves the four parts of 32 keys of each tile of 128, with a
@@ -208,11 +215,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd_few(cons
     const TileLoad<X> load_k(head_rows(a.k, w, kv_head, row_bytes), tid);
     const TileLoad<X> load_v(head_rows(a.v, w, kv_head, row_bytes), tid);
     const int64_t q0 = w.r0, kend = w.len < q0 + kAttnFew ? w.len : q0 + kAttnFew;
-    R rows;
+    const float c = a.scale * kLog2e, slack = kSlack / c;
+    R rows(c);
     load_rows<typename R::X>(rows.q, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
     load_k(ks, 0, kend, wave);
     load_v(vs, 0, kend, wave);
-    const float c = a.scale * kLog2e;
     for (int64_t t = 0; t < kend; t += 128) {
         const int64_t k0 = t + 32 * wave;
         const bool mine = k0 < kend, more = t + 128 < kend;
@@ -221,7 +228,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd_few(cons
         if (mine) s[0] = R::X::rows_by(ks, 32 * wave, rows.q, lane);
         tiles_ready();
         if (more) load_k(ks, t + 128, kend, wave);
-        if (mine) rows.add_scores(s, vs, 32 * wave, c, k0 == q0, lane);
+        if (mine) rows.add_scores(s, vs, 32 * wave, c, slack, k0 == q0, lane);
         __syncthreads();
         if (more) load_v(vs, t + 128, kend, wave);
     }
@@ -238,7 +245,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd_few(cons
                 for (int i = 0; i < 16; ++i) at[(db * 16 + i) * 64] = rows.o[db][i];
         },
         [&](float* at) __attribute__((always_inline)) {
-            const float to = fmaxf(rows.top, end[0]), f = fast_exp2(rows.top - to), g = fast_exp2(end[0] - to);
+            const float to = fmaxf(rows.top, end[0]), f = top_moved(rows.top, to, c), g = top_moved(end[0], to, c);
             rows.top = to;
             rows.sum = rows.sum * f + end[64] * g;
 #pragma unroll
@@ -246,7 +253,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd_few(cons
 #pragma unroll
                 for (int i = 0; i < 16; ++i) rows.o[db][i] = rows.o[db][i] * f + at[(db * 16 + i) * 64] * g;
         });
-    if (wave == 0) rows.finish(a, w, q0, row_bytes, lane);
+    if (wave == 0) rows.finish(a, w, q0, row_bytes, c, lane);
 }
 
 // Two workgroups to a compute unit, heavy with light ones (paired_item).  Fp32 heads of up to 96 elements fit too, but

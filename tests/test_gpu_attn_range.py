@@ -1,0 +1,73 @@
+"""Scores of any finite size, in m3_attention: up to the ends of fp32's range, all of a row far below or
+above zero, equal and unequal ones.
+
+Inputs make every score exact: queries have one element that is not zero, a power of two, and keys numbers of few
+digits there, so the bounds hold no errors of scores.  A probability exp(s - max) is off by 2 |s - max| U32 (scale log2 e, and
+its product with the score) and 16 U32 for the exponential; beyond differences of 200 it is zero in fp32."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from block_ref import U32, assert_close, half_step
+from state_space_sequence_m3_amd import m3attn
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+IO = {"f32": torch.float32, "bf16": torch.bfloat16}
+SIZES = [2.0 ** e for e in (20, 27, 28, 29, 31, 33, 40, 100, 126)]
+
+
+def exact_inputs(n, hq, hk, d, io, size, sign, seed, scale):
+    """q [n, Hq, D], k, v [n, Hkv, D]: scores are sign * size, or that times 127 / 128, key by key at random, and with a
+    negative sign the first half of the keys all equal; the least size has up to 3 more."""
+    g = torch.Generator().manual_seed(seed)
+    q, k = torch.zeros(n, hq, d), torch.zeros(n, hk, d)
+    less = torch.rand(n, hk, generator=g) < 0.5
+    if sign < 0:
+        less[:n // 2] = False
+    q[:, :, 3] = 2.0 ** 60
+    k[:, :, 3] = torch.where(less, 127.0 / 128, 1.0) * sign * size / scale / 2.0 ** 60
+    if size == SIZES[0]:
+        q[:, :, 5], k[:, :, 5] = 1.0, torch.randint(0, 4, (n, hk), generator=g) / scale
+    v = torch.randn(n, hk, d, generator=g)
+    q, k, v = q.to(io), k.to(io), v.to(io)
+    at_first = (q[0, 0].double() @ k[0, 0].double()) * scale - sign * size * (127 / 128 if less[0, 0] else 1)
+    assert 0 <= at_first <= (3 if size == SIZES[0] else 0)
+    return q, k, v
+
+
+def attend(q, k, v, scale, seen, io):
+    """One head in 64 bits: o, lse and their bounds."""
+    n = k.shape[0]
+    s = torch.where(seen, scale * (q.double() @ k.double().T), torch.tensor(float("-inf")).double())
+    top = s.amax(1, keepdim=True)
+    p = torch.exp(s - top)
+    rel = ((top - s).clamp(max=200) * 2 + 16 + n) * U32
+    total = p.sum(1, keepdim=True)
+    o = p @ v.double() / total
+    h = half_step(io) if io is torch.bfloat16 else 0.0
+    tol = (p * (h + rel)) @ v.double().abs() / total + o.abs() * (p * rel).sum(1, keepdim=True) / total
+    lse = (top + total.log()).squeeze(1)
+    return o, tol, lse, 4 * U32 * lse.abs() + 32 * U32 + (p * rel).sum(1) / total.squeeze(1)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("hq,hk,d,n", [(2, 1, 64, 300), (130, 2, 32, 300), (130, 2, 128, 200)])
+def test_prompt_scores_far_from_zero(io, sign, hq, hk, d, n):
+    io = IO[io]
+    for i, size in enumerate(SIZES):
+        for scale in (1.0, 2.0 ** -5):
+            if size / scale > 2.0 ** 126:
+                continue
+            q, k, v = exact_inputs(n, hq, hk, d, io, size, sign, i, scale)
+            o, lse = m3attn.m3_attention(*(x.to(DEV).unsqueeze(0) for x in (q, k, v)), scale=scale, save_lse=True)
+            torch.cuda.synchronize()
+            seen = torch.ones(n, n, dtype=torch.bool).tril()
+            for h in sorted({0, hq // 2, hq - 1}):
+                j = h // (hq // hk)
+                want, tol, wl, tl = attend(q[:, h], k[:, j], v[:, j], scale, seen, io)
+                assert_close(o[0, :, h], want, tol, "o %g %g" % (size, scale))
+                assert_close(lse[0, h], wl, tl, "lse %g %g" % (size, scale))
