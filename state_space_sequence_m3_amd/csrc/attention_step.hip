@@ -14,12 +14,12 @@
 // 24.2 and 4.4 us.
 #include "m3_mma.h"
 #include "m3_pages.h"
+#include "m3_softmax.h"
 
 namespace m3 {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int64_t length_of(const StepArgs& a, int64_t s) {
     const int64_t n = a.lens[s], most = a.pages.table_w * (int64_t)a.pages.size;
@@ -219,8 +219,8 @@ struct Piece {
     }
 };
 
-// Partial results: of each part (piece + sequence) the heads one after another, {maximum (log2 units), sum, D unscaled
-// elements} each.
+// Partial results: of each part (piece + sequence) the heads one after another, {largest score, sum, D unscaled elements}
+// each.
 __device__ __forceinline__ int64_t part_row(const StepArgs& a, int64_t part, int head) {
     return (part * a.heads + head) * (2 + a.dim);
 }
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
             if (in_group < group && at < a.dim * P::ES) q[j] = *(const uint4*)(a.q.p + s * a.q.batch + head * a.q.head + at);
         }
         floatx4 acc[VE] = {};
-        float top = -1e37f, sum = 0.f;
+        float top = kLowest, sum = 0.f;
 
         // keys and values are loaded a tile ahead, and looked up two
         P now, next;
@@ -276,17 +276,22 @@ __global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
 #pragma unroll
             for (int i = 1; i < 4 * P::BLK; ++i) m = fmaxf(m, p[i]);
             m = fmaxf(m, __shfl_xor(m, 16, 64));
-            m = fmaxf(m, __shfl_xor(m, 32, 64)) * c;
+            m = fmaxf(m, __shfl_xor(m, 32, 64));
             if (__ballot(m > top)) {
-                const float to = fmaxf(top, m), f = fast_exp2(top - to);
+                const float to = fmaxf(top, m), f = top_moved(top, to, c);
 #pragma unroll
                 for (int j = 0; j < VE; ++j) acc[j] *= f;
                 sum *= f;
                 top = to;
             }
+            float by = c, base = top * c;
+            if (__ballot(!(fabsf(base) < kFar))) {
+                by = score_factor(top, c);
+                base = top * by;
+            }
 #pragma unroll
             for (int i = 0; i < 4 * P::BLK; ++i) {
-                p[i] = fast_exp2(fmaf(p[i], c, -top));
+                p[i] = fast_exp2(fmaf(p[i], by, -base));
                 sum += p[i];
             }
             now.values(p, acc);
@@ -313,14 +318,14 @@ __global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
             float n = 0.f, o = 0.f;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const float f = fast_exp2(tops[w][h] - t);
+                const float f = top_moved(tops[w][h], t, c);
                 n = fmaf(f, sums[w][h], n);
                 o = fmaf(f, outs[w][h][d], o);
             }
             if (whole) {
                 // nothing to attend to: zeros
-                *(T*)(a.o.p + s * a.o.batch + at * a.o.head + d * P::ES) = from_f32<T>(t > -1e37f || n != 0.f ? o / n : 0.f);
-                if (a.lse && d == 0) a.lse[s * a.heads + at] = (t + __builtin_amdgcn_logf(n)) * kLn2;
+                *(T*)(a.o.p + s * a.o.batch + at * a.o.head + d * P::ES) = from_f32<T>(n != 0.f ? o / n : 0.f);
+                if (a.lse && d == 0) a.lse[s * a.heads + at] = log_sum(t, n, c);
             } else {
                 float* part = a.part + part_row(a, item + s, at);
                 part[2 + d] = o;
@@ -347,7 +352,8 @@ __global__ __launch_bounds__(256) void attn_step_join(const StepArgs a) {
     const float* part = a.part + part_row(a, item + s, head);
     const int64_t next = (int64_t)a.heads * (2 + a.dim);   // from a part to the next one
     const int tid = threadIdx.x, group = tid >> 4, d0 = (tid & 15) * 8;
-    float o[8] = {}, top = -1e37f, sum = 0.f;
+    const float c = a.scale * kLog2e;
+    float o[8] = {}, top = kLowest, sum = 0.f;
     for (int64_t i = group; i < n; i += 16) {
         const float* p = part + i * next;
         const float t = p[0], w = p[1];
@@ -359,7 +365,7 @@ __global__ __launch_bounds__(256) void attn_step_join(const StepArgs a) {
                 x[j] = u.x, x[j + 1] = u.y;
             }
         }
-        const float to = fmaxf(top, t), f = fast_exp2(top - to), g = fast_exp2(t - to);
+        const float to = fmaxf(top, t), f = top_moved(top, to, c), g = top_moved(t, to, c);
         top = to;
         sum = sum * f + w * g;
 #pragma unroll
@@ -378,14 +384,14 @@ __global__ __launch_bounds__(256) void attn_step_join(const StepArgs a) {
         float v = 0.f, w = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float f = fast_exp2(tops[i] - t);
+            const float f = top_moved(tops[i], t, c);
             w = fmaf(f, sums[i], w);
             v = fmaf(f, outs[i][tid], v);
         }
         // nothing to attend to: zeros
         *(T*)(a.o.p + s * a.o.batch + head * a.o.head + tid * (int)sizeof(T)) =
-            from_f32<T>(t > -1e37f || w != 0.f ? v / w : 0.f);
-        if (a.lse && tid == 0) a.lse[s * a.heads + head] = (t + __builtin_amdgcn_logf(w)) * kLn2;
+            from_f32<T>(w != 0.f ? v / w : 0.f);
+        if (a.lse && tid == 0) a.lse[s * a.heads + head] = log_sum(t, w, c);
     }
 }
 

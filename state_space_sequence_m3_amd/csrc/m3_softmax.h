@@ -22,12 +22,12 @@ __device__ __forceinline__ float score_factor(float top, float c) {
     const int e = 40 - __builtin_amdgcn_frexp_expf(top);
     return __builtin_amdgcn_ldexpf(1.f, e < 127 ? e : 127);
 }
-// by what sums relative to a maximum `from` are multiplied for the maximum `to`, at least as large
+// By what sums relative to a maximum `from` are multiplied for the maximum `to`, at least as large.  (-infinity as `from`,
+// of nothing at all, gives 0.)
 __device__ __forceinline__ float top_moved(float from, float to, float c) {
 #pragma clang fp contract(off)
-    if (from == to) return 1.f;
-    const float a = from * c, b = to * c;
-    return fast_exp2(fabsf(a) < kFar && fabsf(b) < kFar ? a - b : (from - to) * c);
+    const float b = to * c;
+    return fast_exp2(fmaxf(fabsf(b) < kFar ? from * c - b : (from - to) * c, -INFINITY));
 }
 // log sum exp of a row's scores, from its maximum and the sum relative to it
 __device__ __forceinline__ float log_sum(float top, float sum, float c) {

@@ -1,4 +1,4 @@
-"""Scores of any finite size, in m3_attention: up to the ends of fp32's range, all of a row far below or
+"""Scores of any finite size, in m3_attention and m3_attention_step: up to the ends of fp32's range, all of a row far below or
 above zero, equal and unequal ones.
 
 Inputs make every score exact: queries have one element that is not zero, a power of two, and keys numbers of few
@@ -71,3 +71,37 @@ def test_prompt_scores_far_from_zero(io, sign, hq, hk, d, n):
                 want, tol, wl, tl = attend(q[:, h], k[:, j], v[:, j], scale, seen, io)
                 assert_close(o[0, :, h], want, tol, "o %g %g" % (size, scale))
                 assert_close(lse[0, h], wl, tl, "lse %g %g" % (size, scale))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("hq,hk,d,page,lens", [(4, 2, 64, 32, [1, 40, 700]), (3, 1, 128, 64, [5000, 130]),
+                                               (20, 1, 128, 7, [300, 3000])])
+def test_token_scores_far_from_zero(io, sign, hq, hk, d, page, lens):
+    """One piece and several, of scores that the first pieces have alone or not."""
+    io = IO[io]
+    need = [-(-n // page) for n in lens]
+    g = torch.Generator().manual_seed(1)
+    order, table, at = torch.randperm(sum(need), generator=g), torch.full((len(lens), max(need)), -1, dtype=torch.int32), 0
+    for s, n in enumerate(need):
+        table[s, :n] = order[at:at + n]
+        at += n
+    for i, size in enumerate(SIZES):
+        kc, vc = (torch.zeros(sum(need), hk, page, d, dtype=io) for _ in range(2))
+        rows = []
+        for s, n in enumerate(lens):
+            q, k, v = exact_inputs(n, hq, hk, d, io, size, sign, 10 * i + s, 1.0)
+            pos = torch.arange(n)
+            kc[table[s, pos // page].long(), :, pos % page] = k
+            vc[table[s, pos // page].long(), :, pos % page] = v
+            rows.append((q[0], k, v))
+        lse = torch.empty(len(lens), hq, device=DEV)
+        o = m3attn.m3_attention_step(torch.stack([r[0] for r in rows]).to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV),
+                                     torch.tensor(lens, dtype=torch.int32).to(DEV), scale=1.0, lse=lse)
+        torch.cuda.synchronize()
+        for s, (q, k, v) in enumerate(rows):
+            for h in (0, hq - 1):
+                j = h // (hq // hk)
+                want, tol, wl, tl = attend(q[h:h + 1], k[:, j], v[:, j], 1.0, torch.ones(1, lens[s], dtype=torch.bool), io)
+                assert_close(o[s, h], want[0], tol[0], "o %g" % size)
+                assert_close(lse[s, h:h + 1], wl, tl, "lse %g" % size)
