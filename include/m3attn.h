@@ -163,6 +163,8 @@ m3_status m3_cache_append(const m3_cache_dims* dims, const int32_t* cu_seqlens, 
  *
  *   lse = log sum_j exp(s_j),  o = sum_j exp(s_j - lse) v_j;  no position: o = 0, lse = -infinity
  *
+ * (positions whose scores are all -infinity: o is NaN, as a prompt's row, and lse = -infinity).
+ *
  * For: decoding.  Reads every page once; long sequences are cut into pieces that run at the same time.
  * Scores, sums and partial results are fp32, their range as m3_attention's; with bf16 io the probabilities are
  * rounded to bf16 for their product with v.  lens[s] past table_width * page_size counts as that.

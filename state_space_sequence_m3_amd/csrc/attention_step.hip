@@ -220,7 +220,7 @@ struct Piece {
 };
 
 // Partial results: of each part (piece + sequence) the heads one after another, {largest score, sum, D unscaled elements}
-// each.
+// each.  A largest score of -infinity: there is no position (where all score -infinity it is kLowest, and the sum 0).
 __device__ __forceinline__ int64_t part_row(const StepArgs& a, int64_t part, int head) {
     return (part * a.heads + head) * (2 + a.dim);
 }
@@ -260,6 +260,7 @@ __global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
         }
         floatx4 acc[VE] = {};
         float top = kLowest, sum = 0.f;
+        bool some = false;   // a position, for all of the wave
 
         // keys and values are loaded a tile ahead, and looked up two
         P now, next;
@@ -272,6 +273,7 @@ __global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
             ahead = far;
             float p[4 * P::BLK];
             now.scores(q, p);
+            some |= __ballot(now.there) != 0;
             float m = p[0];
 #pragma unroll
             for (int i = 1; i < 4 * P::BLK; ++i) m = fmaxf(m, p[i]);
@@ -303,7 +305,7 @@ __global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
         // the four waves' results
         __syncthreads();
         if (g == 0) {
-            tops[wave][col] = top;
+            tops[wave][col] = some ? top : -INFINITY;
             sums[wave][col] = sum;
         }
 #pragma unroll
@@ -324,7 +326,7 @@ __global__ __launch_bounds__(256, 2) void attn_step(const StepArgs a) {
             }
             if (whole) {
                 // nothing to attend to: zeros
-                *(T*)(a.o.p + s * a.o.batch + at * a.o.head + d * P::ES) = from_f32<T>(n != 0.f ? o / n : 0.f);
+                *(T*)(a.o.p + s * a.o.batch + at * a.o.head + d * P::ES) = from_f32<T>(t > -INFINITY ? o / n : 0.f);
                 if (a.lse && d == 0) a.lse[s * a.heads + at] = log_sum(t, n, c);
             } else {
                 float* part = a.part + part_row(a, item + s, at);
@@ -353,7 +355,7 @@ __global__ __launch_bounds__(256) void attn_step_join(const StepArgs a) {
     const int64_t next = (int64_t)a.heads * (2 + a.dim);   // from a part to the next one
     const int tid = threadIdx.x, group = tid >> 4, d0 = (tid & 15) * 8;
     const float c = a.scale * kLog2e;
-    float o[8] = {}, top = kLowest, sum = 0.f;
+    float o[8] = {}, top = -INFINITY, sum = 0.f;
     for (int64_t i = group; i < n; i += 16) {
         const float* p = part + i * next;
         const float t = p[0], w = p[1];
@@ -390,7 +392,7 @@ __global__ __launch_bounds__(256) void attn_step_join(const StepArgs a) {
         }
         // nothing to attend to: zeros
         *(T*)(a.o.p + s * a.o.batch + head * a.o.head + tid * (int)sizeof(T)) =
-            from_f32<T>(w != 0.f ? v / w : 0.f);
+            from_f32<T>(t > -INFINITY ? v / w : 0.f);
         if (a.lse && tid == 0) a.lse[s * a.heads + head] = log_sum(t, w, c);
     }
 }

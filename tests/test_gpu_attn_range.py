@@ -105,3 +105,33 @@ def test_token_scores_far_from_zero(io, sign, hq, hk, d, page, lens):
                 want, tol, wl, tl = attend(q[h:h + 1], k[:, j], v[:, j], 1.0, torch.ones(1, lens[s], dtype=torch.bool), io)
                 assert_close(o[s, h], want[0], tol[0], "o %g" % size)
                 assert_close(lse[s, h:h + 1], wl, tl, "lse %g" % size)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_token_scores_of_minus_infinity(io):
+    """Positions that all score -inf are 0 / 0, as a prompt's row is; positions that are not there give zeros."""
+    io, d, page, hq = IO[io], 64, 16, 4
+    g = torch.Generator().manual_seed(3)
+    kc, vc = (torch.randn(40, 1, page, d, generator=g).to(io) for _ in range(2))
+    q = torch.randn(5, hq, d, generator=g).to(io)
+    kc[:, 0, :, 0] = 0.0
+    q[:, :, 0] = 1.0
+    kc[:36, 0, :, 0] = float("-inf")
+    table = torch.stack([torch.arange(36, dtype=torch.int32)] * 5)
+    table[1, :] = -1
+    table[2, 2] = 38                      # one page of other scores
+    table[3, :20] = 50                    # no pages, then -inf
+    lens = torch.tensor([36 * page, 36 * page, 36 * page, 36 * page, 3], dtype=torch.int32)
+    lse = torch.empty(5, hq, device=DEV)
+    o = m3attn.m3_attention_step(q.to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV), lens.to(DEV), lse=lse)
+    short = m3attn.m3_attention_step(q.to(DEV), kc.to(DEV), vc.to(DEV), table[:, :1].contiguous().to(DEV), lens.to(DEV))
+    torch.cuda.synchronize()
+    for s in (0, 3, 4):
+        assert torch.isnan(o[s].float()).all() and (lse[s] == float("-inf")).all(), s
+    assert (o[1] == 0).all() and (lse[1] == float("-inf")).all()
+    assert torch.isnan(short[[0, 2, 4]].float()).all() and (short[[1, 3]] == 0).all()
+    k, v = kc[38, 0].double(), vc[38, 0].double()
+    for h in range(hq):
+        p = torch.softmax(k @ q[2, h].double() / 8, 0)
+        e = (d + 24) * U32 * 8 + half_step(io)    # of scores below 8
+        assert_close(o[2, h], p @ v, e * (p @ v.abs() + (p @ v).abs()), "o")
