@@ -294,9 +294,9 @@ m3_status plan_cache(Cache* c, const m3_cache_dims* d, const void* k, const void
     const int64_t n[3] = {d->num_pages, d->kv_heads, d->page_size};
     M3_TRY(make_area(&c->k, k, "k_cache", n, {d->k_cache.page, d->k_cache.head, d->k_cache.token}, d->head_dim, c->es, 2));
     M3_TRY(make_area(&c->v, v, "v_cache", n, {d->v_cache.page, d->v_cache.head, d->v_cache.token}, d->head_dim, c->es, 2));
+    if (d->batch * d->table_width >= kMaxSpan) return fail(M3_E_DIMS, "page_table: size out of range");
     c->table = flat(table, d->batch * d->table_width * 4, "page_table");
     c->lens = flat(lens, d->batch * 4, "lens");
-    if (d->batch * d->table_width >= kMaxSpan) return fail(M3_E_DIMS, "page_table: size out of range");
     for (const Area* a : {&c->table, &c->lens}) M3_TRY(check_aligned(*a, 4));
     m3::Pages& p = c->pages;
     p.k = (char*)const_cast<void*>(k), p.v = (char*)const_cast<void*>(v);

@@ -441,3 +441,11 @@ def test_binding_refusals():
         m3attn.m3_attention_step(q[:, 0], cache, cache, table[:1], lens)
     with pytest.raises(ValueError, match="GPU"):
         m3attn.m3_attention_step(q[:, 0], cache, cache, table, lens)
+
+
+def test_table_sizes():
+    """A page table of more bytes than 64 bits count is refused before its size is made."""
+    for batch, width in [((1 << 31) - 1, (1 << 31) - 1), ((1 << 31) - 1, 1 << 30), (1 << 20, (1 << 31) - 1)]:
+        assert APP(dims=APP.make(batch=batch, seqlen=0, table_width=width)) == m3scan.M3_E_DIMS, (batch, width)
+        assert "page_table" in m3scan.last_error()
+        assert STEP(dims=cache_dims(batch=batch, table_width=width)) == m3scan.M3_E_DIMS
