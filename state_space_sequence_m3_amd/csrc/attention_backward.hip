@@ -186,6 +186,13 @@ __device__ __forceinline__ void turn(floatx16& p, const floatx16& dp, const floa
     }
 }
 
+// The first query head of part `split` of a key head's, and their number: parts differ by at most one head.
+__device__ __forceinline__ int part_heads(const AttnArgs& a, int head, uint32_t split, int& number) {
+    const uint32_t all = a.heads / a.kv_heads, from = split * all / a.splits, to = (split + 1) * all / a.splits;
+    number = (int)(to - from);
+    return head * (int)all + (int)from;
+}
+
 // 32 keys' dk and dv, as they are or as part `split` of what is added up by another launch.
 template <typename T, int DB>
 __device__ __forceinline__ void store_grads(const AttnArgs& a, const RowBlock& w, uint32_t split, const floatx16 (&dk)[DB],
@@ -253,7 +260,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void attn_dkv(c
     const uint32_t split = blockIdx.x % a.splits;
     if (!locate_rows<KEYS, false>(a, a.kv_heads, blockIdx.x / a.splits, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int group = a.heads / a.kv_heads / a.splits, head0 = (w.head * a.splits + split) * group;
+    int group;
+    const int head0 = part_heads(a, w.head, split, group);
     const int row_bytes = a.dim * X::ES;
     const int64_t k0 = w.r0 + 32 * wave;
     const bool active = k0 < w.len;
@@ -344,7 +352,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && DC <= 64 ? 2 : 1) void attn_
     if (!locate_rows<kAttnFew, false>(a, a.kv_heads, blockIdx.x / a.splits, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, col = lane & 31;
-    const int group = a.heads / a.kv_heads / a.splits, head0 = (w.head * a.splits + split) * group;
+    int group;
+    const int head0 = part_heads(a, w.head, split, group);
     const int row_bytes = a.dim * X::ES;
     const int64_t k0 = w.r0;
     TileLoad<X> load_q(head_rows(a.q, w, head0, row_bytes), tid);

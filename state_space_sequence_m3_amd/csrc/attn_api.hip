@@ -175,6 +175,9 @@ constexpr int64_t kFewBlocks = 256, kFewKeyBlocks = 256, kFewKeyBlocks32 = 512;
 // whose parts are added up by another launch.  Bf16, with dq, parts for 512, 1024 and 2048 blocks: 2 x 2048, 64/8 heads
 // of 128 758, 577 and 638 us, 4 x 2048, 32/8 heads 733, 586 and 653 us, 16 x 512, 32/8 heads 240, 269 and 330 us.  Blocks of
 // 32 keys, for 64, 128 and 256: 2048 x 8/2 heads 113, 93 and 92 us, fp32 482, 345 and 344.
+// Parts are equal where a number of them that divides the group makes at most twice as many blocks (and 2^18 rows of parts,
+// 268 MB at 128 elements), else uneven ones for one and a half times as many.  Parts, backward in us: 16384 tokens, 28/4
+// heads of 128 2: 7558, 3: 7228, 4: 7543, 7: 6995 (but 470 MB of parts); 8192, 40/8 heads 2: 2643, 3: 2401, 5: 2418.
 constexpr int64_t kSplitBlocks = 1024, kSplitFew = 128;
 // dk and dv of long sequences in bf16, heads over 64 elements: 8 waves with 256 keys share tiles of 64 rows instead of 4
 // waves with 128 tiles of 32, half as many barriers and loads (8 x 2048, 32/8 heads of 128, with dq: 1108 -> 1056 us, 8 x
@@ -191,10 +194,11 @@ KeyPlan plan_keys(const m3_attn_dims* d, bool packed) {
     const int64_t n = full_blocks(d, packed) * d->kv_heads;
     auto split = [&](int64_t to) {
         const int64_t group = d->kv_heads * d->head_dim * 4 < kMaxTokenBytes ? d->heads / d->kv_heads : 1;
-        int64_t best = 1;
-        for (int64_t s = 2; s <= group && n * best < to; ++s)
-            if (group % s == 0) best = s;
-        return (int)best;
+        if (n < 1 || n >= to) return 1;
+        const int64_t least = std::min(group, (to + n - 1) / n);
+        for (int64_t s = least; s <= group && n * s <= 2 * to; ++s)
+            if (group % s == 0) return (int)s;
+        return (int)std::max(least, 3 * to / 2 / n);
     };
     KeyPlan p;
     if (d->io == M3_BF16) {

@@ -449,3 +449,21 @@ def test_table_sizes():
         assert APP(dims=APP.make(batch=batch, seqlen=0, table_width=width)) == m3scan.M3_E_DIMS, (batch, width)
         assert "page_table" in m3scan.last_error()
         assert STEP(dims=cache_dims(batch=batch, table_width=width)) == m3scan.M3_E_DIMS
+
+
+@pytest.mark.parametrize("io", [m3attn.M3_BF16, m3attn.M3_F32])
+@pytest.mark.parametrize("group", [2, 3, 5, 7, 10, 13, 64, 71, 1000, 1009])
+@pytest.mark.parametrize("kv_heads,seqlen", [(1, 128), (1, 1024), (1, 16384), (1, 65536), (4, 16384), (8, 2048), (3, 40000)])
+def test_parts_of_a_group_are_bounded(io, group, kv_heads, seqlen):
+    """dk and dv in parts: at most about twice as many blocks as the GPU takes (1024; few ones 128), whatever the group
+    divides into, and enough of them."""
+    d = attn_dims(batch=1, seqlen=seqlen, heads=kv_heads * group, kv_heads=kv_heads, head_dim=128, io=io)
+    need = m3attn.load().m3_attention_backward_workspace_bytes(ctypes.byref(d), 0)
+    parts = need - seqlen * kv_heads * group * 4
+    one = 2 * seqlen * kv_heads * 128 * 4
+    assert parts % one == 0 and parts != one
+    splits, blocks = max(1, parts // one), (seqlen + 127) // 128 * kv_heads
+    assert splits <= group
+    assert splits == 1 or blocks * splits <= 2 * 1024
+    if io == m3attn.M3_BF16 and blocks > 256:
+        assert splits == group or blocks * splits >= 1024

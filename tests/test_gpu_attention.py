@@ -438,3 +438,20 @@ def test_tokens_far_apart():
     assert_close(o, ref["o"], ref["tol"]["o"], "o")
     for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
         assert_close(g[key], ref[name], ref["tol"][name], name)
+
+
+@pytest.mark.parametrize("io,hq,hk,d,lens", [("f32", 200, 40, 64, [116, 100]), ("f32", 71, 1, 32, [700]),
+                                             ("bf16", 700, 100, 32, [300]), ("bf16", 350, 50, 72, [290, 0, 40, 350])])
+def test_groups_split_into_uneven_parts(io, hq, hk, d, lens):
+    """Groups of 5, 71 and 7 heads in fewer parts than heads, which no number of parts divides."""
+    q, k, v, dout = draw(sum(lens), hq, hk, d, IO[io], hq)
+    check_packed(q, k, v, dout, lens)
+    if len(lens) > 1:
+        return
+    ref = attn_ref.prompt(q, k, v, lens, None, dout)
+    x = [t.to(DEV).unsqueeze(0) for t in (q, k, v, dout)]
+    o, lse = m3attn.m3_attention(*x[:3], save_lse=True)
+    g = m3attn.m3_attention_backward(*x[:3], o, lse, x[3])
+    torch.cuda.synchronize()
+    for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        assert_close(g[key][0], ref[name], ref["tol"][name], name)
