@@ -218,8 +218,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd_few(cons
     const float c = a.scale * kLog2e, slack = kSlack / c;
     R rows(c);
     load_rows<typename R::X>(rows.q, head_rows(a.q, w, w.head, row_bytes), q0, w.len, lane);
+    in_order();
     load_k(ks, 0, kend, wave);
+    in_order();
     load_v(vs, 0, kend, wave);
+    in_order();
     for (int64_t t = 0; t < kend; t += 128) {
         const int64_t k0 = t + 32 * wave;
         const bool mine = k0 < kend, more = t + 128 < kend;

@@ -139,8 +139,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_few(const
     const int64_t q0 = w.r0, kend = w.len < q0 + kAttnFew ? w.len : q0 + kAttnFew;
     R rows(a, w, q0, wave == 0, lane);
     const float c = a.scale * kLog2e;
+    in_order();
     load_v(vs, 0, kend, wave);
+    in_order();
     load_k(ks, 0, kend, wave);
+    in_order();
     for (int64_t t = 0; t < kend; t += 128) {
         const int64_t k0 = t + 32 * wave;
         const bool mine = k0 < kend, more = t + 128 < kend;
@@ -363,8 +366,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && DC <= 64 ? 2 : 1) void attn_
     load_rows<X>(k, head_rows(a.k, w, w.head, row_bytes), k0, w.len, lane);
     load_rows<X>(v, head_rows(a.v, w, w.head, row_bytes), k0, w.len, lane);
     floatx16 dk[X::DB] = {}, dv[X::DB] = {};
+    in_order();
     load_d(ds, k0, w.len, wave);
+    in_order();
     load_q(qs, k0, w.len, wave);
+    in_order();
     int64_t t = k0;
     for (int h = 0; h < group;) {
         const int64_t r0 = t + 32 * wave;

@@ -245,7 +245,10 @@ __device__ __forceinline__ void tiles_ready() {
     __syncthreads();
 }
 
-// The same for all but the last N loads of each wave.
+// Loads asked for after it are issued after those before it, so that tiles_ready_but can tell them apart.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// tiles_ready for all but the last N loads of each wave.
 template <int N>
 __device__ __forceinline__ void tiles_ready_but() {
     static_assert(N < 64, "vmcnt has 6 bits");

@@ -98,3 +98,88 @@ def test_masked_copies_on_written_cases():
     assert _masked_copies(region + [("v_accvgpr_write_b32", ["a160", "v145"]), restore], at)
     assert not _masked_copies(region + [restore, copy], at)
     assert not _masked_copies(region + [("v_mov_b32_e32", ["v3", "0"]), restore], at)
+
+
+def _fills(ins):
+    """Loads into LDS in the order they are issued, as places in LDS ((unknown part, offset) of m0), and "|" for a
+    barrier.  Scalar registers are followed in program order through what makes such places: a wave's part, shifted and
+    added to, moves and spills."""
+    val, spilled, out = {}, {}, []
+
+    def read(t, at):
+        if re.fullmatch(r"-?(0x[0-9a-f]+|\d+)", t):
+            return (None, int(t, 0))
+        return val.setdefault(t, (at, 0))
+
+    for at, (op, oo) in enumerate(ins):
+        if op == "s_barrier":
+            out.append("|")
+        elif op.startswith("buffer_load") and any("lds" in x.split() for x in oo):
+            out.append(read("m0", at))
+        elif op == "v_writelane_b32":
+            spilled[oo[0], oo[2]] = read(oo[1], at)
+        elif op == "v_readlane_b32":
+            val[oo[0]] = spilled.get((oo[1], oo[2]), (at, 0))
+        elif op.startswith(("s_", "v_readfirstlane")) and oo:
+            made = None
+            if op in ("s_mov_b32", "s_movk_i32"):
+                made = read(oo[1], at)
+            elif op in ("s_add_i32", "s_add_u32", "s_or_b32", "s_addk_i32"):
+                a, b = [read(t, at) for t in (oo[1:3] if op != "s_addk_i32" else (oo[0], oo[1]))]
+                if a[0] is None or b[0] is None:
+                    made = (a[0] if b[0] is None else b[0], a[1] + b[1])
+            pair = re.fullmatch(r"s\[(\d+):(\d+)\]", oo[0])
+            for t in (["s%d" % i for i in range(int(pair.group(1)), int(pair.group(2)) + 1)] if pair else [oo[0]]):
+                val[t] = made if made is not None and not pair else (at, 0)
+    return out
+
+
+def _tiles(fills, size):
+    """Their tiles: 0 for the first one filled, 1 for the other; None: neither a tile nor whole rounds of one."""
+    if not fills or any(f[0] != fills[0][0] for f in fills):
+        return None
+    low = min(f[1] for f in fills)
+    tiles = [(f[1] - low) >= size for f in fills]
+    if any(not 0 <= f[1] - low - t * (max(g[1] for g in fills) + 4096 - size - low) < size for f, t in zip(fills, tiles)):
+        return None
+    return [int(t != tiles[0]) for t in tiles]
+
+
+def _run_order(fills, n):
+    """The first n fills, then those of the loop behind them from its first barrier on: what stands before that is the
+    loop's end, laid out at its top."""
+    rest = fills[n:]
+    first = rest.index("|") if "|" in rest else 0
+    return fills[:n] + rest[first:] + rest[:first]
+
+
+def test_tiles_are_filled_in_the_order_they_are_waited_for():
+    """Few rows: the first barrier lets the second tile's loads be on their way, so those have to be the last ones issued,
+    before the loop and in it, where the tile that is done with first is filled first again."""
+    with tempfile.TemporaryDirectory() as d:
+        kernels = [k for s in SOURCES[:2] for k in _split_kernels(_assembly(s, d)) if "_few" in k[0]]
+    assert len(kernels) == 24
+    for name, ins, _ in kernels:
+        dim, size = (int(re.search(r"ELi(\d+)E|fLi(\d+)E", name).group(g) or 0) for g in (1, 2)), 2 if "bf16" in name else 4
+        size *= 128 * (64 if sum(dim) <= 64 else 128)
+        n = size // 16 // 256
+        fills = _run_order(_fills(ins), 2 * n)
+        tiles = _tiles([f for f in fills if f != "|"], size)
+        assert tiles == [0] * n + [1] * n + [0] * n + [1] * n, (name, fills)
+        assert fills[2 * n:2 * n + 2] == ["|", "|"] and fills[fills.index("|") + 1:].count("|") >= 2, (name, fills)
+        loop = fills[2 * n:]
+        assert "|" in loop[loop.index(next(f for f in loop if f != "|")) + n:][:1], (name, fills)   # between its tiles
+
+
+def test_fill_order_on_written_cases():
+    load, size = ("buffer_load_dwordx4", ["v1", "s[0:3]", "0 offen lds"]), 4096
+    ins = [("s_lshl_b32", ["s5", "s4", "10"]), ("s_mov_b32", ["m0", "s5"]), load, ("s_add_i32", ["s6", "s5", "0x1000"]),
+           ("v_writelane_b32", ["v9", "s6", "3"]), ("s_mov_b32", ["m0", "s6"]), load, ("s_barrier", []),
+           ("s_mov_b32", ["s6", "s7"]), ("v_readlane_b32", ["s8", "v9", "3"]), ("s_mov_b32", ["m0", "s8"]), load,
+           ("s_mov_b32", ["m0", "s5"]), load]
+    fills = _fills(ins)
+    assert [f[1] for f in fills if f != "|"] == [0, 4096, 4096, 0] and fills[2] == "|"
+    assert _tiles([f for f in fills if f != "|"], size) == [0, 1, 1, 0]
+    assert _run_order([1, 2, 5, "|", "|", 4, "|"], 2) == [1, 2, "|", "|", 4, "|", 5]
+    assert _run_order([1, 2, "|", "|", 4, "|", 5], 2) == [1, 2, "|", "|", 4, "|", 5]
+    assert _tiles(_fills([("s_mov_b32", ["m0", "s5"]), load, ("s_mov_b32", ["m0", "s6"]), load]), size) is None
