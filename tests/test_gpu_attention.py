@@ -455,3 +455,44 @@ def test_groups_split_into_uneven_parts(io, hq, hk, d, lens):
     torch.cuda.synchronize()
     for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
         assert_close(g[key][0], ref[name], ref["tol"][name], name)
+
+
+# Dense fp32 batches of many heads take two workgroups to a compute unit where heads have up to 96 elements, packed ones one.
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [8, 32, 40, 72, 96, 104, 128])
+@pytest.mark.parametrize("n", [128, 290])
+def test_many_heads_dense_widths(io, d, n):
+    b, hq, hk = 2, 132, 132
+    q, k, v, dout = draw(b * n, hq, hk, d, IO[io], n + d)
+    ref = attn_ref.prompt(q, k, v, [n] * b, None, dout)
+    qd, kd, vd, dd = (x.to(DEV).unflatten(0, (b, n)) for x in (q, k, v, dout))
+    o, lse = m3attn.m3_attention(qd, kd, vd, save_lse=True)
+    g = m3attn.m3_attention_backward(qd, kd, vd, o, lse, dd)
+    torch.cuda.synchronize()
+    assert_close(o.flatten(0, 1), ref["o"], ref["tol"]["o"], "o")
+    assert_close(lse.transpose(0, 1).flatten(1), ref["lse"], ref["tol"]["lse"], "lse")
+    for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        assert_close(g[key].flatten(0, 1), ref[name], ref["tol"][name], name)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("d", [32, 72, 96, 128])
+def test_later_tokens_do_not_reach_a_row_of_dense_batches(io, bad, d):
+    n, h = 300, 130
+    q, k, v, _ = draw(n, h, 1, d, IO[io], 44)
+    x = [t.to(DEV).unsqueeze(0) for t in (q, k, v)]
+    want = m3attn.m3_attention(*x)[0]
+    for at in (0, 40, 127, 200, 299):
+        x[2] = v.clone().unsqueeze(0)
+        x[2][0, at, 0, 3] = bad
+        x[2] = x[2].to(DEV)
+        o = m3attn.m3_attention(*x)[0]
+        torch.cuda.synchronize()
+        tol = 2.0 ** -6 if io == "bf16" else 2.0 ** -18   # the block is added up in another order, unrounded
+        assert torch.allclose(o[:at].float(), want[:at].float(), atol=tol, rtol=tol), at
+        touched = o[at:, :, 3].float()
+        assert (torch.isnan(touched) if bad != bad else touched == bad).all(), at
+        rest = torch.cat([o[at:, :, :3], o[at:, :, 4:]], 2)
+        assert torch.isfinite(rest.float()).all()
