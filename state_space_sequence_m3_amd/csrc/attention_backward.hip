@@ -35,7 +35,7 @@ struct DqRows {
     floatx16 dq[X::DB] = {};
     float lse, delta;
 
-    // reads the rows, and computes delta; `write`: keeps it for the second launch
+    // reads the rows, and computes delta from o; `write`: keeps it for the second launch
     __device__ __forceinline__ DqRows(const AttnArgs& a, const RowBlock& w, int64_t q0, bool write, int lane) {
         const int row = lane & 31, row_bytes = a.dim * X::ES;
         load_rows<X>(q, head_rows(a.o, w, w.head, row_bytes), q0, w.len, lane);
@@ -51,6 +51,20 @@ struct DqRows {
             lse = a.lse[at] * kLog2e;
             if (write && lane < 32) a.delta[at] = delta;
         }
+    }
+    // delta without o's rounding: this half's sum of p dp over 32 keys, and what all sums make
+    __device__ __forceinline__ float delta_part(const floatx16& s, const floatx16& dp, float c, bool diagonal, int lane) const {
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float x = fast_exp2(fmaf(s[i], c, -lse)) * dp[i];
+            d += diagonal && acc_row(i, lane >> 5) > (lane & 31) ? 0.f : x;
+        }
+        return d;
+    }
+    __device__ __forceinline__ void set_delta(const AttnArgs& a, const RowBlock& w, int64_t q0, float d, bool write, int lane) {
+        delta = d;
+        if (write && lane < 32 && q0 + lane < w.len) a.delta[token_row(a, w, w.head) + q0 + lane] = d;
     }
     // scores and the products of dout with the values become ds
     __device__ __forceinline__ void turn(floatx16& s, const floatx16& dp, float c, bool diagonal, int lane) {
@@ -68,6 +82,15 @@ struct DqRows {
         X::columns_by(K, r0, s, dq, lane);
     }
 };
+
+// A row that sees few keys has most of dp - delta cancel: delta from the rounded o would leave half a step of o whole, 2^-9 of
+// dout and o where ds itself may be nothing (dq and dk of sequences of one token: 0.01 for 0).  Bf16 rows that see at most
+// 128 keys, whose scores are at hand together, take delta as sum_j p_ij dp_ij in fp32 instead.  o of later rows is smaller,
+// as a mean of more values: with even weights its rounding counts for less than a tenth of theirs.  (dq and dk of 8
+// sequences of 16 tokens are 0.0023 off, as those of long ones are.  Backward of 32 x 128 tokens, 32/8 heads of 128: 118 ->
+// 125 us, 64 x 40, 16 heads of 64 26.6 -> 28.8, 8 x 2048 unchanged.)
+template <typename T>
+__device__ __forceinline__ bool takes_sum(int64_t keys) { return sizeof(T) == 2 && keys <= kAttnRows; }
 
 // dq: as the forward pass, scores transposed, 128 query rows to a workgroup and 32 to a wave.  3 products to the forward
 // pass's 2 with the same softmax to hide: at b8 L2048, 32/8 heads of 128 bf16, 416 us, matrix units busy 54% of the time, LDS
@@ -92,8 +115,29 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq(const Att
     load_v(v0, 0, w.len, wave);
     const int64_t q0 = w.r0 + 32 * wave;
     const bool active = q0 < w.len;
-    DqRows<T, DC> rows(a, w, q0, true, lane);
+    const bool sums = takes_sum<T>(kend);
+    DqRows<T, DC> rows(a, w, q0, !sums, lane);
     const float c = a.scale * kLog2e;
+    if constexpr (sizeof(T) == 2) {
+        if (sums) {
+            static_assert(kAttnRows == 2 * X::ROWS, "all keys of the first block are in the two buffers");
+            if (ntiles > 1) {
+                load_k(k1, X::ROWS, w.len, wave);
+                load_v(v1, X::ROWS, w.len, wave);
+            }
+            tiles_ready();
+            if (active) {
+                float d = 0.f;
+#pragma unroll 1
+                for (int r0 = 0; r0 <= q0; r0 += 32) {
+                    const floatx16 s = X::rows_by(r0 < X::ROWS ? k0 : k1, r0 % X::ROWS, rows.q, lane);
+                    const floatx16 dp = X::rows_by(r0 < X::ROWS ? v0 : v1, r0 % X::ROWS, rows.dout, lane);
+                    d += rows.delta_part(s, dp, c, r0 == q0, lane);
+                }
+                rows.set_delta(a, w, q0, halves_sum(d), true, lane);
+            }
+        }
+    }
 
     auto turn = [&](int t, const char* K, const char* V, char* next_k, char* next_v) __attribute__((always_inline)) {
         tiles_ready();
@@ -130,6 +174,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_few(const
     using R = DqRows<T, DC>;
     __shared__ alignas(16) char ks[X::BYTES];
     __shared__ alignas(16) char vs[X::BYTES];
+    __shared__ float deltas[sizeof(T) == 2 ? 4 : 1][32];   // of the waves' keys
     RowBlock w;
     if (!locate_rows<kAttnFew, true>(a, a.heads, blockIdx.x, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -137,14 +182,36 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_few(const
     const TileLoad<X> load_k(head_rows(a.k, w, kv_head, row_bytes), tid);
     const TileLoad<X> load_v(head_rows(a.v, w, kv_head, row_bytes), tid);
     const int64_t q0 = w.r0, kend = w.len < q0 + kAttnFew ? w.len : q0 + kAttnFew;
-    R rows(a, w, q0, wave == 0, lane);
+    const bool sums = takes_sum<T>(kend);
+    R rows(a, w, q0, wave == 0 && !sums, lane);
     const float c = a.scale * kLog2e;
     in_order();
     load_v(vs, 0, kend, wave);
     in_order();
     load_k(ks, 0, kend, wave);
     in_order();
-    for (int64_t t = 0; t < kend; t += 128) {
+    if constexpr (sizeof(T) == 2) {
+        if (sums) {
+            const bool mine = 32 * wave < kend, diagonal = 32 * wave == q0;
+            floatx16 s, dp;
+            float d = 0.f;
+            tiles_ready();
+            if (mine) {
+                s = X::rows_by(ks, 32 * wave, rows.q, lane);
+                dp = X::rows_by(vs, 32 * wave, rows.dout, lane);
+                d = halves_sum(rows.delta_part(s, dp, c, diagonal, lane));
+            }
+            if (lane < 32) deltas[wave][lane] = d;
+            tiles_ready();
+            const int row = lane & 31;
+            rows.set_delta(a, w, q0, deltas[0][row] + deltas[1][row] + deltas[2][row] + deltas[3][row], wave == 0, lane);
+            if (mine) {
+                rows.turn(s, dp, c, diagonal, lane);
+                X::columns_by(ks, 32 * wave, s, rows.dq, lane);
+            }
+        }
+    }
+    for (int64_t t = sums ? kend : 0; t < kend; t += 128) {
         const int64_t k0 = t + 32 * wave;
         const bool mine = k0 < kend, more = t + 128 < kend;
         floatx16 s, dp;
