@@ -51,9 +51,9 @@ __global__ __launch_bounds__(256) void cache_append(const AppendArgs a) {
         at = t - s * a.L;
         n = a.L;
     }
-    const int32_t pos = (int32_t)((a.lens ? (int64_t)a.lens[s] : n) - n + at);
+    const int64_t pos = (a.lens ? (int64_t)a.lens[s] : n) - n + at;   // below 2^31, but not always above -2^31
     int place = 0, page = -1;
-    if (a.pages.k) page = page_of(a.pages, a.pages.table + s * a.pages.table_w, pos, place);
+    if (a.pages.k && pos >= 0) page = page_of(a.pages, a.pages.table + s * a.pages.table_w, (int32_t)pos, place);
 
     // places of a row: pairs of units (halves) or units that are rotated, then units that are copied
     const int turned = a.rot / (HALVES ? 2 * U : U), places = turned + (a.dim - a.rot) / U;

@@ -408,3 +408,26 @@ def test_large_cache():
             assert torch.equal(kd[table[s, i // page], :, i % page].cpu(), k[s, i])
     ref = attn_ref.step(q, [x.transpose(0, 1) for x in k], [x.transpose(0, 1) for x in v])
     assert_close(o, ref["o"], ref["tol"]["o"], "o")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("halves", [False, True])
+def test_positions_below_32_bits(io, halves):
+    """Lengths at int32's ends: positions lens - n + i beyond it are what they are, and are not cached."""
+    g = torch.Generator().manual_seed(23)
+    lens = torch.tensor([-(1 << 31), -(1 << 31) + 2, -5, 0, (1 << 31) - 1], dtype=torch.int32)
+    b, n, d = len(lens), 4, 64
+    q, k = (torch.randn(b, n, h, d, generator=g).to(IO[io]) for h in (3, 1))
+    freq = frequencies(d) * 2.0 ** -9
+    kc = torch.full((2, 1, 16, d), 7.0, dtype=IO[io], device=DEV)
+    table = torch.zeros(b, 3, dtype=torch.int32, device=DEV)
+    k_out = torch.empty_like(k.to(DEV))
+    out = m3attn.m3_cache_append(k.to(DEV), k.to(DEV), kc, kc.clone(), table, lens.to(DEV), q=q.to(DEV), inv_freq=freq.to(DEV),
+                                 halves=halves, k_out=k_out)
+    torch.cuda.synchronize()
+    pos = (lens.long().unsqueeze(1) - n + torch.arange(n)).flatten()
+    assert int(pos.min()) < -(1 << 31)
+    for got, x in ((out, q), (k_out, k)):
+        want, tol = attn_ref.rotate(x.flatten(0, 1), pos, freq, halves)
+        assert_close(got.flatten(0, 1), want, tol, "rotated")
+    assert (kc == 7.0).all()
