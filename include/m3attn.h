@@ -53,7 +53,7 @@ typedef struct {
     m3_head_strides dout, dq, dk, dv; /* backward                                             */
     int32_t io;         /* m3_dtype of q, k, v, o and their gradients                         */
     uint32_t flags;     /* 0                                                                  */
-    float scale;        /* positive; 0: 1 / sqrt(D)                                           */
+    float scale;        /* positive, at most 2.3e38; 0: 1 / sqrt(D)                           */
 } m3_attn_dims;
 
 /*
@@ -126,7 +126,7 @@ typedef struct {
     m3_head_strides o;  /* step (token is not used)                                           */
     int32_t io;         /* m3_dtype of the caches and of q, k, v, q_out, k_out, o             */
     uint32_t flags;     /* append: M3_ROTATE_HALVES or 0; step: 0                             */
-    float scale;        /* step: positive; 0: 1 / sqrt(D)                                     */
+    float scale;        /* step: positive, at most 2.3e38; 0: 1 / sqrt(D)                     */
 } m3_cache_dims;
 
 /* m3_cache_dims.flags: pairs are elements (k, k + rotary_dim / 2), else (2k, 2k + 1), as the core's are */

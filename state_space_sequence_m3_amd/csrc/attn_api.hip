@@ -148,7 +148,8 @@ m3_status check_counts(int64_t batch, int64_t seqlen) {
     return M3_OK;
 }
 m3_status check_scale(float scale, int64_t dim, float* use) {
-    if (!(scale >= 0.f) || isinf(scale)) return fail(M3_E_DIMS, "scale must be positive, or 0 for 1 / sqrt(D)");
+    if (!(scale >= 0.f) || scale > 2.3e38f)   // its product with log2 e is an fp32 number
+        return fail(M3_E_DIMS, "scale must be positive and at most 2.3e38, or 0 for 1 / sqrt(D)");
     *use = scale > 0.f ? scale : (float)(1.0 / sqrt((double)dim));
     return M3_OK;
 }

@@ -114,8 +114,8 @@ def _like(t, dense):
 def _scale(scale):
     if scale is None:
         return 0.0
-    if not scale > 0:
-        raise ValueError("scale must be positive, got %s" % (scale,))
+    if not scale > 2.0 ** -150:   # what fp32 rounds to 0, the default's mark
+        raise ValueError("scale must be positive in float32, got %s" % (scale,))
     return scale
 
 

@@ -467,3 +467,27 @@ def test_parts_of_a_group_are_bounded(io, group, kv_heads, seqlen):
     assert splits == 1 or blocks * splits <= 2 * 1024
     if io == m3attn.M3_BF16 and blocks > 256:
         assert splits == group or blocks * splits >= 1024
+
+
+def test_scales_out_of_range():
+    """Scales that fp32 does not hold: the binding's float would become 0, which stands for the default, and the library's
+    product with log2 e infinite."""
+    q, k = torch.zeros(2, 5, 4, 64), torch.zeros(2, 5, 2, 64)
+    cache, table, lens = torch.zeros(9, 2, 16, 64), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for bad in (1e-50, 2.0 ** -150, -1e-50, float("nan")):
+        with pytest.raises(ValueError, match="scale"):
+            m3attn.m3_attention(q, k, k, scale=bad)
+        with pytest.raises(ValueError, match="scale"):
+            m3attn.m3_attention_backward(q, k, k, q, torch.zeros(2, 4, 5), q, scale=bad)
+        with pytest.raises(ValueError, match="scale"):
+            m3attn.m3_attention_step(q[:, 0], cache, cache, table, lens, scale=bad)
+    for call in (FWD, BWD, STEP):
+        for bad in (2.4e38, 3.4e38):
+            assert call(dims=call.make(scale=bad)) == m3scan.M3_E_DIMS and "scale" in m3scan.last_error()
+
+
+@pytest_nodev
+def test_scales_at_the_ends_of_the_range():
+    for call in (FWD, BWD, STEP):
+        for scale in (2.0 ** -149, 1e-38, 2.3e38):
+            assert call(dims=call.make(scale=scale)) == NODEVICE

@@ -135,3 +135,31 @@ def test_token_scores_of_minus_infinity(io):
         p = torch.softmax(k @ q[2, h].double() / 8, 0)
         e = (d + 24) * U32 * 8 + half_step(io)    # of scores below 8
         assert_close(o[2, h], p @ v, e * (p @ v.abs() + (p @ v).abs()), "o")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** -149, 1e-41, 1e-38, 1e-30, 2.3e38])
+@pytest.mark.parametrize("h", [2, 130])
+def test_scales_at_the_ends_of_the_range(io, scale, h):
+    """All scores all but equal: means of the values."""
+    io, n, d, page = IO[io], 290, 64, 16
+    g = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn(1, n, h, d, generator=g).to(io) for _ in range(3))
+    if scale > 1:
+        q.zero_()
+    o, lse = m3attn.m3_attention(q.to(DEV), k.to(DEV), v.to(DEV), scale=scale, save_lse=True)
+    pages = -(-n // page)
+    kc, vc = (torch.zeros(pages, h, page, d, dtype=io, device=DEV) for _ in range(2))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).unsqueeze(0)
+    m3attn.m3_cache_append(k.to(DEV), v.to(DEV), kc, vc, table)
+    o1 = m3attn.m3_attention_step(q[:, -1].contiguous().to(DEV), kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV),
+                                  scale=scale)
+    torch.cuda.synchronize()
+    count = torch.arange(1, n + 1).double().view(n, 1, 1)
+    want, size = v[0].double().cumsum(0) / count, v[0].double().abs().cumsum(0) / count
+    # scores of up to 2^-90 are nothing beside 1; a probability and the sum are off by 16 units and one per addition
+    tol = (2 * (16 + n) * U32 + (half_step(io) if io is torch.bfloat16 else 0.0)) * size
+    assert_close(o[0], want, tol, "o")
+    assert_close(o1[0], want[-1], tol[-1], "token")
+    want = count.view(n).log().expand(h, n)
+    assert_close(lse[0], want, (32 + n + 8 * want) * U32, "lse")
