@@ -81,8 +81,8 @@ m3_status m3_attention(const m3_attn_dims* dims, const int32_t* cu_seqlens, cons
  *   delta_i = dout_i . o_i,  ds_ij = p_ij (dout_i . v_j - delta_i)
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
  *
- * With bf16 io, delta of a row that sees at most 128 keys is sum_j p_ij (dout_i . v_j), which is the same but for o's
- * rounding.  dk and dv are summed over the query heads of their group.  With bf16 io, p and ds are rounded to bf16 for
+ * With bf16 io, delta of a row that sees at most 128 keys is sum_j p_ij (dout_i . v_j) / sum_j p_ij, which is the same
+ * but for o's rounding.  dk and dv are summed over the query heads of their group.  With bf16 io, p and ds are rounded to bf16 for
  * their products; sums are fp32.  p is off by |lse| 2^-23 of itself, as much as lse is: it has no digits where scores
  * reach 2^24, and from 2^30 on gradients may not be finite.  An infinity or NaN in a row of an input makes gradients of up to 31 other rows
  * of its block of 32 tokens NaN beside those that the formulas make so.

@@ -52,19 +52,22 @@ struct DqRows {
             if (write && lane < 32) a.delta[at] = delta;
         }
     }
-    // delta without o's rounding: this half's sum of p dp over 32 keys, and what all sums make
-    __device__ __forceinline__ float delta_part(const floatx16& s, const floatx16& dp, float c, bool diagonal, int lane) const {
-        float d = 0.f;
+    // delta without o's rounding: this half's sums of p dp and of p over 32 keys, and what all sums make.  (p is off by as
+    // much as lse is, the same for a whole row, which drops out of the quotient.)
+    __device__ __forceinline__ void delta_parts(const floatx16& s, const floatx16& dp, float c, bool diagonal, int lane,
+                                                float& top, float& bottom) const {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float x = fast_exp2(fmaf(s[i], c, -lse)) * dp[i];
-            d += diagonal && acc_row(i, lane >> 5) > (lane & 31) ? 0.f : x;
+            const float p = fast_exp2(fmaf(s[i], c, -lse));
+            const bool seen = !diagonal || acc_row(i, lane >> 5) <= (lane & 31);
+            top += seen ? p * dp[i] : 0.f;
+            bottom += seen ? p : 0.f;
         }
-        return d;
     }
-    __device__ __forceinline__ void set_delta(const AttnArgs& a, const RowBlock& w, int64_t q0, float d, bool write, int lane) {
-        delta = d;
-        if (write && lane < 32 && q0 + lane < w.len) a.delta[token_row(a, w, w.head) + q0 + lane] = d;
+    __device__ __forceinline__ void set_delta(const AttnArgs& a, const RowBlock& w, int64_t q0, float top, float bottom,
+                                              bool write, int lane) {
+        delta = bottom != 0.f ? top / bottom : 0.f;   // (rows that are not there)
+        if (write && lane < 32 && q0 + lane < w.len) a.delta[token_row(a, w, w.head) + q0 + lane] = delta;
     }
     // scores and the products of dout with the values become ds
     __device__ __forceinline__ void turn(floatx16& s, const floatx16& dp, float c, bool diagonal, int lane) {
@@ -85,10 +88,10 @@ struct DqRows {
 
 // A row that sees few keys has most of dp - delta cancel: delta from the rounded o would leave half a step of o whole, 2^-9 of
 // dout and o where ds itself may be nothing (dq and dk of sequences of one token: 0.01 for 0).  Bf16 rows that see at most
-// 128 keys, whose scores are at hand together, take delta as sum_j p_ij dp_ij in fp32 instead.  o of later rows is smaller,
-// as a mean of more values: with even weights its rounding counts for less than a tenth of theirs.  (dq and dk of 8
-// sequences of 16 tokens are 0.0023 off, as those of long ones are.  Backward of 32 x 128 tokens, 32/8 heads of 128: 118 ->
-// 125 us, 64 x 40, 16 heads of 64 26.6 -> 28.8, 8 x 2048 unchanged.)
+// 128 keys, whose scores are at hand together, take delta as sum_j p_ij dp_ij / sum_j p_ij in fp32 instead.  o of later
+// rows is smaller, as a mean of more values: with even weights its rounding counts for less than a tenth of theirs.  (dq and
+// dk of 8 sequences of 16 tokens are 0.0023 off, as those of long ones are.  Backward of 32 x 128 tokens, 32/8 heads of
+// 128: 118 -> 126 us, 64 x 40, 16 heads of 64 26.5 -> 29.1, 8 x 2048 unchanged.)
 template <typename T>
 __device__ __forceinline__ bool takes_sum(int64_t keys) { return sizeof(T) == 2 && keys <= kAttnRows; }
 
@@ -127,14 +130,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq(const Att
             }
             tiles_ready();
             if (active) {
-                float d = 0.f;
+                float top = 0.f, bottom = 0.f;
 #pragma unroll 1
                 for (int r0 = 0; r0 <= q0; r0 += 32) {
                     const floatx16 s = X::rows_by(r0 < X::ROWS ? k0 : k1, r0 % X::ROWS, rows.q, lane);
                     const floatx16 dp = X::rows_by(r0 < X::ROWS ? v0 : v1, r0 % X::ROWS, rows.dout, lane);
-                    d += rows.delta_part(s, dp, c, r0 == q0, lane);
+                    rows.delta_parts(s, dp, c, r0 == q0, lane, top, bottom);
                 }
-                rows.set_delta(a, w, q0, halves_sum(d), true, lane);
+                rows.set_delta(a, w, q0, halves_sum(top), halves_sum(bottom), true, lane);
             }
         }
     }
@@ -174,7 +177,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_few(const
     using R = DqRows<T, DC>;
     __shared__ alignas(16) char ks[X::BYTES];
     __shared__ alignas(16) char vs[X::BYTES];
-    __shared__ float deltas[sizeof(T) == 2 ? 4 : 1][32];   // of the waves' keys
+    __shared__ float parts[sizeof(T) == 2 ? 4 : 1][2][32];   // of delta, over the waves' keys
     RowBlock w;
     if (!locate_rows<kAttnFew, true>(a, a.heads, blockIdx.x, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -194,17 +197,21 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_few(const
         if (sums) {
             const bool mine = 32 * wave < kend, diagonal = 32 * wave == q0;
             floatx16 s, dp;
-            float d = 0.f;
+            float top = 0.f, bottom = 0.f;
             tiles_ready();
             if (mine) {
                 s = X::rows_by(ks, 32 * wave, rows.q, lane);
                 dp = X::rows_by(vs, 32 * wave, rows.dout, lane);
-                d = halves_sum(rows.delta_part(s, dp, c, diagonal, lane));
+                rows.delta_parts(s, dp, c, diagonal, lane, top, bottom);
+                top = halves_sum(top), bottom = halves_sum(bottom);
             }
-            if (lane < 32) deltas[wave][lane] = d;
+            parts[wave][lane >> 5][lane & 31] = lane < 32 ? top : bottom;
             tiles_ready();
             const int row = lane & 31;
-            rows.set_delta(a, w, q0, deltas[0][row] + deltas[1][row] + deltas[2][row] + deltas[3][row], wave == 0, lane);
+            top = bottom = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) top += parts[n][0][row], bottom += parts[n][1][row];
+            rows.set_delta(a, w, q0, top, bottom, wave == 0, lane);
             if (mine) {
                 rows.turn(s, dp, c, diagonal, lane);
                 X::columns_by(ks, 32 * wave, s, rows.dq, lane);

@@ -84,3 +84,27 @@ def test_dense(hq, hk, n):
     want, tol = gradients(q, k, v, dout, [n] * b)
     for x in "qkv":
         assert_close(g[x].flatten(0, 1), want["d" + x], tol["d" + x], "d" + x)
+
+
+@pytest.mark.parametrize("hq,hk", [(2, 1), (300, 100)])
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 14, 2.0 ** 18])
+def test_one_token_of_large_scores(hq, hk, size):
+    """One key alone: ds is 0 whatever the score.  p is off by |lse| 2^-23 of 1, below 2 here, delta by its quotient's and dp's
+    rounding."""
+    lens, d = [1] * 5, 64
+    q, k, v, dout = draw(sum(lens), hq, hk, d, 3)
+    big = size ** 0.5
+    q, k = (q.float() * big).bfloat16(), (k.float() * big).bfloat16()
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(DEV)
+    qd, kd, vd, dd = (x.to(DEV) for x in (q, k, v, dout))
+    o, lse = m3attn.m3_attention(qd, kd, vd, cu, save_lse=True)
+    g = m3attn.m3_attention_backward(qd, kd, vd, o, lse, dd, cu)
+    torch.cuda.synchronize()
+    assert float(lse.abs().max()) > size / 8
+    group, scale = hq // hk, d ** -0.5
+    kg, vg = (x.double().repeat_interleave(group, 1) for x in (k, v))
+    # dp in either kernel has an order of its own: d additions each, and 4 units of delta
+    ds = 2 * (2 * d + 4) * U32 * (dout.double().abs() * vg.abs()).sum(-1, keepdim=True)
+    assert (g["q"].cpu().double().abs() <= scale * ds * kg.abs() * (1 + half_step(torch.bfloat16)) ** 2).all()
+    dk = (scale * ds * q.double().abs()).unflatten(1, (hk, group)).sum(2)
+    assert (g["k"].cpu().double().abs() <= dk * (1 + half_step(torch.bfloat16)) ** 2).all()
