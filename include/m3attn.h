@@ -63,9 +63,8 @@ typedef struct {
  *
  * For: the forward pass of training, prefill.  Scores, maxima, sums and o are fp32; with bf16 io the
  * probabilities are rounded to bf16 for their product with v (relative to the largest score of their row so
- * far, within 2^8).  q . k and scale log2(e) q . k may be any fp32 numbers; beyond them they are infinite.  A row whose
- * scores are all -infinity is NaN (0 / 0).  What later tokens hold, infinities and NaN included, does not reach a
- * row.
+ * far, within 2^8).  q . k may be any fp32 number; beyond them it is infinite.  A row whose scores are all
+ * -infinity is NaN (0 / 0).  What later tokens hold, infinities and NaN included, does not reach a row.
  *
  *   q        [b, L, Hq, D] or [T, Hq, D] io;  k, v with Hkv heads            required
  *   o        like q                                                         required
@@ -81,11 +80,11 @@ m3_status m3_attention(const m3_attn_dims* dims, const int32_t* cu_seqlens, cons
  *   delta_i = dout_i . o_i,  ds_ij = p_ij (dout_i . v_j - delta_i)
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
  *
- * With bf16 io, delta of a row that sees at most 128 keys is sum_j p_ij (dout_i . v_j) / sum_j p_ij, which is the same
- * but for o's rounding.  dk and dv are summed over the query heads of their group.  With bf16 io, p and ds are rounded to bf16 for
- * their products; sums are fp32.  p is off by |lse| 2^-23 of itself, as much as lse is: it has no digits where scores
- * reach 2^24, and from 2^30 on gradients may not be finite.  An infinity or NaN in a row of an input makes gradients of up to 31 other rows
- * of its block of 32 tokens NaN beside those that the formulas make so.
+ * dk and dv are summed over the query heads of their group.  With bf16 io, p and ds are rounded to bf16 for
+ * their products, and delta of a row that sees at most 128 keys is sum_j p_ij (dout_i . v_j) / sum_j p_ij, the same
+ * but for o's rounding; sums are fp32.  p is off by |lse| 2^-23 of itself, as much as lse is: it has no digits
+ * where scores reach 2^24, and from 2^30 on gradients may not be finite.  An infinity or NaN in a row of an input
+ * makes gradients of up to 31 other rows of its block of 32 tokens NaN beside those that the formulas make so.
  *
  *   o, lse     what m3_attention wrote for the same dims, offsets and inputs      required
  *   dout       like o                                                            required
@@ -164,11 +163,10 @@ m3_status m3_cache_append(const m3_cache_dims* dims, const int32_t* cu_seqlens, 
  *
  *   lse = log sum_j exp(s_j),  o = sum_j exp(s_j - lse) v_j;  no position: o = 0, lse = -infinity
  *
- * (positions whose scores are all -infinity: o is NaN, as a prompt's row, and lse = -infinity).
- *
  * For: decoding.  Reads every page once; long sequences are cut into pieces that run at the same time.
  * Scores, sums and partial results are fp32, their range as m3_attention's; with bf16 io the probabilities are
- * rounded to bf16 for their product with v.  lens[s] past table_width * page_size counts as that.
+ * rounded to bf16 for their product with v.  Positions whose scores are all -infinity make o NaN, as a prompt's
+ * row, and lse -infinity.  lens[s] past table_width * page_size counts as that.
  *
  *   q          [b, Hq, D] io, strides dims->q (batch, head)              required
  *   o          like q, strides dims->o; may be q itself (same strides)   required

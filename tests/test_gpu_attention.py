@@ -496,3 +496,17 @@ def test_later_tokens_do_not_reach_a_row_of_dense_batches(io, bad, d):
         assert (torch.isnan(touched) if bad != bad else touched == bad).all(), at
         rest = torch.cat([o[at:, :, :3], o[at:, :, 4:]], 2)
         assert torch.isfinite(rest.float()).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gradients_of_broadcast_keys(io):
+    """One key head given as four by a stride of 0: a gradient for each of the four."""
+    lens = [90, 0, 33]
+    q, k, v, dout = draw(sum(lens), 4, 1, 64, IO[io], 45)
+    ref = attn_ref.prompt(q, k.repeat(1, 4, 1), v.repeat(1, 4, 1), lens, None, dout)
+    kd, vd, cu = k.to(DEV).expand(-1, 4, -1), v.to(DEV).expand(-1, 4, -1), offsets(lens)
+    o, lse = m3attn.m3_attention(q.to(DEV), kd, vd, cu, save_lse=True)
+    g = m3attn.m3_attention_backward(q.to(DEV), kd, vd, o, lse, dout.to(DEV), cu)
+    torch.cuda.synchronize()
+    for name, key in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        assert_close(g[key], ref[name], ref["tol"][name], name)

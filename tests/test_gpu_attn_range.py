@@ -163,3 +163,34 @@ def test_scales_at_the_ends_of_the_range(io, scale, h):
     assert_close(o1[0], want[-1], tol[-1], "token")
     want = count.view(n).log().expand(h, n)
     assert_close(lse[0], want, (32 + n + 8 * want) * U32, "lse")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("h", [2, 130])
+def test_scores_at_the_ends_of_the_range(io, sign, h):
+    """Scores whose products with log2 e are beyond fp32."""
+    io, n, d, page = IO[io], 200, 64, 16
+    g = torch.Generator().manual_seed(5)
+    q, k = torch.zeros(n, h, d), torch.zeros(n, h, d)
+    q[:, :, 9], k[:, :, 9] = 2.0 ** 60, torch.where(torch.rand(n, h, generator=g) < 0.5, 1.75, 1.5) * sign * 2.0 ** 67
+    if sign < 0:
+        k[:70] = k[:70].clamp(max=0).where(k[:70] != -1.5 * 2.0 ** 67, torch.tensor(-1.75 * 2.0 ** 67))
+    v = torch.randn(n, h, d, generator=g)
+    q, k, v = q.to(io), k.to(io), v.to(io)
+    o, lse = m3attn.m3_attention(*(x.to(DEV).unsqueeze(0) for x in (q, k, v)), scale=1.0, save_lse=True)
+    pages = -(-n // page)
+    kc, vc = (torch.zeros(pages, h, page, d, dtype=io, device=DEV) for _ in range(2))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).unsqueeze(0)
+    m3attn.m3_cache_append(k.to(DEV).unsqueeze(0), v.to(DEV).unsqueeze(0), kc, vc, table)
+    lse1 = torch.empty(1, h, device=DEV)
+    o1 = m3attn.m3_attention_step(q[-1:].to(DEV), kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV), scale=1.0,
+                                  lse=lse1)
+    torch.cuda.synchronize()
+    seen = torch.ones(n, n, dtype=torch.bool).tril()
+    for i in (0, h - 1):
+        want, tol, wl, tl = attend(q[:, i], k[:, i], v[:, i], 1.0, seen, io)
+        assert_close(o[0, :, i], want, tol, "o")
+        assert_close(lse[0, i], wl, tl, "lse")
+        assert_close(o1[0, i], want[-1], tol[-1], "token")
+        assert_close(lse1[0, i], wl[-1], tl[-1], "token's lse")
