@@ -123,8 +123,8 @@ struct Rows {
 };
 
 // Bound by how far two waves to a SIMD cover each other's softmax, LDS reads and barriers: at b8 L2048, 32/8 heads of 128
-// bf16, 331 us (820 TFLOP/s of the causal half), the matrix units are busy 45% of the time, LDS 23%, and waves
-// wait 32% of theirs.  8192 tokens, 32/4 heads of 64: 327 us.
+// bf16, 327 us (840 TFLOP/s of the causal half), the matrix units are busy 45% of the time, vector units 51%, LDS 23%, and
+// waves wait 32% of theirs.  8192 tokens, 32/4 heads of 64: 309 us, vector units 84%, matrix units 51%.
 template <typename T, int DC, int PER_CU>
 __global__ __launch_bounds__(256, PER_CU) void attn_fwd(const AttnArgs a) {
     using X = HeadTile<T, DC>;
@@ -166,7 +166,8 @@ __global__ __launch_bounds__(256, PER_CU) void attn_fwd(const AttnArgs a) {
         if (t + 2 < ntiles) load_k(old_k, (int64_t)(t + 2) * X::ROWS, w.len, wave);
         load_v(old_v, (int64_t)(t + 1) * X::ROWS, w.len, wave);
         rows.raise(s, c, slack);
-        // a wave with products to issue goes first: 343 -> 323 us at b8 L2048, 32/8 heads of 128 bf16
+        // a wave with products to issue goes first: 340 -> 334 us at b8 L2048, 32/8 heads of 128 bf16, 73 -> 69 for 2 x 2048,
+        // 32/16 heads of 96; 16 x 512, 32/8 heads of 128 loses, 74 -> 78
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int n = 0; n < X::SUB; ++n) ahead[n] = X::rows_by(K, 32 * n, rows.q, lane);
@@ -200,8 +201,8 @@ __global__ __launch_bounds__(256, PER_CU) void attn_fwd(const AttnArgs a) {
 
 // For few rows: a workgroup takes 32 query rows, and its waves the four parts of 32 keys of each tile of 128, with a
 // softmax of their own each, which are joined at the end.  Keys are loaded while probabilities meet values, values
-// while queries meet keys.  64 tokens, 32/8 heads of 128 bf16: 8.0 us, latency; 13 packed prompts of up to 701, 6/2 heads
-// of 80 fp32: 83 us.
+// while queries meet keys.  64 tokens, 32/8 heads of 128 bf16: 8.4 us, latency; 13 packed prompts of up to 701, 6/2 heads
+// of 80 fp32: 83 us, matrix units 33% busy.
 template <typename T, int DC>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_fwd_few(const AttnArgs a) {
     using X = HeadTile<T, DC, 128>;

@@ -96,8 +96,8 @@ template <typename T>
 __device__ __forceinline__ bool takes_sum(int64_t keys) { return sizeof(T) == 2 && keys <= kAttnRows; }
 
 // dq: as the forward pass, scores transposed, 128 query rows to a workgroup and 32 to a wave.  3 products to the forward
-// pass's 2 with the same softmax to hide: at b8 L2048, 32/8 heads of 128 bf16, 416 us, matrix units busy 54% of the time, LDS
-// 27%; 9 packed sequences of up to 1100, 12/4 heads of 96 fp32, 196 us.
+// pass's 2 with the same softmax to hide: at b8 L2048, 32/8 heads of 128 bf16, 408 us, matrix units busy 55% of the time, LDS
+// 27%; 9 packed sequences of up to 1100, 12/4 heads of 96 fp32, 197 us.
 template <typename T, int DC>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq(const AttnArgs a) {
     using X = HeadTile<T, DC>;
@@ -318,8 +318,9 @@ struct Grads {
 };
 
 // dk, dv: 32 keys to a wave, whose two sums stay in registers over all rows and heads of the group; query and dout rows
-// go by in LDS.  Bound by waiting: b8 L2048, 32/8 heads of 128 bf16, 8 waves, 667 us, matrix units busy 38% of the
-// time, waves waiting 56% of theirs, without LDS conflicts.
+// go by in LDS.  Bound by waiting: b8 L2048, 32/8 heads of 128 bf16, 8 waves, 670 us, matrix units busy 39% of the
+// time, waves waiting 57% of theirs, without LDS conflicts; of 411 vector instructions to a tile of 64 rows 250 are
+// addresses.
 template <typename T, int DC, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void attn_dkv(const AttnArgs a) {
     using G = Grads<T, DC>;
@@ -417,7 +418,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void attn_dkv(c
 }
 
 // For few keys: 32 of them to a workgroup, and the four parts of 32 rows of each tile of 128 to its waves, whose sums
-// are joined at the end.  9 packed sequences of up to 1100, 12/4 heads of 96 fp32: 303 us.
+// are joined at the end.  9 packed sequences of up to 1100, 12/4 heads of 96 fp32: 305 us.
 template <typename T, int DC>
 __global__ __launch_bounds__(256, sizeof(T) == 2 && DC <= 64 ? 2 : 1) void attn_dkv_few(const AttnArgs a) {
     using X = HeadTile<T, DC, 128>;

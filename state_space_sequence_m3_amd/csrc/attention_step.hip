@@ -10,8 +10,8 @@
 // product with the values, whose left operand is the values' rows as they are loaded, 16 lanes to a row, with (bf16) an
 // 8 x 8 transpose inside each lane.  Nothing goes through LDS but the join of the waves.
 //
-// 32/8 heads of 128 bf16: 64 sequences of up to 8192 178 us and 6.5 for the join (5.5 TB/s over the call); one of 32768
-// 24.2 and 4.4 us.
+// 32/8 heads of 128 bf16: 64 sequences of up to 8192 182 us and 6.6 for the join (5.4 TB/s over the call, 5.5 with pages of
+// 16); one of 32768 26 and 4.7 us.  16 sequences of up to 8192, fp32: 106 us, 4.7 TB/s.
 #include "m3_mma.h"
 #include "m3_pages.h"
 #include "m3_softmax.h"

@@ -167,9 +167,11 @@ int64_t row_blocks(const m3_attn_dims* d, bool packed, int64_t R) {
 }
 // Workgroups of 128 rows need to be many: where they are at most so many, blocks of 32 rows are taken, whose waves
 // share the other axis.  Forward, at 256 of them: 4096 x 8 heads of 128 bf16 86 -> 73 us, 4 x 1024 29.5 -> 29.6, fp32
-// 155 -> 129; at 512: 2 x 2048 x 16 heads bf16 57 -> 80, fp32 321 -> 429.  dk and dv in bf16 at 512 blocks of keys lose (2
-// x 2048 x 16 heads, with dq: 202 -> 287 us), in fp32 they gain (4 x 2048, 32/8 heads 5051 -> 4704, 4096, 32/16 heads
-// 4897 -> 4468) and lose at 1024 (1394 -> 1498).
+// 155 -> 129; at 320: 2560 x 16 bf16 54.6 -> 61.3, fp32 355 -> 335; at 384: 4 x 1024 x 12 bf16 30.1 -> 43.5, 3 x 1024 x 16
+// fp32 155 -> 196; at 512: 2 x 2048 x 16 heads bf16 57 -> 80, fp32 321 -> 429.  dk and dv (with dq) in bf16: at 320 blocks of
+// keys 2560 x 16 235 -> 230, at 384 4 x 1024 x 12 113 -> 149, at 512 2 x 2048 x 16 202 -> 287; in fp32 they gain at 512 (4 x
+// 2048, 32/8 heads 5051 -> 4704, 4096, 32/16 heads 4897 -> 4468) and lose at 640 (4 x 1024 x 20 945 -> 976) and 1024 (1394
+// -> 1498).
 // (A packed batch's block numbers are taken to be half a sequence's too many each.)
 constexpr int64_t kFewBlocks = 256, kFewKeyBlocks = 256, kFewKeyBlocks32 = 512;
 // dk and dv: the heads of a group are summed by one workgroup, or split over as many as make this number of blocks,

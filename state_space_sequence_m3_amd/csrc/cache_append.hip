@@ -3,7 +3,7 @@
 // Memory-bound: every row is read once and written once.  A workgroup takes a token; a thread keeps one place of
 // a row (16 bytes, or the two places that a rotation of halves pairs), computes that place's angles once, in fp64
 // (a far position times its frequency has more digits than fp32 holds), and goes through the heads with
-// them.  8 x 2048 tokens, 32/8 heads of 128 bf16: 77 us, 5.2 TB/s, as a copy; 64 single tokens: 4.3 us, latency.
+// them.  8 x 2048 tokens, 32/8 heads of 128 bf16: 77 us, 5.2 TB/s, as a copy; 64 single tokens: 4.5 us, latency.
 #include "m3_mma.h"
 #include "m3_pages.h"
 
